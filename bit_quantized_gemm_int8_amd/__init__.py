@@ -28,6 +28,15 @@ Entry points (same names as the C ABI):
   gemm_w4a8_g128_sparse24(xq, x_scale, wsp, w_scale, w_zero, out_dtype)
   quantize_kv_i8_segments(kv)                   -> (kv_q int8 [T,H,D], kv_scale f32 [H,ceil(T/128),D])
   dequantize_kv_i8_segments(kv_q, kv_scale, out_dtype) -> [T,H,D]
+  quantize_f8_g128(x)                           -> (xq float8_e4m3fn [M,K], x_scale f32 [M,G])
+  quantize_weight_f8_b128(w)                    -> (wq float8_e4m3fn [N,K], w_scale f32 [B,G]); w [E,K,N]: [E,...]
+  gemm_f8_b128(xq, x_scale, wq, w_scale, out_dtype)
+  route_experts(logits, k, bias, score, groups, top_groups, renormalize, scale) -> (expert int32 [T,k], weight f32 [T,k])
+  plan_experts(expert, E)                       -> (offsets int32 [E+1], row_token int32 [T*k], slot int32 [T,k])
+  gemm_f8_b128_experts(xq, x_scale, wq, w_scale, offsets, row_token, out_dtype) -> y [R,N]
+  combine_experts(rows, slot, weight, out_dtype) -> y [T,N]
+with G = ceil(K/128) and B = ceil(N/128); these seven run on the device of
+their first tensor, whichever device is current.
 """
 from __future__ import annotations
 
@@ -50,6 +59,8 @@ __all__ = [
     "quantize_kv_i8_segments", "dequantize_kv_i8_segments", "KV_SEGMENT",
     "quantize_weight_u4_g128_outliers", "gemm_w4a8_g128_outliers",
     "quantize_weight_u4_g128_sparse24", "gemm_w4a8_g128_sparse24",
+    "quantize_f8_g128", "quantize_weight_f8_b128", "gemm_f8_b128", "gemm_f8_b128_experts",
+    "route_experts", "plan_experts", "combine_experts",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqgemm.so")
@@ -86,6 +97,15 @@ _SIGNATURES = {
     "quantize_weight_u4_g128_sparse24": [_vp, _i64, _i64, _vp, _vp, _vp, _vp],
     "gemm_w4a8_g128_sparse24": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp],
     "dequantize_kv_i8_segments": [_vp, _vp, _i64, _i64, _i64, _vp, _int, _vp],
+    "quantize_f8_g128": [_vp, _int, _i64, _i64, _vp, _vp, _vp],
+    "quantize_weight_f8_b128": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp],
+    "gemm_f8_b128": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp],
+    "gemm_f8_b128_experts": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _int,
+                             _vp],
+    "route_experts": [_vp, _int, _vp, _i64, _i64, _i64, _i64, _i64, _int, _int, ctypes.c_float, _vp,
+                      _vp, _vp],
+    "plan_experts": [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp],
+    "combine_experts": [_vp, _int, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _int, _vp],
 }
 
 # measurement probes (include/qgemm_peaks.h)
@@ -553,6 +573,169 @@ def dequantize_kv_i8_segments(kv_q: torch.Tensor, kv_scale: torch.Tensor,
     y = _out(out, (T, H, D), out_dtype, kv_q.device)
     _call("dequantize_kv_i8_segments", pq, ps, T, H, D, y.data_ptr(), _DTYPE_CODE[out_dtype],
           _stream())
+    return y
+
+
+# ------------------------------------------- e4m3 codes with block scales
+
+F8_BLOCK = 128   # inputs (and output channels) per scale of the e4m3 paths
+_F8 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def _call_on(device: torch.device, name: str, *args) -> None:
+    """_call on `device`'s current stream, with `device` current."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args, stream)
+
+
+def quantize_f8_g128(x: torch.Tensor, out=None):
+    """x [M, K] (f32/f16/bf16) -> (xq float8_e4m3fn [M, K], x_scale f32
+    [M, ceil(K/128)]): one scale per token and 128 inputs."""
+    px = _dev(x, "x", _FLOATS)
+    M, K = _2d(x, "x")
+    xq, xs = out if out is not None else (None, None)
+    xq = _out(xq, (M, K), _F8, x.device, "xq out")
+    xs = _out(xs, (M, _blocks(K)), torch.float32, x.device, "x_scale out")
+    _call_on(x.device, "quantize_f8_g128", px, _DTYPE_CODE[x.dtype], M, K, xq.data_ptr(),
+             xs.data_ptr())
+    return xq, xs
+
+
+def quantize_weight_f8_b128(w: torch.Tensor, out=None):
+    """w [K, N] (f32/f16/bf16) -> (wq float8_e4m3fn [N, K], w_scale f32
+    [ceil(N/128), ceil(K/128)]): one scale per 128 x 128 block.  A stack of
+    matrices [E, K, N] gives stacks [E, ...]."""
+    pw = _dev(w, "w", _FLOATS)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [K, N] or [E, K, N]")
+    K, N = w.shape[-2:]
+    lead = tuple(w.shape[:-2])
+    wq, ws = out if out is not None else (None, None)
+    wq = _out(wq, lead + (N, K), _F8, w.device, "wq out")
+    ws = _out(ws, lead + (_blocks(N), _blocks(K)), torch.float32, w.device, "w_scale out")
+    _call_on(w.device, "quantize_weight_f8_b128", pw, _DTYPE_CODE[w.dtype], lead[0] if lead else 1,
+             K, N, wq.data_ptr(), ws.data_ptr())
+    return wq, ws
+
+
+def _float_code(dtype, name="out_dtype"):
+    if dtype not in _FLOATS:
+        raise TypeError(f"{name} must be one of {_FLOATS}, got {dtype}")
+    return _DTYPE_CODE[dtype]
+
+
+def gemm_f8_b128(xq, x_scale, wq, w_scale, out_dtype=torch.bfloat16, out=None):
+    """y [M, N] = X W from e4m3 codes xq [M, K] (x_scale [M, ceil(K/128)]) and
+    wq [N, K] (w_scale [ceil(N/128), ceil(K/128)])."""
+    pxq = _dev(xq, "xq", (_F8,))
+    M, K = _2d(xq, "xq")
+    dev, G = xq.device, _blocks(K)
+    N = _2d(wq, "wq")[0]
+    pwq = _dev(wq, "wq", (_F8,), (N, K), dev)
+    pxs = _dev(x_scale, "x_scale", (torch.float32,), (M, G), dev)
+    pws = _dev(w_scale, "w_scale", (torch.float32,), (_blocks(N), G), dev)
+    code = _float_code(out_dtype)
+    y = _out(out, (M, N), out_dtype, dev)
+    _call_on(dev, "gemm_f8_b128", pxq, pxs, pwq, pws, M, N, K, y.data_ptr(), code)
+    return y
+
+
+def gemm_f8_b128_experts(xq, x_scale, wq, w_scale, offsets, row_token=None,
+                         out_dtype=torch.bfloat16, out=None):
+    """y [R, N]: rows offsets[e] .. offsets[e+1]-1 are products with expert e's
+    weights wq[e] ([E, N, K], w_scale [E, ceil(N/128), ceil(K/128)]); row r
+    takes the codes of token row_token[r], or of row r if row_token is None
+    (then R is the number of rows of xq).  Rows from offsets[E] on are left as
+    they were in `out` (without `out`: undefined)."""
+    pxq = _dev(xq, "xq", (_F8,))
+    T, K = _2d(xq, "xq")
+    dev, G = xq.device, _blocks(K)
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 3:
+        raise ValueError("wq must be [E, N, K]")
+    E, N = wq.shape[:2]
+    pwq = _dev(wq, "wq", (_F8,), (E, N, K), dev)
+    pxs = _dev(x_scale, "x_scale", (torch.float32,), (T, G), dev)
+    pws = _dev(w_scale, "w_scale", (torch.float32,), (E, _blocks(N), G), dev)
+    po = _dev(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    pt, R = None, T
+    if row_token is not None:
+        pt = _dev(row_token, "row_token", (torch.int32,), None, dev)
+        if row_token.dim() != 1:
+            raise ValueError("row_token must be a 1-D tensor")
+        R = row_token.shape[0]
+    code = _float_code(out_dtype)
+    y = _out(out, (R, N), out_dtype, dev)
+    _call_on(dev, "gemm_f8_b128_experts", pxq, pxs, pwq, pws, po, pt, T, R, E, N, K, y.data_ptr(),
+             code)
+    return y
+
+
+# ------------------------------------------------------- expert routing
+
+QG_SCORE_SOFTMAX, QG_SCORE_SIGMOID = 0, 1
+_SCORE = {"softmax": QG_SCORE_SOFTMAX, "sigmoid": QG_SCORE_SIGMOID}
+
+
+def route_experts(logits, k, bias=None, score="softmax", groups=1, top_groups=1, renormalize=True,
+                  scale=1.0, out=None):
+    """logits [T, E] (f32/f16/bf16) -> (expert int32 [T, k], weight f32
+    [T, k]): the k experts of largest score + bias (bias f32 [E] or None)
+    within the top_groups of `groups` groups, and their scores, without the
+    bias, renormalised and scaled.  A logit of -inf closes an expert; expert
+    -1 with weight 0 where none is open."""
+    pl = _dev(logits, "logits", _FLOATS)
+    T, E = _2d(logits, "logits")
+    dev = logits.device
+    pb = _opt(bias, "bias", (torch.float32,), (E,), dev)
+    if score not in _SCORE:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    expert, weight = out if out is not None else (None, None)
+    expert = _out(expert, (T, k), torch.int32, dev, "expert out")
+    weight = _out(weight, (T, k), torch.float32, dev, "weight out")
+    _call_on(dev, "route_experts", pl, _DTYPE_CODE[logits.dtype], pb, T, E, groups, top_groups, k,
+             _SCORE[score], int(bool(renormalize)), scale, expert.data_ptr(), weight.data_ptr())
+    return expert, weight
+
+
+def plan_experts(expert, E, out=None):
+    """expert int32 [T, k] -> (offsets int32 [E+1], row_token int32 [T*k],
+    slot int32 [T, k]): the (token, choice) pairs sorted by expert, in order;
+    entries outside 0 .. E-1 get slot -1 and no row."""
+    pe = _dev(expert, "expert", (torch.int32,))
+    T, k = _2d(expert, "expert")
+    dev = expert.device
+    offsets, row_token, slot = out if out is not None else (None, None, None)
+    offsets = _out(offsets, (E + 1,), torch.int32, dev, "offsets out")
+    row_token = _out(row_token, (T * k,), torch.int32, dev, "row_token out")
+    slot = _out(slot, (T, k), torch.int32, dev, "slot out")
+    _call_on(dev, "plan_experts", pe, T, k, E, offsets.data_ptr(), row_token.data_ptr(),
+             slot.data_ptr())
+    return offsets, row_token, slot
+
+
+def combine_experts(rows, slot, weight, out_dtype=None, out=None):
+    """y [T, N] = sum_j weight[t, j] rows[slot[t, j]] (binary32 sums), rows
+    [R, N] (f32/f16/bf16), slot int32 [T, k] (outside 0 .. R-1: no row),
+    weight f32 [T, k]; out_dtype None: that of rows."""
+    pr = _dev(rows, "rows", _FLOATS)
+    R, N = _2d(rows, "rows")
+    dev = rows.device
+    T, k = _2d(slot, "slot")
+    ps = _dev(slot, "slot", (torch.int32,), None, dev)
+    pw = _dev(weight, "weight", (torch.float32,), (T, k), dev)
+    out_dtype = rows.dtype if out_dtype is None else out_dtype
+    code = _float_code(out_dtype)
+    y = _out(out, (T, N), out_dtype, dev)
+    _call_on(dev, "combine_experts", pr, _DTYPE_CODE[rows.dtype], ps, pw, T, k, R, N, y.data_ptr(),
+             code)
     return y
 
 

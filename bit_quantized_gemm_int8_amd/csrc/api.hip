@@ -40,6 +40,28 @@ qg_status_t check_kv_dims(int64_t T, int64_t H, int64_t D) {
   return QG_OK;
 }
 
+// Sizes of the e4m3 paths: K a multiple of 16 up to 2^20 (a tile of 256 rows
+// then spans less than the 2^31 bytes that 32-bit buffer offsets reach), row
+// and column counts up to 2^30.
+constexpr int64_t kMaxF8K = (int64_t)1 << 20, kMaxF8Dim = (int64_t)1 << 30;
+constexpr int64_t kMaxExperts = 1024, kMaxChoices = 64, kMaxExpertGroups = 64;
+
+qg_status_t check_f8_dims(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K <= 0 || M > kMaxF8Dim || N > kMaxF8Dim || K > kMaxF8K || K % 16)
+    return QG_ERR_SHAPE;
+  return QG_OK;
+}
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned_to(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == QG_F32 ? 3u : 1u)) == 0;
+}
+
+// A launch holds fewer than 2^32 threads.
+inline bool fits_grid(int64_t workgroups, int64_t threads) {
+  return workgroups <= ((int64_t)1 << 32) / threads - 1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -397,6 +419,110 @@ qg_status_t dequantize_kv_i8_segments(const int8_t* kv_q, const float* kv_scale,
   if (!aligned16(kv_q) || !aligned16(kv_scale) || !aligned16(out)) return QG_ERR_ALIGN;
   return hip_status(qg::launch_kv_dequant_seg(kv_q, kv_scale, T, H, D, out, out_dtype,
                                               static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t quantize_f8_g128(const void* x, int x_dtype, int64_t M, int64_t K, uint8_t* xq,
+                             float* x_scale, void* stream) {
+  if (qg_status_t s = check_f8_dims(M, 1, K)) return s;
+  if (!fits_grid(M * ((K + 127) / 128), 8)) return QG_ERR_SHAPE;
+  if (!is_float_dtype(x_dtype)) return QG_ERR_DTYPE;
+  if (M == 0) return QG_OK;
+  if (!x || !xq || !x_scale) return QG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(xq) || !aligned4(x_scale)) return QG_ERR_ALIGN;
+  return hip_status(qg::launch_quant_f8_rows(x, x_dtype, M, K, xq, x_scale,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t quantize_weight_f8_b128(const void* w, int w_dtype, int64_t E, int64_t K, int64_t N,
+                                    uint8_t* wq, float* w_scale, void* stream) {
+  if (qg_status_t s = check_f8_dims(E, N, K)) return s;
+  if (E > kMaxExperts || !fits_grid(E * ((N + 127) / 128) * ((K + 127) / 128), 256)) return QG_ERR_SHAPE;
+  if (!is_float_dtype(w_dtype)) return QG_ERR_DTYPE;
+  if (E == 0 || N == 0) return QG_OK;
+  if (!w || !wq || !w_scale) return QG_ERR_NULL;
+  if (!aligned16(w) || !aligned16(wq) || !aligned4(w_scale)) return QG_ERR_ALIGN;
+  return hip_status(qg::launch_quant_f8_weight(w, w_dtype, E, K, N, wq, w_scale,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
+                         const float* w_scale, int64_t M, int64_t N, int64_t K, void* y,
+                         int y_dtype, void* stream) {
+  if (qg_status_t s = check_f8_dims(M, N, K)) return s;
+  if (!fits_grid(((M + 63) / 64) * ((N + 63) / 64), 512)) return QG_ERR_SHAPE;
+  if (!is_float_dtype(y_dtype)) return QG_ERR_DTYPE;
+  if (M == 0 || N == 0) return QG_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !y) return QG_ERR_NULL;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned4(x_scale) || !aligned4(w_scale) || !aligned_to(y, y_dtype))
+    return QG_ERR_ALIGN;
+  return hip_status(qg::launch_gemm_f8(xq, x_scale, wq, w_scale, nullptr, nullptr, M, M, 1, N, K, y,
+                                       y_dtype, static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
+                                 const float* w_scale, const int32_t* offsets,
+                                 const int32_t* row_token, int64_t T, int64_t R, int64_t E,
+                                 int64_t N, int64_t K, void* y, int y_dtype, void* stream) {
+  if (qg_status_t s = check_f8_dims(R, N, K)) return s;
+  if (T < 0 || T > kMaxF8Dim || E < 1 || E > kMaxExperts) return QG_ERR_SHAPE;
+  if (row_token ? T * K > kMaxDim : T != R) return QG_ERR_SHAPE;
+  if (!fits_grid(E * ((N + 15) / 16), 512)) return QG_ERR_SHAPE;
+  if (!is_float_dtype(y_dtype)) return QG_ERR_DTYPE;
+  if (R == 0 || N == 0) return QG_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !offsets || !y) return QG_ERR_NULL;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned4(x_scale) || !aligned4(w_scale) ||
+      !aligned4(offsets) || !aligned4(row_token) || !aligned_to(y, y_dtype))
+    return QG_ERR_ALIGN;
+  return hip_status(qg::launch_gemm_f8(xq, x_scale, wq, w_scale, offsets, row_token, T, R, E, N, K, y,
+                                       y_dtype, static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t route_experts(const void* logits, int logits_dtype, const float* bias, int64_t T,
+                          int64_t E, int64_t groups, int64_t top_groups, int64_t k, int score,
+                          int renormalize, float scale, int32_t* expert, float* weight,
+                          void* stream) {
+  if (T < 0 || T > kMaxF8Dim || E < 1 || E > kMaxExperts) return QG_ERR_SHAPE;
+  if (groups < 1 || groups > kMaxExpertGroups || E % groups || top_groups < 1 || top_groups > groups)
+    return QG_ERR_SHAPE;
+  if (k < 1 || k > kMaxChoices || k > top_groups * (E / groups)) return QG_ERR_SHAPE;
+  if (!fits_grid((T + 3) / 4, 256)) return QG_ERR_SHAPE;
+  if (score != QG_SCORE_SOFTMAX && score != QG_SCORE_SIGMOID) return QG_ERR_ARG;
+  if (renormalize != 0 && renormalize != 1) return QG_ERR_ARG;
+  if (!is_float_dtype(logits_dtype)) return QG_ERR_DTYPE;
+  if (T == 0) return QG_OK;
+  if (!logits || !expert || !weight) return QG_ERR_NULL;
+  if (!aligned_to(logits, logits_dtype) || !aligned4(bias) || !aligned4(expert) || !aligned4(weight))
+    return QG_ERR_ALIGN;
+  return hip_status(qg::launch_route(logits, logits_dtype, bias, T, E, groups, top_groups, k,
+                                     score == QG_SCORE_SIGMOID, renormalize, scale, expert, weight,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t plan_experts(const int32_t* expert, int64_t T, int64_t k, int64_t E, int32_t* offsets,
+                         int32_t* row_token, int32_t* slot, void* stream) {
+  if (T < 0 || T > kMaxF8Dim || k < 1 || k > kMaxChoices || T * k > kMaxF8Dim) return QG_ERR_SHAPE;
+  if (E < 1 || E > kMaxExperts) return QG_ERR_SHAPE;
+  if (!offsets || (T > 0 && (!expert || !row_token || !slot))) return QG_ERR_NULL;
+  if (!aligned4(expert) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(slot))
+    return QG_ERR_ALIGN;
+  return hip_status(qg::launch_plan(expert, T, k, E, offsets, row_token, slot,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t combine_experts(const void* rows, int rows_dtype, const int32_t* slot,
+                            const float* weight, int64_t T, int64_t k, int64_t R, int64_t N,
+                            void* y, int y_dtype, void* stream) {
+  if (T < 0 || T > kMaxF8Dim || k < 1 || k > kMaxChoices || R < 0 || R > kMaxF8Dim || N < 0 ||
+      N > kMaxF8Dim)
+    return QG_ERR_SHAPE;
+  if (!fits_grid(T * ((N + 255) / 256), 256)) return QG_ERR_SHAPE;
+  if (!is_float_dtype(rows_dtype) || !is_float_dtype(y_dtype)) return QG_ERR_DTYPE;
+  if (T == 0 || N == 0) return QG_OK;
+  if ((R > 0 && !rows) || !slot || !weight || !y) return QG_ERR_NULL;
+  if (!aligned_to(rows, rows_dtype) || !aligned4(slot) || !aligned4(weight) || !aligned_to(y, y_dtype))
+    return QG_ERR_ALIGN;
+  return hip_status(qg::launch_combine(rows, rows_dtype, slot, weight, T, k, R, N, y, y_dtype,
+                                       static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -84,5 +84,24 @@ hipError_t launch_kv_quant_seg(const void* kv, int kv_dtype, int64_t T, int64_t 
                                int8_t* kv_q, float* kv_scale, hipStream_t st);
 hipError_t launch_kv_dequant_seg(const int8_t* kv_q, const float* kv_scale, int64_t T, int64_t H,
                                  int64_t D, void* out, int out_dtype, hipStream_t st);
+// e4m3 codes with a scale for each 128 inputs (rows) or each 128 x 128 block
+// (weights), and their product: plain (offsets null, R = M rows) or with one
+// weight matrix for each run of rows.
+hipError_t launch_quant_f8_rows(const void* x, int x_dtype, int64_t M, int64_t K, uint8_t* xq,
+                                float* xs, hipStream_t st);
+hipError_t launch_quant_f8_weight(const void* w, int w_dtype, int64_t E, int64_t K, int64_t N,
+                                  uint8_t* wq, float* ws, hipStream_t st);
+hipError_t launch_gemm_f8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                          const int32_t* offsets, const int32_t* row_token, int64_t T, int64_t R,
+                          int64_t E, int64_t N, int64_t K, void* y, int y_dtype, hipStream_t st);
+hipError_t launch_route(const void* logits, int dtype, const float* bias, int64_t tokens,
+                        int64_t E, int64_t groups, int64_t top_groups, int64_t k, int sigmoid,
+                        int renormalize, float scale, int32_t* expert, float* weight,
+                        hipStream_t st);
+hipError_t launch_plan(const int32_t* expert, int64_t T, int64_t k, int64_t E, int32_t* offsets,
+                       int32_t* row_token, int32_t* slot, hipStream_t st);
+hipError_t launch_combine(const void* rows, int dtype, const int32_t* slot, const float* weight,
+                          int64_t tokens, int64_t k, int64_t R, int64_t N, void* y, int y_dtype,
+                          hipStream_t st);
 
 }  // namespace qg

@@ -510,6 +510,139 @@ qg_status_t dequantize_kv_i8_segments(const int8_t* kv_q, const float* kv_scale,
                                       int64_t H, int64_t D, void* out, int out_dtype,
                                       void* stream);
 
+/*
+ * ---- 8-bit float (e4m3) codes with a scale for each block of 128 ----
+ *
+ * e4m3: 1 sign, 4 exponent (bias 7), 3 mantissa bits, subnormals, no
+ * infinities; the largest finite value is 448.  Codes are stored one a byte.
+ * The last block along K (and along N, for weights) is shorter where 128 does
+ * not divide the size.  G = ceil(K / 128), B = ceil(N / 128).
+ * In this part K is a positive multiple of 16 up to 2^20, and M, N, T and R go
+ * up to 2^30.  Code arrays, x and w are 16-byte aligned; scales, indices, y,
+ * logits and expert rows need the alignment of their element only.
+ */
+
+/*
+ * Per-token e4m3 quantization of activations, a scale for each 128 inputs.
+ *   For each row m and block g, over its inputs:
+ *     a = max |x|;  s = a / 448;  xq = e4m3(clamp(x / s, -448, 448));
+ *   a block with s == 0 gets zero codes.  Both quotients are binary32,
+ *   correctly rounded; e4m3() rounds to nearest, halves to even.
+ *   A block that holds an infinity gets s = inf and zero codes, one that holds
+ *   a NaN s = NaN and zero codes: every output it reaches is then NaN.
+ * x:        [M][K] of x_dtype (QG_F32, QG_F16 or QG_BF16), read only.
+ * xq:       [M][K] codes, written.
+ * x_scale:  [M][G] float scales, written.
+ */
+qg_status_t quantize_f8_g128(const void* x, int x_dtype, int64_t M, int64_t K, uint8_t* xq,
+                             float* x_scale, void* stream);
+
+/*
+ * e4m3 quantization of weight matrices, a scale for each 128 x 128 block
+ * (offline).  The rule of quantize_f8_g128 over each block of one matrix.
+ * w:        [E][K][N] of w_dtype (QG_F32, QG_F16 or QG_BF16), read only: E
+ *           matrices (1 for a plain layer, one for each expert), E <= 1024.
+ * wq:       [E][N][K] codes (K-contiguous per output channel), written.
+ * w_scale:  [E][B][G] float scales, written.
+ */
+qg_status_t quantize_weight_f8_b128(const void* w, int w_dtype, int64_t E, int64_t K, int64_t N,
+                                    uint8_t* wq, float* w_scale, void* stream);
+
+/*
+ * Product of e4m3 codes with block scales.
+ *   y[m,n] = sum_g x_scale[m,g] w_scale[n/128,g] sum_{k in g} xq[m,k] wq[n,k]
+ * xq [M][K], x_scale [M][G], wq [N][K], w_scale [B][G]: as the quantizers
+ * write them, read.
+ * y: [M][N] of y_dtype (QG_F32, QG_BF16 or QG_F16), written.
+ * The sums over blocks are binary32.  The products of a block are exact and
+ * summed in binary32 for QG_F32 outputs and for M <= 64; for QG_BF16 and
+ * QG_F16 outputs of more rows the 8-bit matrix cores take them 8 at a time
+ * and drop, of each product, what lies below 2^-13 of the largest of its 8:
+ * a part of at most 7 * 2^-13 of the sum of those largest products, and
+ * about 2^-14 of the result where the terms are spread as in a linear layer.
+ */
+qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
+                         const float* w_scale, int64_t M, int64_t N, int64_t K, void* y,
+                         int y_dtype, void* stream);
+
+/*
+ * The same product where each run of rows has its own weight matrix (the
+ * experts of a routed layer), in one launch:
+ *   for e < E and offsets[e] <= r < offsets[e+1], with t = row_token[r] (or
+ *   t = r where row_token is NULL):  y[r] = x_t . W_e as in gemm_f8_b128.
+ * xq [T][K], x_scale [T][G]; wq [E][N][K], w_scale [E][B][G]: read.
+ * offsets:   [E + 1] int32, rising, offsets[E] <= R: read on the GPU.  Values
+ *            outside 0 .. R are clamped to it, and a run that ends below its
+ *            start is empty; in a row that two runs name each element is
+ *            either's.
+ * row_token: [R] int32 or NULL (then T must equal R): read.  A row whose
+ *            token is outside 0 .. T-1 is written as zeros.  T * K < 2^31.
+ * y:         [R][N]; rows ahead of offsets[0] and from offsets[E] on are left
+ *            as they were.
+ * 1 <= E <= 1024.  The kernel is chosen by the mean number of rows, R / E:
+ * up to 64 the products are exact as for M <= 64 above.
+ */
+qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
+                                 const float* w_scale, const int32_t* offsets,
+                                 const int32_t* row_token, int64_t T, int64_t R, int64_t E,
+                                 int64_t N, int64_t K, void* y, int y_dtype, void* stream);
+
+/*
+ * Choice of k experts for each token.
+ *   p[t,e] = softmax over e of logits[t], or sigmoid(logits[t,e]);
+ *   c[t,e] = p[t,e] + bias[e]  (bias NULL: p itself).
+ *   groups > 1: the experts form `groups` runs of E / groups; a group's value
+ *   is the sum of its two largest c, and only the experts of the top_groups
+ *   groups of largest value stay.
+ *   expert[t] = the k experts of largest c, in falling order;
+ *   weight[t,j] = scale * p[t, expert[t,j]], divided by the sum of the k
+ *   chosen p first if renormalize is 1 (p unbiased; a sum of 0 gives 0).
+ * The comparisons take c in binary64 whatever the type of the logits; equal
+ * values go to the lowest expert (group).
+ * A logit of -inf or NaN closes the expert for that token (softmax leaves it
+ * out), and so does a bias of -inf or NaN for all tokens; +inf counts as the
+ * largest binary32 value.  Where fewer than k experts are open the remaining
+ * choices are expert -1 with weight 0.
+ * logits [T][E] of logits_dtype (QG_F32, QG_F16 or QG_BF16), bias [E] float
+ * or NULL: read.  expert [T][k] int32, weight [T][k] float: written.
+ * 1 <= E <= 1024; groups <= 64 divides E; 1 <= top_groups <= groups;
+ * 1 <= k <= 64 and k <= top_groups * E / groups.
+ */
+typedef enum qg_score {
+  QG_SCORE_SOFTMAX = 0,
+  QG_SCORE_SIGMOID = 1
+} qg_score_t;
+
+qg_status_t route_experts(const void* logits, int logits_dtype, const float* bias, int64_t T,
+                          int64_t E, int64_t groups, int64_t top_groups, int64_t k, int score,
+                          int renormalize, float scale, int32_t* expert, float* weight,
+                          void* stream);
+
+/*
+ * Row plan of a choice: the T * k (token, choice) pairs sorted by expert, in
+ * the order of tokens and choices within an expert.
+ *   offsets[e]   = first row of expert e; offsets[E] = number of rows;
+ *   row_token[r] = the token of row r, -1 from offsets[E] on;
+ *   slot[t,j]    = the row of choice j of token t, -1 where expert[t,j] is
+ *                  outside 0 .. E-1 (no expert, or one of another GPU).
+ * expert [T][k] int32: read.  offsets [E + 1], row_token [T * k], slot [T][k]
+ * int32: written.  T * k <= 2^30, k <= 64, 1 <= E <= 1024.  T == 0 writes
+ * offsets only.
+ */
+qg_status_t plan_experts(const int32_t* expert, int64_t T, int64_t k, int64_t E, int32_t* offsets,
+                         int32_t* row_token, int32_t* slot, void* stream);
+
+/*
+ * Weighted sum of each token's expert rows:
+ *   y[t] = sum_j weight[t,j] rows[slot[t,j]]   (binary32, in the order of j)
+ * without the choices whose slot is outside 0 .. R-1.
+ * rows [R][N] of rows_dtype, slot [T][k] int32, weight [T][k] float: read.
+ * y: [T][N] of y_dtype, written.  Types QG_F32, QG_F16, QG_BF16; k <= 64.
+ */
+qg_status_t combine_experts(const void* rows, int rows_dtype, const int32_t* slot,
+                            const float* weight, int64_t T, int64_t k, int64_t R, int64_t N,
+                            void* y, int y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,3 +48,4 @@ from .outlier import (quantize_weight_u4_g128_outliers, gemm_w4a8_g128_outliers,
                       gemm_w4a8_g128_outlier_acc, decode_records, select_outliers)
 from .sparse24 import (quantize_weight_u4_g128_sparse24, gemm_w4a8_g128_sparse24,
                        gemm_w4a8_g128_sparse24_acc, expand_sparse24, prune_2_4)
+from . import experts, f8
