@@ -41,7 +41,7 @@ namespace qg {
 struct F8Rows {
   const int32_t* offsets;
   const int32_t* token;   // row -> row of xq, or null: the row itself
-  int64_t T;              // rows of xq
+  int T;                  // rows of xq
   int R;                  // rows of y
 };
 
@@ -52,15 +52,15 @@ __device__ __forceinline__ void f8_expert_rows(const F8Rows& fr, int e, int& lo,
 
 // The row of xq that row r of y is made from; -1: none (r past the run, or a
 // token that does not exist: its row is computed as zeros).
-__device__ __forceinline__ int64_t f8_source(const F8Rows& fr, int r, int hi) {
+__device__ __forceinline__ int f8_source(const F8Rows& fr, int r, int hi) {
   if (r >= hi) return -1;
-  const int64_t t = fr.token ? (int64_t)fr.token[r] : (int64_t)r;
+  const int t = fr.token ? fr.token[r] : r;
   return t >= 0 && t < fr.T ? t : -1;
 }
 
 // ---------------------------------------------------------------------------
 // Stream kernel.  A workgroup of NB x KS waves owns NB blocks of 16 weight
-// rows and up to 16 MT token rows.  K is walked in phases of PU = KS UPW
+// rows and up to 16 token rows (at a time).  K is walked in phases of PU = KS UPW
 // units of 128: the token codes and scales of a phase are staged in LDS once
 // for all waves (two buffers, one barrier a phase, the next phase's loads in
 // flight), wave (blk, ks) takes units ks UPW .. of the phase, and the KS
@@ -70,11 +70,11 @@ __device__ __forceinline__ int64_t f8_source(const F8Rows& fr, int r, int hi) {
 // are 4 consecutive outputs of one token and the scale of a unit is one
 // value per lane.
 // ---------------------------------------------------------------------------
-template <int MT, int NB, int KS, int UPW, typename OutT, bool EXPERTS>
+template <int NB, int KS, int UPW, typename OutT, bool EXPERTS>
 __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, F8Rows fr, int N, int K, OutT* __restrict__ y, int vec) {
-  constexpr int kThreads = 64 * NB * KS, kRows = 16 * MT;
+  constexpr int kThreads = 64 * NB * KS, kRows = 16;
   constexpr int PU = KS * UPW, PB = kUnitBytes * PU, kRowChunks = PB / 16;
   constexpr int kPitch = PB + 16;                  // an odd number of chunks: no bank conflicts
   constexpr int CPT = (kRows * kRowChunks + kThreads - 1) / kThreads;
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
   __shared__ __attribute__((aligned(16))) int8_t xbuf[2][kRows * kPitch];
   __shared__ float xsbuf[2][PU * kRows];
   __shared__ __attribute__((aligned(16))) int8_t tiles[NB * KS][kTileBytes];
-  __shared__ __attribute__((aligned(16))) v4f red[KS > 1 ? KS - 1 : 1][NB][MT][64];
+  __shared__ __attribute__((aligned(16))) v4f red[KS > 1 ? KS - 1 : 1][NB][64];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -115,14 +115,14 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
     const float* sp[SPT];
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
-      const int64_t t = f8_source(fr, m0 + (tid + c * kThreads) / kRowChunks, hi);
-      xp[c] = t < 0 ? nullptr : xq + t * K;
+      const int t = f8_source(fr, m0 + (tid + c * kThreads) / kRowChunks, hi);
+      xp[c] = t < 0 ? nullptr : xq + (int64_t)t * K;
     }
 #pragma unroll
     for (int c = 0; c < SPT; ++c) {
       const int i = tid + c * kThreads;
-      const int64_t t = i < kRows * PU ? f8_source(fr, m0 + i / PU, hi) : -1;
-      sp[c] = t < 0 ? nullptr : xs + t * G;
+      const int t = i < kRows * PU ? f8_source(fr, m0 + i / PU, hi) : -1;
+      sp[c] = t < 0 ? nullptr : xs + (int64_t)t * G;
     }
     auto load = [&](Batch& bt, int p) {
 #pragma unroll
@@ -140,9 +140,7 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
       __builtin_amdgcn_sched_barrier(0);
     };
 
-    v4f acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
     auto process = [&](const Batch& bt, int p) {
       int8_t* buf = xbuf[p & 1];
       float* sbuf = xsbuf[p & 1];
@@ -171,20 +169,17 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
           wf[2 * s] = f8_to_f16x8(f[s][0], f[s][1]);
           wf[2 * s + 1] = f8_to_f16x8(f[s][2], f[s][3]);
         }
+        v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          v4f d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            // past K both operands are zero
-            const v4i a = ld16(buf + (16 * t + r) * kPitch + kUnitBytes * u + 64 * s + 16 * j);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[2 * s], f8_to_f16x8(a[0], a[1]), d, 0, 0, 0);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[2 * s + 1], f8_to_f16x8(a[2], a[3]), d, 0, 0, 0);
-          }
-          const float sc = sbuf[u * kRows + 16 * t + r] * sw;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(d[i], sc, acc[t][i]);
+        for (int s = 0; s < 2; ++s) {
+          // past K both operands are zero
+          const v4i a = ld16(buf + r * kPitch + kUnitBytes * u + 64 * s + 16 * j);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[2 * s], f8_to_f16x8(a[0], a[1]), d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[2 * s + 1], f8_to_f16x8(a[2], a[3]), d, 0, 0, 0);
         }
+        const float sc = sbuf[u * kRows + r] * sw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], sc, acc[i]);
       }
     };
 
@@ -200,34 +195,24 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
     }
 
     if constexpr (KS > 1) {
-      if (ks > 0) {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) red[ks - 1][blk][t][lane] = acc[t];
-      }
+      if (ks > 0) red[ks - 1][blk][lane] = acc;
       lds_barrier();
       if (ks == 0) {
 #pragma unroll
-        for (int o = 0; o < KS - 1; ++o)
-#pragma unroll
-          for (int t = 0; t < MT; ++t) acc[t] += red[o][blk][t][lane];
+        for (int o = 0; o < KS - 1; ++o) acc += red[o][blk][lane];
       }
     }
-    if (ks == 0) {
-      const int n = n_base + 4 * j;
+    const int m = m0 + r, n = n_base + 4 * j;
+    if (ks == 0 && m < hi) {
+      OutT* dst = y + (int64_t)m * N + n;
+      if (vec && n + 4 <= N) {
+        typedef OutT o4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<o4*>(dst) = o4{Out<OutT>::cvt(acc[0]), Out<OutT>::cvt(acc[1]),
+                                         Out<OutT>::cvt(acc[2]), Out<OutT>::cvt(acc[3])};
+      } else {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int m = m0 + 16 * t + r;
-        if (m >= hi) continue;
-        OutT* dst = y + (int64_t)m * N + n;
-        if (vec && n + 4 <= N) {
-          typedef OutT o4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<o4*>(dst) = o4{Out<OutT>::cvt(acc[t][0]), Out<OutT>::cvt(acc[t][1]),
-                                           Out<OutT>::cvt(acc[t][2]), Out<OutT>::cvt(acc[t][3])};
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n + i < N) dst[i] = Out<OutT>::cvt(acc[t][i]);
-        }
+        for (int i = 0; i < 4; ++i)
+          if (n + i < N) dst[i] = Out<OutT>::cvt(acc[i]);
       }
     }
     // the next run of rows overwrites phase buffers and partial sums that
@@ -236,29 +221,29 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
   }
 }
 
-template <int MT, int NB, int KS, typename OutT>
+template <int NB, int KS, typename OutT>
 static void launch_f8_stream_nb(const uint8_t* xq, const float* xs, const uint8_t* wq,
                                 const float* ws, const F8Rows& fr, int64_t E, int N, int K,
                                 OutT* y, int vec, hipStream_t st) {
-  constexpr int UPW = MT == 1 ? 2 : 1;
+  constexpr int UPW = 2;
   const int64_t groups_n = ((N + 15) / 16 + NB - 1) / NB;
   const dim3 block(64 * NB * KS);
   if (fr.offsets)
-    k_f8_stream<MT, NB, KS, UPW, OutT, true><<<dim3((unsigned)(E * groups_n)), block, 0, st>>>(
+    k_f8_stream<NB, KS, UPW, OutT, true><<<dim3((unsigned)(E * groups_n)), block, 0, st>>>(
         xq, xs, wq, ws, fr, N, K, y, vec);
   else
-    k_f8_stream<MT, NB, KS, UPW, OutT, false><<<dim3((unsigned)groups_n), block, 0, st>>>(
+    k_f8_stream<NB, KS, UPW, OutT, false><<<dim3((unsigned)groups_n), block, 0, st>>>(
         xq, xs, wq, ws, fr, N, K, y, vec);
 }
 
-template <int MT, typename OutT>
+template <typename OutT>
 static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* wq,
                              const float* ws, const F8Rows& fr, int64_t E, int N, int K, OutT* y,
                              int vec, hipStream_t st) {
   const int64_t blocks = E * ((N + 15) / 16);
-  if (blocks <= 256) launch_f8_stream_nb<MT, 1, MT <= 2 ? 8 : 4, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  else if (blocks <= 768) launch_f8_stream_nb<MT, 2, 4, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  else launch_f8_stream_nb<MT, 4, 2, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  if (blocks <= 256) launch_f8_stream_nb<1, 8>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  else if (blocks <= 768) launch_f8_stream_nb<2, 4>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  else launch_f8_stream_nb<4, 2>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -275,194 +260,369 @@ static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* 
 // ---------------------------------------------------------------------------
 constexpr int kF8Stage = 128;   // bytes of a row in a stage = one scale block
 
+// Token rows, weight rows, token scales in runs of 64, and the weight scales of
+// the tile's column blocks.
 template <int BM, int BN>
-constexpr int f8_stage_bytes() { return (BM + BN) * kF8Stage + 4 * BM; }
+constexpr int f8_stage_bytes() { return (BM + BN) * kF8Stage + 4 * BM + 256; }
+
+// Direct loads into LDS, 16 and 4 bytes a lane at lds (wave-uniform) + 16 or
+// 4 lane, at byte voff + soff of the resource; out of range reads zeros.
+__device__ __forceinline__ void f8_dma16(rsrc_t r, int8_t* lds, u32 voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, QG_LDS(lds), 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void f8_dma4(rsrc_t r, int8_t* lds, u32 voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, QG_LDS(lds), 4, voff, soff, 0, 0);
+}
 
 // Tile of a workgroup: rows m0 .. < hi of y (m0 + BM may pass hi), columns n0 ..
 struct F8Tile {
   int e, m0, hi, n0;
 };
 
-template <int BM, int BN, int WM, int WN, bool EXACT, typename OutT, bool EXPERTS>
-__device__ __forceinline__ void f8_tile(int8_t* lds, const uint8_t* __restrict__ xq,
-                                        const float* __restrict__ xs,
-                                        const uint8_t* __restrict__ wq,
-                                        const float* __restrict__ ws, const F8Rows& fr,
-                                        const F8Tile& at, int N, int K, OutT* __restrict__ y,
-                                        int vec) {
+template <int BM, int BN, int WM, int WN, int KS, int NB, bool EXACT, typename OutT, bool EXPERTS, typename Next>
+__device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict__ xq,
+                                         const float* __restrict__ xs,
+                                         const uint8_t* __restrict__ wq,
+                                         const float* __restrict__ ws, const F8Rows& fr, int N,
+                                         int K, OutT* __restrict__ y, int vec, Next next_tile) {
   constexpr int NW = WM * WN, MI = BM / WM / 32, NJ = BN / WN / 32;
   constexpr int kStage = f8_stage_bytes<BM, BN>();
-  constexpr int kLoadsA = BM / 8, kLoadsB = BN / 8;      // 1 KB loads of 8 rows
-  constexpr int LA = kLoadsA / NW, LB = kLoadsB / NW;    // of each wave
-  constexpr int LS = BM / 64;                            // scale loads: 64 rows each
-  static_assert(LA * NW == kLoadsA && LB * NW == kLoadsB && LS <= NW, "whole loads per wave");
+  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;      // 1 KB loads of 8 rows, of each wave
+  static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && BM < 64 * NW && BM % 64 == 0,
+                "whole loads per wave");
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // KS groups of waves share a tile: group kg multiplies stages kg, kg + KS, ..
+  // out of a ring of its own, and the sums meet at the end
+  const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * NW));
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % NW);
+  int8_t* const lds = lds0 + kg * (NB * kStage);
   const int wm = wave / WN, wn = wave % WN;
   const int row_a = wm * 32 * MI, row_b = wn * 32 * NJ;
   const int G = (K + kF8Block - 1) / kF8Block, B = (N + kF8Block - 1) / kF8Block;
-
-  // Token rows come from one resource: of this tile's rows where they follow
-  // each other, else of all of xq (whose size the host keeps under 2 GiB).
   const bool gather = EXPERTS && fr.token != nullptr;
-  const int64_t row0 = gather ? 0 : at.m0;
-  const int rows_x = gather ? (int)fr.T : (int)min((int64_t)BM, min((int64_t)at.hi, fr.T) - at.m0);
-  const rsrc_t ar = make_rsrc_uniform(xq + row0 * K, (u32)(max(rows_x, 0) * K));
-  const rsrc_t sr = make_rsrc_uniform(xs + row0 * G, (u32)(max(rows_x, 0) * G * 4));
-  const rsrc_t br = make_rsrc_uniform(wq + ((int64_t)at.e * N + at.n0) * K,
-                                      (u32)(min(BN, N - at.n0) * K));
-  const float* wsr = ws + ((int64_t)at.e * B + min((at.n0 + row_b) / kF8Block, B - 1)) * G;
 
-  // Byte offset of this lane's row for each of its loads (kOOB: no row).
+  // ---- loads of a tile's stages ----
+  // Byte offset of this lane's chunk of stage 0 for each of its loads (kOOB: no
+  // row), the scale's likewise.  A stage adds 128 bytes as a scalar offset; in
+  // the last stage the chunks past K are masked.
   const int lrow = lane >> 3, slot = lane & 7;
-  u32 offa[LA];
-  int cha[LA];
+  u32 offa[LA], offb[LB], offs;
+  rsrc_t ar, sr, br;
 #pragma unroll
-  for (int i = 0; i < LA; ++i) {
-    const int row = 8 * (wave * LA + i) + lrow;
-    cha[i] = 16 * (slot ^ ((row >> 1) & 7));
-    if (EXPERTS) {
-      const int64_t t = f8_source(fr, at.m0 + row, at.hi);
-      offa[i] = t < 0 ? kOOB : (u32)((t - row0) * K);
-    } else {
-      offa[i] = row < rows_x ? (u32)(row * K) : kOOB;
-    }
+  for (int i = 0; i < LB; ++i) {   // rows past N lie behind the resource's end
+    const int row = 8 * (wave * LB + i) + lrow;
+    offb[i] = (u32)(row * K) + 16 * (slot ^ ((row >> 1) & 7));
   }
-  u32 offs = kOOB;
-  if (wave < LS) {
+  // The rows of xq this lane's loads of a tile take, and that of its scale;
+  // -1: none.  Wave w < BM / 64 loads token scales, the others (all alike) the
+  // weight scales.
+  struct Rows {
+    int a[LA], s;
+  };
+  auto rows_of = [&](const F8Tile& at) {
+    Rows r;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) r.a[i] = f8_source(fr, at.m0 + 8 * (wave * LA + i) + lrow, at.hi);
     const int row = 64 * wave + lane;
-    if (EXPERTS) {
-      const int64_t t = f8_source(fr, at.m0 + row, at.hi);
-      offs = t < 0 ? kOOB : (u32)((t - row0) * G * 4);
+    r.s = row < BM ? f8_source(fr, at.m0 + row, at.hi) : -1;
+    return r;
+  };
+  auto aim = [&](const F8Tile& at, const Rows& r) {
+    // Token rows come from one resource: of this tile's rows where they follow
+    // each other, else of all of xq (whose size the host keeps under 2 GiB).
+    // (Never 0 rows long: a scalar offset past a resource's size is not in its
+    // range check; a row that does not exist has an offset past any size.)
+    const int row0 = gather ? 0 : at.m0;
+    const int rows_x = max(gather ? fr.T : min(BM, min(at.hi, fr.T) - at.m0), 1);
+    ar = make_rsrc_uniform(xq + (int64_t)row0 * K, (u32)(rows_x * K));
+    br = make_rsrc_uniform(wq + ((int64_t)at.e * N + at.n0) * K, (u32)(min(BN, N - at.n0) * K));
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      offa[i] = r.a[i] < 0 ? kOOB : (u32)((r.a[i] - row0) * K) + 16 * (slot ^ (((8 * (wave * LA + i) + lrow) >> 1) & 7));
+    if (wave < BM / 64) {
+      sr = make_rsrc_uniform(xs + (int64_t)row0 * G, (u32)(rows_x * G * 4));
+      offs = r.s < 0 ? kOOB : (u32)((r.s - row0) * G * 4);
     } else {
-      offs = row < rows_x ? (u32)(row * G * 4) : kOOB;
+      const int b0 = at.n0 / kF8Block, blocks = min((BN + kF8Block - 1) / kF8Block, B - b0);
+      sr = make_rsrc_uniform(ws + ((int64_t)at.e * B + b0) * G, (u32)(blocks * G * 4));
+      offs = lane < blocks ? (u32)(lane * G * 4) : kOOB;
     }
-  }
-  // One load of a stage: i < LA token rows, then weight rows, then scales.
-  auto dma = [&](int8_t* buf, int g, int i) {
+  };
+  // One load of stage g: i < LA token rows, then weight rows, then scales.
+  // in.row[b]: whether the lane's chunk of a load with q % 2 == b lies within K
+  // (never past the last stage, whose successor is loaded as zeros).
+  struct StageIn {
+    bool row[2], scale;
+  };
+  auto stage_in = [&](int g) {
+    StageIn in;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) in.row[b] = g * kF8Stage + 16 * (slot ^ ((4 * b + (lrow >> 1)) & 7)) < K;
+    in.scale = g < G;
+    return in;
+  };
+  auto dma = [&](int8_t* buf, int g, int i, const StageIn& in) {
     if (i < LA) {
-      const int k = g * kF8Stage + cha[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, QG_LDS(buf + (wave * LA + i) * 1024), 16,
-                                               k < K && offa[i] != kOOB ? offa[i] + k : kOOB, 0, 0, 0);
+      const int q = wave * LA + i;
+      f8_dma16(ar, buf + q * 1024, in.row[LA % 2 ? q & 1 : i & 1] ? offa[i] : kOOB, g * kF8Stage);
     } else if (i < LA + LB) {
-      const int q = wave * LB + i - LA, row = 8 * q + lrow;
-      const int k = g * kF8Stage + 16 * (slot ^ ((row >> 1) & 7));
-      // rows past N lie behind the resource's end
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, QG_LDS(buf + BM * kF8Stage + q * 1024), 16,
-                                               k < K ? (u32)(row * K + k) : kOOB, 0, 0, 0);
-    } else if (wave < LS) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, QG_LDS(buf + (BM + BN) * kF8Stage + wave * 256), 4,
-                                               g < G && offs != kOOB ? offs + 4 * g : kOOB, 0, 0, 0);
+      const int q = wave * LB + i - LA;
+      f8_dma16(br, buf + BM * kF8Stage + q * 1024, in.row[LB % 2 ? q & 1 : (i - LA) & 1] ? offb[i - LA] : kOOB, g * kF8Stage);
+    } else {
+      f8_dma4(sr, buf + (BM + BN) * kF8Stage + min(wave, BM / 64) * 256, in.scale ? offs : kOOB, 4 * g);
     }
   };
   constexpr int kLoads = LA + LB + 1;
-
-  v16f acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int jj = 0; jj < NJ; ++jj) acc[i][jj] = v16f{};
-
+  // ---- products of a stage ----
   const int l31 = lane & 31, half = lane >> 5;
-  // The four chunks of a row that a lane holds: 4 (of 8) 16-byte chunks; both
-  // operands split k alike, so any fixed split will do.
-  auto frag = [&](const int8_t* base, int row, v4i (&f)[4]) {
+  // A lane holds 4 of a row's 8 chunks; both operands split k alike, so any
+  // fixed split will do.  The swizzle depends on the row's low bits only, so
+  // the slots are the same for every 32-row block.
+  int cslot[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int ch = 4 * half + c;
-      f[c] = ld16(base + row * kF8Stage + ((ch ^ ((row >> 1) & 7)) << 4));
-    }
+  for (int c = 0; c < 4; ++c) cslot[c] = l31 * kF8Stage + (((4 * half + c) ^ ((l31 >> 1) & 7)) << 4);
+  auto frag = [&](const int8_t* base, v4i (&f)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] = ld16(base + cslot[c]);
   };
-  auto multiply = [&](const int8_t* buf, int8_t* next, int g) {
-    v4i bf[NJ][4];
+  v16f acc[MI][NJ];
+  // The product of a 32 x 32 block over the stage is a chain of its own that
+  // starts at zero; it is scaled into the accumulators one step later, so the
+  // vector ALU works on one block while the matrix core is at the next.  The
+  // last block's turn comes in the next stage.
+  constexpr int kSteps = MI * NJ;
+  static_assert(kSteps % 2 == 0 || kSteps == 1, "the two products in flight alternate");
+  v16f d[2];
+  float sprev;
+  auto scale_in = [&](int t, const v16f& p, float sc) {
 #pragma unroll
-    for (int jj = 0; jj < NJ; ++jj) frag(buf + BM * kF8Stage, row_b + 32 * jj + l31, bf[jj]);
+    for (int q = 0; q < 16; ++q) acc[t / NJ][t % NJ][q] = fmaf(p[q], sc, acc[t / NJ][t % NJ][q]);
+    // keeps the sums here, next to the following block's products: the
+    // compiler would gather them at the end and hold every product until then
+    asm volatile("" : "+v"(acc[t / NJ][t % NJ]));
+  };
+  auto multiply = [&](const int8_t* buf, int8_t* ahead, int g) {
+    v4i bf[NJ][4], af[2][4];
+    float sx[MI];
+    frag(buf + row_a * kF8Stage, af[0]);
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) frag(buf + BM * kF8Stage + (row_b + 32 * jj) * kF8Stage, bf[jj]);
     const float* sc = reinterpret_cast<const float*>(buf + (BM + BN) * kF8Stage);
-    const float sw = wsr[min(g, G - 1)];
-    v4i af[2][4];
-    frag(buf, row_a + l31, af[0]);
-    constexpr int kEvery = (kLoads + MI * NJ - 1) / (MI * NJ);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (i + 1 < MI) frag(buf, row_a + 32 * (i + 1) + l31, af[(i + 1) & 1]);
+    for (int i = 0; i < MI; ++i) sx[i] = sc[row_a + 32 * i + l31];
+    const StageIn in = stage_in(g + KS * (NB - 1));
+    const float sw = sc[BM + row_b / kF8Block];
+    constexpr int kEvery = (kLoads + kSteps - 1) / kSteps;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+      const int i = t / NJ, jj = t % NJ;
+      if (jj == 0 && i + 1 < MI) frag(buf + (row_a + 32 * (i + 1)) * kF8Stage, af[(i + 1) & 1]);
       const v4i (&a)[4] = af[i & 1];
-      const float s = sc[row_a + 32 * i + l31] * sw;
+      const v4i (&b)[4] = bf[jj];
+      v16f p = {};
+      if constexpr (EXACT) {
 #pragma unroll
-      for (int jj = 0; jj < NJ; ++jj) {
-        __builtin_amdgcn_sched_barrier(0);
-        v16f d = {};
-        const v4i (&b)[4] = bf[jj];
-        if constexpr (EXACT) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            d = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_f16x8(b[c][0], b[c][1]), f8_to_f16x8(a[c][0], a[c][1]), d, 0, 0, 0);
-            d = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_f16x8(b[c][2], b[c][3]), f8_to_f16x8(a[c][2], a[c][3]), d, 0, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            const v8i bb = {b[c][0], b[c][1], b[c][2], b[c][3], b[c + 1][0], b[c + 1][1], b[c + 1][2], b[c + 1][3]};
-            const v8i aa = {a[c][0], a[c][1], a[c][2], a[c][3], a[c + 1][0], a[c + 1][1], a[c + 1][2], a[c + 1][3]};
-            d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bb, aa, d, 0, 0, 0, 0, 0, 0);
-          }
+        for (int c = 0; c < 4; ++c) {
+          p = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_f16x8(b[c][0], b[c][1]), f8_to_f16x8(a[c][0], a[c][1]), p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_32x32x16_f16(f8_to_f16x8(b[c][2], b[c][3]), f8_to_f16x8(a[c][2], a[c][3]), p, 0, 0, 0);
         }
-        // this wave's loads of the next stage, spread over the products
+      } else {
 #pragma unroll
-        for (int l = 0; l < kEvery; ++l) {
-          const int ld = (i * NJ + jj) * kEvery + l;
-          if (ld < kLoads) dma(next, g + 1, ld);
+        for (int c = 0; c < 4; c += 2) {
+          const v8i bb = {b[c][0], b[c][1], b[c][2], b[c][3], b[c + 1][0], b[c + 1][1], b[c + 1][2], b[c + 1][3]};
+          const v8i aa = {a[c][0], a[c][1], a[c][2], a[c][3], a[c + 1][0], a[c + 1][1], a[c + 1][2], a[c + 1][3]};
+          p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bb, aa, p, 0, 0, 0, 0, 0, 0);
         }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[i][jj][q] = fmaf(d[q], s, acc[i][jj][q]);
       }
+      // this wave's loads of a later stage, ahead of its last products
+#pragma unroll
+      for (int l = 0; l < kEvery; ++l)
+        if (t * kEvery + l < kLoads) dma(ahead, g + KS * (NB - 1), t * kEvery + l, in);
+      if constexpr (kSteps == 1) {
+        scale_in(0, d[0], sprev);
+        d[0] = p;
+      } else {
+        scale_in((t + kSteps - 1) % kSteps, d[(t + 1) & 1], sprev);
+        d[t & 1] = p;
+      }
+      sprev = sx[i] * sw;
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // This wave's loads have landed and all waves are done with the buffer that
-  // the next loads overwrite.
+  // This wave's loads have landed, its LDS reads are done, and so are all
+  // other waves'.  (Stages are awaited by sync_stage, which leaves the loads of
+  // the stages after it under way: vmcnt counts in order.)
   auto sync = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) dma(lds, 0, i);
-  for (int g = 0; g < G; g += 2) {
-    // a stage past G is loaded as zeros and adds nothing (one at most)
-    sync();
-    multiply(lds, lds + kStage, g);
-    sync();
-    multiply(lds + kStage, lds, g + 1);
-  }
-  sync();   // the last (zero) loads have landed before LDS is used again
-
+  // ---- outputs of a tile ----
   // Lane l holds token row 32 i + (l & 31); register q of block (i, jj) output
-  // column 32 jj + 8 (q >> 2) + 4 (l >> 5) + (q & 3).
+  // column 32 jj + 8 (q >> 2) + 4 (l >> 5) + (q & 3).  Stored from there, a wave
+  // would touch 32 rows with 16 bytes each, so where rows of y are 16-byte
+  // aligned (vec 2) the outputs are turned in LDS, JP column blocks (up to 128
+  // bytes of a row) at a time, and leave as 16-byte chunks of consecutive lanes
+  // (4096 x 4096 x 11008: 211 us with the direct stores, 197 so).
+  typedef OutT o4 __attribute__((ext_vector_type(4)));
+  constexpr int E = (int)sizeof(OutT);
+  constexpr int kRegion = (EXPERTS || KS > 1 ? 1 : NB) * kStage;   // experts: the others hold the next tile's loads
+  constexpr int JP = NJ % 2 == 0 && 64 * E <= 128 && NW * 32 * MI * 64 * E <= kRegion ? 2 : 1;
+  constexpr int RB = JP * 32 * E, CH = RB / 16;
+  constexpr int IP = NW * 32 * MI * RB <= kRegion ? MI : MI % 2 == 0 ? MI / 2 : 1;   // row blocks at a time
+  constexpr int kStoresPerPass = 32 * IP * CH / 64, kStores = MI / IP * (NJ / JP) * kStoresPerPass;
+  constexpr int kUnder = (NB - 2) * kLoads;              // loads of the later stages
+  static_assert(kUnder + (EXPERTS ? kStores : 0) <= 63, "vmcnt counts to 63");
+  static_assert(NW * 32 * IP * RB <= kRegion, "a region of LDS for each wave");
+  auto four = [&](int i, int jj, int q) {
+    return o4{Out<OutT>::cvt(acc[i][jj][4 * q]), Out<OutT>::cvt(acc[i][jj][4 * q + 1]),
+              Out<OutT>::cvt(acc[i][jj][4 * q + 2]), Out<OutT>::cvt(acc[i][jj][4 * q + 3])};
+  };
+  auto store_lines = [&](const F8Tile& at, int8_t* region) {
+    int8_t* reg = region + wave * (32 * IP * RB);
+    // rows past the run and columns past N go out of the resource's range:
+    // every store is issued, so their number is known to the next wait
+    const rsrc_t yr = make_rsrc_uniform(y + (int64_t)at.m0 * N, (u32)((at.hi - at.m0 < BM ? at.hi - at.m0 : BM) * N * E));
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = at.m0 + row_a + 32 * i + l31;
-    if (m >= at.hi) continue;
+    for (int ps = 0; ps < MI / IP * (NJ / JP); ++ps) {
+      const int ip = ps / (NJ / JP) * IP, jp = ps % (NJ / JP) * JP;
 #pragma unroll
-    for (int jj = 0; jj < NJ; ++jj)
+      for (int jj = 0; jj < JP; ++jj)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = at.n0 + row_b + 32 * jj + 8 * q + 4 * half;
-        OutT* dst = y + (int64_t)m * N + n;
-        if (vec && n + 4 <= N) {
-          typedef OutT o4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<o4*>(dst) =
-              o4{Out<OutT>::cvt(acc[i][jj][4 * q]), Out<OutT>::cvt(acc[i][jj][4 * q + 1]),
-                 Out<OutT>::cvt(acc[i][jj][4 * q + 2]), Out<OutT>::cvt(acc[i][jj][4 * q + 3])};
-        } else {
+        for (int i = 0; i < IP; ++i)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (n + t < N) dst[t] = Out<OutT>::cvt(acc[i][jj][4 * q + t]);
-        }
+          for (int q = 0; q < 4; ++q) {
+            const int row = 32 * i + l31, byte = E * (32 * jj + 8 * q + 4 * half);
+            *reinterpret_cast<o4*>(reg + row * RB + (((byte >> 4) ^ (row & (CH - 1))) << 4) + (byte & 15)) = four(ip + i, jp + jj, q);
+          }
+      // one wave's LDS accesses execute in order; the statement keeps the
+      // compiler from reordering them
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int it = 0; it < kStoresPerPass; ++it) {
+        const int row = it * (64 / CH) + lane / CH, ch = lane % CH;
+        const int n = at.n0 + row_b + 32 * jp + ch * (16 / E);
+        const v4i v = ld16(reg + row * RB + ((ch ^ (row & (CH - 1))) << 4));
+        __builtin_amdgcn_raw_buffer_store_b128(v, yr, n < N ? (u32)(((row_a + 32 * ip + row) * N + n) * E) : kOOB, 0, 0);
       }
+      asm volatile("" ::: "memory");
+    }
+  };
+  auto store_direct = [&](const F8Tile& at) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = at.m0 + row_a + 32 * i + l31;
+      if (m >= at.hi) continue;
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = at.n0 + row_b + 32 * jj + 8 * q + 4 * half;
+          OutT* dst = y + (int64_t)m * N + n;
+          if (vec && n + 4 <= N) {
+            *reinterpret_cast<o4*>(dst) = four(i, jj, q);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              if (n + t < N) dst[t] = Out<OutT>::cvt(acc[i][jj][4 * q + t]);
+          }
+        }
+    }
+  };
+
+  // ---- the tiles ----
+  // The first stages of the next tile are loaded ahead of a tile's stores, and
+  // the next tile waits for those loads only, not for the stores behind them.
+  auto sync_stage = [&](bool stores) {
+    if (EXPERTS && stores)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kUnder + kStores) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kUnder) : "memory");
+  };
+  auto buffer = [&](int b) { return lds + (b >= NB ? b - NB : b) * kStage; };
+  F8Tile at, next;
+  if (!next_tile(at)) return;
+  int sb = 0;                        // buffer of the tile's first stage
+  aim(at, rows_of(at));
+  auto first_stages = [&](int b) {
+#pragma unroll
+    for (int g = 0; g < NB - 1; ++g) {
+      const StageIn in = stage_in(kg + KS * g);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) dma(buffer(b + g), kg + KS * g, i, in);
+    }
+  };
+  first_stages(0);
+  bool stored = false;               // kStores stores were issued behind the first stages' loads
+  for (;;) {
+    const bool more = next_tile(next);
+    Rows rn;
+    if (EXPERTS && more) rn = rows_of(next);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) acc[i][jj] = v16f{};
+    d[0] = d[1] = v16f{};
+    sprev = 0.f;
+    int b = sb;                      // buffer of stage g; the one before it is free
+    // (every group runs the same number of stages; one past G is all zeros)
+    for (int g = 0; g < (G + KS - 1) / KS; ++g) {
+      sync_stage(stored && g < NB - 1);
+      multiply(buffer(b), buffer(b + NB - 1), kg + KS * g);
+      b = b + 1 == NB ? 0 : b + 1;
+    }
+    scale_in(kSteps - 1, d[(kSteps - 1) & 1], sprev);
+    sync();   // the stage buffers are free
+    if (EXPERTS && more) {
+      aim(next, rn);
+      first_stages(b);
+    }
+    if constexpr (KS > 1) {
+      // the other groups hand their sums to group 0, which adds them in order
+      constexpr int kSums = 4096;     // 16 sums of 64 lanes
+      static_assert(NW * MI * NJ * kSums <= kStage, "a wave's sums in its ring's free buffer");
+      auto part = [&](int k, int i, int jj, int c) {
+        int8_t* free = buffer(b + NB - 1) + (k - kg) * (NB * kStage);
+        return free + ((wave * MI + i) * NJ + jj) * kSums + c * 1024 + 16 * lane;
+      };
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int jj = 0; jj < NJ; ++jj)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (kg > 0)
+              *reinterpret_cast<v4f*>(part(kg, i, jj, c)) = v4f{acc[i][jj][4 * c], acc[i][jj][4 * c + 1], acc[i][jj][4 * c + 2], acc[i][jj][4 * c + 3]};
+      lds_barrier();
+      if (kg == 0) {
+#pragma unroll
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int jj = 0; jj < NJ; ++jj)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const v4f o = *reinterpret_cast<const v4f*>(part(k, i, jj, c));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][jj][4 * c + q] += o[q];
+              }
+      }
+    }
+    if (kg == 0) {
+      if (vec > 1) store_lines(at, EXPERTS || KS > 1 ? buffer(b + NB - 1) : lds);
+      else store_direct(at);
+    }
+    if (!EXPERTS || !more) return;
+    at = next;
+    sb = b;
+    stored = vec > 1 && kg == 0;
   }
 }
 
-template <int BM, int BN, int WM, int WN, bool EXACT, typename OutT>
-__global__ __launch_bounds__(64 * WM * WN) void k_f8_tile(
+template <int BM, int BN, int WM, int WN, int KS, int NB, bool EXACT, typename OutT>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, F8Rows fr, int N, int K, OutT* __restrict__ y, int vec) {
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * f8_stage_bytes<BM, BN>()];
+  __shared__ __attribute__((aligned(16))) int8_t lds[KS * NB * f8_stage_bytes<BM, BN>()];
   const int M = fr.R;
   // Consecutive workgroups go to the 8 XCDs in turn: renumber so that each
   // XCD walks a contiguous run of tiles, in column-major groups of 4 tile
@@ -473,8 +633,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile(
   constexpr int GROUP = 4;
   const int group = bid / (GROUP * tiles_n), first = group * GROUP;
   const int gsize = min(tiles_m - first, GROUP), in = bid - group * GROUP * tiles_n;
-  const F8Tile at{0, (first + in % gsize) * BM, M, in / gsize * BN};
-  f8_tile<BM, BN, WM, WN, EXACT, OutT, false>(lds, xq, xs, wq, ws, fr, at, N, K, y, vec);
+  int left = 1;
+  f8_tiles<BM, BN, WM, WN, KS, NB, EXACT, OutT, false>(lds, xq, xs, wq, ws, fr, N, K, y, vec, [&](F8Tile& t) {
+    t = F8Tile{0, (first + in % gsize) * BM, M, in / gsize * BN};
+    return left-- > 0;
+  });
 }
 
 // The experts' tiles.  The row counts are on the GPU only, so every workgroup
@@ -483,12 +646,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile(
 // weights stay in one L2.
 constexpr int kF8MaxExperts = 1024;
 
-template <int BM, int BN, int WM, int WN, bool EXACT, typename OutT>
-__global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_experts(
+template <int BM, int BN, int WM, int WN, int KS, int NB, bool EXACT, typename OutT>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, F8Rows fr, int E, int N, int K, OutT* __restrict__ y, int vec) {
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * f8_stage_bytes<BM, BN>()];
-  __shared__ int first[kF8MaxExperts + 1];   // tile rows ahead of each expert
+  __shared__ __attribute__((aligned(16))) int8_t lds[KS * NB * f8_stage_bytes<BM, BN>()];
+  // tile rows ahead of each expert, and its rows
+  __shared__ int first[kF8MaxExperts + 1], low[kF8MaxExperts], high[kF8MaxExperts];
   const int tiles_n = (N + BN - 1) / BN;
   if (threadIdx.x < kWave) {
     // each lane counts a run of experts, the lanes' sums are scanned; offsets
@@ -499,6 +663,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_experts(
     for (int e = e0; e < min(e0 + per, E); ++e) {
       int lo, hi;
       f8_expert_rows(fr, e, lo, hi);
+      low[e] = lo;
+      high[e] = hi;
       sum += (hi - lo + BM - 1) / BM;
     }
     int64_t run = sum;
@@ -509,10 +675,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_experts(
     }
     run -= sum;
     for (int e = e0; e < min(e0 + per, E); ++e) {
-      int lo, hi;
-      f8_expert_rows(fr, e, lo, hi);
       first[e] = (int)min(run, most);
-      run += (hi - lo + BM - 1) / BM;
+      run += (high[e] - low[e] + BM - 1) / BM;
     }
     if (threadIdx.x == kWave - 1) first[E] = (int)min(run, most);
   }
@@ -520,7 +684,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_experts(
   const int total = first[E] * tiles_n;
   const int per = total / 8, rem = total % 8, xcd = blockIdx.x % 8;
   const int begin = xcd * per + min(xcd, rem), end = begin + per + (xcd < rem);
-  for (int t = begin + blockIdx.x / 8; t < end; t += gridDim.x / 8) {
+  int t = begin + blockIdx.x / 8;
+  f8_tiles<BM, BN, WM, WN, KS, NB, EXACT, OutT, true>(lds, xq, xs, wq, ws, fr, N, K, y, vec, [&](F8Tile& to) {
+    if (t >= end) return false;
     // the last expert whose first tile is at or before t
     int a = 0, b = E - 1;
     while (a < b) {
@@ -528,51 +694,79 @@ __global__ __launch_bounds__(64 * WM * WN) void k_f8_tile_experts(
       if (first[mid] * tiles_n <= t) a = mid;
       else b = mid - 1;
     }
-    int lo, hi;
-    f8_expert_rows(fr, a, lo, hi);
-    const int rows = first[a + 1] - first[a], in = t - first[a] * tiles_n;
-    const F8Tile at{a, lo + in % rows * BM, hi, in / rows * BN};
-    f8_tile<BM, BN, WM, WN, EXACT, OutT, true>(lds, xq, xs, wq, ws, fr, at, N, K, y, vec);
-  }
+    a = __builtin_amdgcn_readfirstlane(a);
+    const int lo = __builtin_amdgcn_readfirstlane(low[a]), hi = __builtin_amdgcn_readfirstlane(high[a]);
+    const int in = t - __builtin_amdgcn_readfirstlane(first[a]) * tiles_n, rows = (hi - lo + BM - 1) / BM;
+    to = F8Tile{a, lo + in % rows * BM, hi, in / rows * BN};
+    t += gridDim.x / 8;
+    return true;
+  });
 }
 
-template <int BM, int BN, int WM, int WN, typename OutT>
+template <int BM, int BN, int WM, int WN, int KS, int NB, typename OutT>
+static void launch_f8_tile(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                           const F8Rows& fr, int N, int K, OutT* y, int vec, hipStream_t st) {
+  const int64_t tiles = ((int64_t)fr.R + BM - 1) / BM * ((N + BN - 1) / BN);
+  k_f8_tile<BM, BN, WM, WN, KS, NB, std::is_same<OutT, float>::value, OutT>
+      <<<dim3((unsigned)tiles), dim3(64 * WM * WN * KS), 0, st>>>(xq, xs, wq, ws, fr, N, K, y, vec);
+}
+
+template <int BM, int BN, int WM, int WN, int KS, int NB, typename OutT>
 static void launch_f8_tile(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                            const F8Rows& fr, int64_t E, int N, int K, OutT* y, int vec,
                            hipStream_t st) {
-  constexpr bool EXACT = std::is_same<OutT, float>::value;
-  constexpr int kLds = 2 * f8_stage_bytes<BM, BN>() + 4 * (kF8MaxExperts + 1);
-  const dim3 block(64 * WM * WN);
-  const int64_t tiles_n = (N + BN - 1) / BN;
-  if (fr.offsets) {
-    // as many workgroups as can be resident, a multiple of the 8 XCDs
-    const int64_t most = ((int64_t)fr.R + BM - 1) / BM + E;
-    const int64_t grid = std::min<int64_t>(256 * (int64_t)(kLdsBytesPerCU / kLds), (most * tiles_n + 7) / 8 * 8);
-    k_f8_tile_experts<BM, BN, WM, WN, EXACT, OutT><<<dim3((unsigned)grid), block, 0, st>>>(
-        xq, xs, wq, ws, fr, (int)E, N, K, y, vec);
-  } else {
-    const int64_t tiles = ((int64_t)fr.R + BM - 1) / BM * tiles_n;
-    k_f8_tile<BM, BN, WM, WN, EXACT, OutT><<<dim3((unsigned)tiles), block, 0, st>>>(
-        xq, xs, wq, ws, fr, N, K, y, vec);
-  }
+  if (!fr.offsets)
+    return launch_f8_tile<BM, BN, WM, WN, KS, NB>(xq, xs, wq, ws, fr, N, K, y, vec, st);
+  // as many workgroups as can be resident, a multiple of the 8 XCDs
+  constexpr int kLds = KS * NB * f8_stage_bytes<BM, BN>() + 12 * kF8MaxExperts + 4;
+  const int64_t most = (((int64_t)fr.R + BM - 1) / BM + E) * ((N + BN - 1) / BN);
+  const int64_t grid = std::min<int64_t>(256 * (int64_t)(kLdsBytesPerCU / kLds), (most + 7) / 8 * 8);
+  k_f8_tile_experts<BM, BN, WM, WN, KS, NB, std::is_same<OutT, float>::value, OutT>
+      <<<dim3((unsigned)grid), dim3(64 * WM * WN * KS), 0, st>>>(xq, xs, wq, ws, fr, (int)E, N, K, y, vec);
 }
 
+// Kernel by the rows of one weight matrix (of the mean expert) and the number
+// of tiles, measured on MI355X (us):
+//  * the stream kernel up to 16 rows (16 x 11008 x 4096: 15.5, tiles 21.6; it
+//    loses from 17 rows on wide layers, 17 x 4096 x 11008: 15.6, tiles 10.8, and
+//    gains 1.4 on 17 x 4096 x 4096), with experts up to a mean of 8, since an
+//    expert with more than 16 rows reads its weights again (16 experts of 1376 x
+//    4096, mean 16: 37.7, tiles 20.4; mean 8: 22.4 both);
+//  * 64 x 64 tiles, two groups of waves sharing K, while one round of
+//    workgroups holds them all (200 x 4096 x 4096: 11.2, one group 12.7), one
+//    group beyond (128 x 4096 x 11008: 17.9, two groups 20.7);
+//  * 128 x 128 tiles from 256 of them on (512 x 4096 x 11008: 32.6, 64 x 64 tiles
+//    48.5);
+//  * 256 x 256 tiles, 16-bit outputs of one matrix, where their rounds (one
+//    workgroup on a CU) cost less than those of 128 x 128 (two on a CU, a round
+//    5/8 as long): 4096 x 4096 x 11008 187 against 225, 1024 x 4096 x 11008 57
+//    against 64, but 2048 x 4096 x 4096 53 against 40.
+// Of the two groups of products, binary32 outputs take more registers than a
+// 256 x 256 tile leaves; experts' rows seldom fill one (64 experts of 384 rows:
+// 310 against 268).
 template <typename OutT>
 static hipError_t gemm_f8_t(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                             const F8Rows& fr, int64_t E, int N, int K, OutT* y, hipStream_t st) {
   const int64_t rows = fr.offsets ? (fr.R + E - 1) / E : fr.R;   // of one weight matrix
-  // 4 consecutive outputs as one store where every row is aligned to it
-  const int vec = N % 4 == 0 && (uintptr_t)y % (4 * sizeof(OutT)) == 0;
-  if (rows <= 16) {
-    launch_f8_stream<1, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  } else if (rows <= 32) {
-    launch_f8_stream<2, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  } else if (rows <= 64) {
-    launch_f8_stream<4, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  // how wide a store every row of y is aligned to: 2: 16 bytes (and a tile's
+  // rows within reach of 32-bit offsets), 1: 4 outputs
+  const int vec = (uintptr_t)y % 16 == 0 && N * sizeof(OutT) % 16 == 0 && N <= (1 << 20) ? 2
+                  : (uintptr_t)y % (4 * sizeof(OutT)) == 0 && N % 4 == 0 ? 1 : 0;
+  auto tiles = [&](int64_t s) { return (rows + s - 1) / s * ((N + s - 1) / s) * E; };
+  auto rounds = [&](int64_t s, int64_t at_once) { return (tiles(s) + at_once - 1) / at_once; };
+  if (rows <= (fr.offsets ? 8 : 16)) {
+    launch_f8_stream(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  } else if (tiles(128) < 256) {
+    if (tiles(64) > 256) launch_f8_tile<64, 64, 2, 2, 1, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+    else launch_f8_tile<64, 64, 2, 2, 2, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
   } else {
-    const int64_t mid = ((rows + 127) / 128) * ((N + 127) / 128) * E;
-    if (mid >= 256) launch_f8_tile<128, 128, 2, 2, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-    else launch_f8_tile<64, 64, 2, 2, OutT>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+    if constexpr (sizeof(OutT) == 2) {
+      if (!fr.offsets && 8 * rounds(256, 256) < 5 * rounds(128, 512)) {
+        launch_f8_tile<256, 256, 2, 4, 1, 2>(xq, xs, wq, ws, fr, N, K, y, vec, st);
+        return hipGetLastError();
+      }
+    }
+    launch_f8_tile<128, 128, 2, 2, 1, 2>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
   }
   return hipGetLastError();
 }
@@ -580,7 +774,7 @@ static hipError_t gemm_f8_t(const uint8_t* xq, const float* xs, const uint8_t* w
 hipError_t launch_gemm_f8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                           const int32_t* offsets, const int32_t* row_token, int64_t T, int64_t R,
                           int64_t E, int64_t N, int64_t K, void* y, int y_dtype, hipStream_t st) {
-  const F8Rows fr{offsets, row_token, T, (int)R};
+  const F8Rows fr{offsets, row_token, (int)T, (int)R};
   const int n = (int)N, k = (int)K;
   switch (y_dtype) {
     case F32: return gemm_f8_t<float>(xq, xs, wq, ws, fr, E, n, k, (float*)y, st);

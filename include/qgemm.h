@@ -555,7 +555,7 @@ qg_status_t quantize_weight_f8_b128(const void* w, int w_dtype, int64_t E, int64
  * write them, read.
  * y: [M][N] of y_dtype (QG_F32, QG_BF16 or QG_F16), written.
  * The sums over blocks are binary32.  The products of a block are exact and
- * summed in binary32 for QG_F32 outputs and for M <= 64; for QG_BF16 and
+ * summed in binary32 for QG_F32 outputs and for M <= 16; for QG_BF16 and
  * QG_F16 outputs of more rows the 8-bit matrix cores take them 8 at a time
  * and drop, of each product, what lies below 2^-13 of the largest of its 8:
  * a part of at most 7 * 2^-13 of the sum of those largest products, and
@@ -580,7 +580,7 @@ qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t*
  * y:         [R][N]; rows ahead of offsets[0] and from offsets[E] on are left
  *            as they were.
  * 1 <= E <= 1024.  The kernel is chosen by the mean number of rows, R / E:
- * up to 64 the products are exact as for M <= 64 above.
+ * up to 8 the products are exact as for M <= 16 above.
  */
 qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
                                  const float* w_scale, const int32_t* offsets,

@@ -140,11 +140,12 @@ def dense_f64(xq, xs, wq, ws):
     return x @ w.T
 
 
-# stream kernels (rows up to 64, each width of the launch), tile kernels of
-# every size, K and N that end inside a block, single rows and columns
+# the stream kernel (rows up to 16, each width of its launch), every tile size,
+# K and N that end inside a block, single rows and columns, rows of y that are
+# aligned to 16 bytes, to 4 outputs and to neither
 SHAPES = [(1, 1, 16), (1, 4096, 256), (2, 5000, 400), (7, 33, 144), (16, 131, 1376), (16, 9000, 160), (17, 260, 528),
           (31, 12300, 144), (33, 520, 1040), (64, 4100, 272), (50, 13000, 128), (65, 64, 128), (65, 130, 2064), (77, 4100, 288),
-          (128, 128, 256), (200, 2052, 400), (257, 4099, 144), (300, 12288, 272), (1030, 4100, 400), (2049, 4400, 144)]
+          (128, 128, 256), (200, 2052, 400), (257, 4099, 144), (300, 12288, 272), (1030, 4100, 400), (2049, 4400, 144), (2100, 4353, 656), (1024, 11008, 272)]
 
 
 @pytest.mark.parametrize("out", list(DT))
@@ -170,7 +171,7 @@ def test_products_of_random_data(M, N, K, out):
     xq, xs = f8.quantize_f8_g128(x)
     wq, ws = f8.quantize_weight_f8_b128(w)
     y = qg.gemm_f8_b128(f8_dev(xq), to_dev(xs), f8_dev(wq), to_dev(ws), out_dtype=DT[out])
-    check_products(y, f8.gemm_f8_b128(xq, xs, wq, ws), K, out, tile=M > 64)
+    check_products(y, f8.gemm_f8_b128(xq, xs, wq, ws), K, out, tile=M > 16)
 
 
 @pytest.mark.parametrize("M", [1, 40, 100])
@@ -187,7 +188,7 @@ def test_large_and_subnormal_codes(M):
         if out == "f16":
             xs = xs * np.float32(2.0 ** -10)
         y = qg.gemm_f8_b128(f8_dev(xq), to_dev(xs), f8_dev(wq), to_dev(ws), out_dtype=DT[out])
-        check_products(y, f8.gemm_f8_b128(xq, xs, wq, ws), K, out, tile=M > 64)
+        check_products(y, f8.gemm_f8_b128(xq, xs, wq, ws), K, out, tile=M > 16)
 
 
 # ---- one weight matrix for each run of rows -----------------------------------------
