@@ -20,7 +20,7 @@ __device__ __forceinline__ float logit_f32(uint16_t v) { return bf16_bits_to_f32
 // -inf and is never chosen.
 //
 // Binary64 for all of a token's experts costs more than reading them (16384
-// tokens, 256 experts, 8 choices: 105 us against 9 as below), so the wave
+// tokens, 256 experts, 8 choices: 105 us against 13.8 as below), so the wave
 // chooses by binary32 values first and checks that every two neighbours in the
 // order it finds, the first value not chosen among them, are further apart than
 // their errors (or have the same logit and bias, and then the same value in any
@@ -37,15 +37,27 @@ struct RouteArgs {
   float scale;
 };
 
-// The definition: logits x (closed ones -inf) of one token, the largest `top`.
-template <int EPL>
-__device__ __noinline__ void route_exact(const float* xs, float top, const RouteArgs& a,
-                                         double* values, int32_t* expert, float* weight) {
+// A logit as it counts: closed (-inf) for NaN, the largest finite value for +inf.
+template <typename T>
+__device__ __forceinline__ float logit_at(const T* row, int e) {
+  const float v = logit_f32(row[e]);
+  return v > -kInf ? fminf(v, 3.402823466e38f) : -kInf;
+}
+
+// The definition, for one token by a whole wave.
+template <int EPL, typename T>
+__device__ void route_exact(const T* row, const RouteArgs& a, double* values, int32_t* expert,
+                            float* weight) {
   const int lane = threadIdx.x & 63;
   const double ninf = -__builtin_inf();
-  float x[EPL];
+  float x[EPL], top = -kInf;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) x[i] = xs[i];
+  for (int i = 0; i < EPL; ++i) {
+    const int e = 64 * i + lane;
+    x[i] = e < a.E ? logit_at(row, e) : -kInf;
+    top = fmaxf(top, x[i]);
+  }
+  top = wave_max(top);
   double p[EPL], c[EPL];
   if (a.sigmoid) {
 #pragma unroll
@@ -133,69 +145,72 @@ __device__ __forceinline__ int order_key(float v) {
 }
 __device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// Max of integers over a wave: rotations within rows of 16 lanes, then the four
-// rows' values read into scalars.  The result is uniform.
-__device__ __forceinline__ int wave_max_int(int x) {
+// Max over the LPT lanes of a token, in all of them.
+template <int LPT>
+__device__ __forceinline__ int token_max(int x) {
   x = max(x, __builtin_amdgcn_mov_dpp(x, 0x121, 0xF, 0xF, false));   // row_ror:1
   x = max(x, __builtin_amdgcn_mov_dpp(x, 0x122, 0xF, 0xF, false));   // row_ror:2
   x = max(x, __builtin_amdgcn_mov_dpp(x, 0x124, 0xF, 0xF, false));   // row_ror:4
   x = max(x, __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false));   // row_ror:8
-  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
-             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+  if constexpr (LPT == 64)
+    x = max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+            max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+  return x;
 }
 
-// Bound on the binary32 error of a score p = e^d / sum or 1 / (1 + e^-d): the
-// argument of the exponential is off by 2^-23 of itself at most (difference and
-// product with log2 e), the exponential, the sum (a tree over at most 16 + 6
-// values, 2^-24 each) and the quotient by less than 40 * 2^-24 in all.
-__device__ __forceinline__ float score_error(float p, float d) {
-  return p * ((1.5f * fabsf(d) + 20.f) * 0x1p-23f) + 0x1p-120f;
-}
-
-template <int EPL, typename T>
+// LPT lanes a token (16, or 64 where a token needs more registers or choices
+// than 16 lanes have), expert e = LPT i + its lane in register i: the
+// instructions of a choice serve 64 / LPT tokens (16384 tokens, 256 experts:
+// 32 us with 64 lanes, 13.8 with 16).
+template <int LPT, int EPL, typename T>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const T* __restrict__ logits,
                                                             int64_t tokens, RouteArgs a,
                                                             int32_t* __restrict__ expert,
                                                             float* __restrict__ weight) {
-  __shared__ double values[kRouteWaves][64 * EPL];
+  constexpr int TPW = 64 / LPT, EPW = (LPT * EPL + 63) / 64;   // tokens a wave; values a lane of route_exact
+  __shared__ __attribute__((aligned(8))) int values[kRouteWaves][TPW * LPT * EPL > 128 * EPW ? TPW * LPT * EPL : 128 * EPW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= tokens) return;     // no barrier below: the waves are independent
+  const int l = lane % LPT;
+  const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TPW;
+  if (t0 >= tokens) return;    // no barrier below: the waves are independent
+  const int64_t t = t0 + lane / LPT;
+  const bool here = t < tokens;      // (a token past the end takes part, closed)
   const T* row = logits + t * a.E;
-  expert += t * a.k;
-  weight += t * a.k;
 
   float x[EPL];
   int most = kClosed;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = 64 * i + lane;
-    const float v = e < a.E ? logit_f32(row[e]) : -kInf;
-    x[i] = v > -kInf ? fminf(v, 3.402823466e38f) : -kInf;   // NaN is closed
+    const int e = LPT * i + l;
+    x[i] = here && e < a.E ? logit_at(row, e) : -kInf;
     most = max(most, x[i] > -kInf ? order_key(x[i]) : kClosed);
   }
-  most = wave_max_int(most);
-  const float top = most == kClosed ? -kInf : key_value(most);
+  most = token_max<LPT>(most);
+  const float top = most == kClosed ? 0.f : key_value(most);
 
+  // Binary32 values and a bound on their errors.  A score e^d / sum is off by
+  // at most p (1.5 |d| + 20) 2^-23: the argument of the exponential by 2^-23 of
+  // itself (difference and product with log2 e), the exponential, the sum (a
+  // tree over EPL and 6 more, 2^-24 each) and the quotient by less than 40 *
+  // 2^-24; e^d |d| <= 1 / e and p <= 1 / sum make that 21 2^-23 / sum.  A score
+  // 1 / (1 + e^-d) has no sum, and p (1 - p) |d| < 0.3: 4.5 * 2^-23.
   const bool plain = !a.bias && a.groups == 1;
-  auto score = [&](float v, float total) {   // of an open logit
-    return a.sigmoid ? 1.f / (1.f + __expf(-v)) : __expf(v - top) / total;
-  };
   float total = 1.f;
   if (!a.sigmoid && !(plain && a.renormalize)) {
     total = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) total += x[i] > -kInf ? __expf(x[i] - top) : 0.f;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) total += __shfl_xor(total, d, kWave);
+    for (int d = LPT / 2; d >= 1; d >>= 1) total += __shfl_xor(total, d, kWave);
   }
+  const float err = a.sigmoid ? 4.5f * 0x1p-23f : 21.f * 0x1p-23f / fmaxf(total, 1.f);
   int key[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = 64 * i + lane;
+    const int e = LPT * i + l;
     float c = x[i];
     if (!plain && c > -kInf) {
-      c = score(c, total);
+      c = a.sigmoid ? 1.f / (1.f + __expf(-c)) : __expf(c - top) / total;
       if (a.bias) c += a.bias[e];
     }
     key[i] = c > -kInf ? order_key(c) : kClosed;
@@ -203,116 +218,109 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(const T* __restrict_
 
   bool sure = true;
   if (a.groups > 1) {
-    // lane g < groups: the sum of its group's two largest values, and a bound
-    // on the sum's error: that of a score of 1 at the far end of the logits
+    // lane l < groups of a token: the sum of its group's two largest values
     const int size = a.E / a.groups;
-    int* v = reinterpret_cast<int*>(values[wave]);
+    int* v = values[wave] + lane / LPT * (LPT * EPL);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[64 * i + lane] = key[i];
+    for (int i = 0; i < EPL; ++i) v[LPT * i + l] = key[i];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     int u = kClosed, w = kClosed;
-    if (lane < a.groups) {
+    if (l < a.groups) {
       // each lane starts at another place of its group: fewer bank conflicts
-      int at = lane % size;
+      int at = l % size;
       for (int i = 0; i < size; ++i) {
-        const int o = v[lane * size + at];
+        const int o = v[l * size + at];
         w = max(w, min(u, o));
         u = max(u, o);
         at = at + 1 == size ? 0 : at + 1;
       }
     }
     float value = u == kClosed ? -kInf : key_value(u);
-    float off = u == kClosed ? 0.f : fabsf(value) * 0x1p-22f;
-    if (w != kClosed) {
-      const float second = key_value(w);
-      off += fabsf(second) * 0x1p-22f;
+    // a value is off by its score's error and a rounding, the sum by another
+    float off = 2.f * err;
+    if (u != kClosed) {
+      const float second = w == kClosed ? 0.f : key_value(w);
+      off += (fabsf(value) + fabsf(second)) * 0x1p-22f;
       value += second;
     }
-    // p (1.5 |d| + 20) 2^-23 is at most 1.5 / e + 20 of 2^-23 for each of the two
-    off += 2.f * 21.f * 0x1p-23f;
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), g));
-      rank += o > value || (o == value && g < lane);
+      const float o = __shfl(value, lane - l + g, kWave);
+      rank += o > value || (o == value && g < l);
     }
-    const bool in = lane < a.groups && rank < a.top_groups;
-    const uint64_t kept = __ballot(in);
+    const bool in = l < a.groups && rank < a.top_groups;
+    const uint64_t kept = __ballot(in) >> (lane - l);
     // the kept values' lower ends against the others' upper ends; closed groups
     // are last in any arithmetic
-    const int low = wave_max_int(in && value > -kInf ? order_key(off - value) : kClosed);
-    const int high = wave_max_int(lane < a.groups && !in && value > -kInf ? order_key(value + off) : kClosed);
+    const int low = token_max<LPT>(in && value > -kInf ? order_key(off - value) : kClosed);
+    const int high = token_max<LPT>(l < a.groups && !in && value > -kInf ? order_key(value + off) : kClosed);
     if (high != kClosed && !(-key_value(low) > key_value(high))) sure = false;
+    // e / size as a product: e < 2^10 and the factor is less than one too large
+    const u32 by = ((1u << 20) + size - 1) / size;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = 64 * i + lane;
-      if (e < a.E && !((kept >> (e / size)) & 1)) key[i] = kClosed;
+      const int e = LPT * i + l;
+      if (!(e < a.E && ((kept >> ((e * by) >> 20)) & 1))) key[i] = kClosed;
     }
   }
 
-  // k times the largest value that is left, and once more to see how near the
-  // first value not chosen is; lane j keeps choice j
-  int chosen = -1, before = kClosed, before_e = 0, count = 0;
-  float cx = 0.f, before_x = 0.f;
-  for (int s = 0; s <= a.k && sure; ++s) {
-    int best = key[0];
+  // k times the largest value that is left, the lowest expert of equal ones,
+  // and once more to see how near the first value not chosen is; lane j keeps
+  // choice j
+  int chosen = -1, before = kClosed, before_e = 0;
+  for (int s = 0; s <= a.k; ++s) {
+    int m = key[0];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
-    best = wave_max_int(best);
-    if (best == kClosed) break;
-    int e = -1;
-    float v = 0.f;
+    for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
+    const int best = token_max<LPT>(m);
+    if (!__any(best != kClosed)) break;
+    int e = kRouteMaxExperts;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const uint64_t who = __ballot(key[i] == best);
-      if (e < 0 && who) {
-        const int l = __builtin_ctzll(who);
-        e = 64 * i + l;
-        v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x[i]), l));
-        if (lane == l) key[i] = kClosed;
-      }
-    }
-    if (s > 0) {
+    for (int i = EPL - 1; i >= 0; --i) e = key[i] == best ? LPT * i + l : e;
+    e = -token_max<LPT>(-e);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = e - l == LPT * i ? kClosed : key[i];
+    if (s > 0 && best != kClosed) {
       const float hi = key_value(before), lo = key_value(best), gap = hi - lo;
       bool apart;
-      if (plain) {
+      if (plain)
         // scores rise with the logits: apart in binary64 unless the logits are
         // within a few of its steps, or the scores round to 0 or 1
         apart = a.sigmoid ? gap * __expf(-fmaxf(hi, 0.f)) > 0x1p-44f && lo > -600.f
                           : gap > 0x1p-44f && lo - top > -600.f;
-      } else {
-        const float pa = score(before_x, total), pb = score(v, total);
-        const float da = a.sigmoid ? before_x : before_x - top, db = a.sigmoid ? v : v - top;
-        apart = gap > score_error(pa, da) + score_error(pb, db) + (fabsf(hi) + fabsf(lo)) * 0x1p-22f;
-      }
-      if (!apart) sure = v == before_x && (!a.bias || a.bias[e] == a.bias[before_e]);
+      else
+        apart = gap > 2.f * err + (fabsf(hi) + fabsf(lo)) * 0x1p-22f;
+      if (!apart)
+        sure = sure && logit_at(row, e) == logit_at(row, before_e) && (!a.bias || a.bias[e] == a.bias[before_e]);
     }
     before = best;
     before_e = e;
-    before_x = v;
-    if (s < a.k) {
-      if (lane == s) chosen = e, cx = v;
-      ++count;
-    }
+    if (l == s && s < a.k && best != kClosed) chosen = e;
   }
-  if (!sure) {
-    route_exact<EPL>(x, top, a, values[wave], expert, weight);
-    return;
-  }
+
   // The chosen scores in binary64 (one a lane).  Renormalised softmax needs no
   // sum over the other experts.
   double mine = 0.0;
-  if (lane < count) mine = a.sigmoid ? 1.0 / (1.0 + exp(-(double)cx)) : exp((double)cx - (double)top);
+  if (chosen >= 0) {
+    const double d = (double)logit_at(row, chosen);
+    mine = a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - (double)top);
+  }
   if (a.renormalize) {
     double sum = mine;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+    for (int d = LPT / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
     mine = sum > 0.0 ? mine / sum : 0.0;
-  } else if (!a.sigmoid) {
-    mine = lane < count ? mine / (double)total : 0.0;   // (no expert open: no sum)
+  } else if (!a.sigmoid && chosen >= 0) {
+    mine /= (double)total;
   }
-  if (lane < a.k) {
-    expert[lane] = chosen;
-    weight[lane] = (float)(mine * (double)a.scale);
+  if (here && l < a.k) {
+    expert[t * a.k + l] = chosen;
+    weight[t * a.k + l] = (float)(mine * (double)a.scale);
+  }
+  // tokens whose order the binary32 values leave open
+  for (uint64_t open = __ballot(here && !sure && l == 0); open; open &= open - 1) {
+    const int64_t o = t0 + __builtin_ctzll(open) / LPT;
+    route_exact<EPW>(logits + o * a.E, a, reinterpret_cast<double*>(values[wave]), expert + o * a.k, weight + o * a.k);
   }
 }
 
@@ -320,15 +328,21 @@ template <typename T>
 static hipError_t route_t(const T* logits, const float* bias, int64_t tokens, int E, int groups,
                           int top_groups, int k, int sigmoid, int renormalize, float scale,
                           int32_t* expert, float* weight, hipStream_t st) {
-  const dim3 grid((unsigned)((tokens + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   const RouteArgs a{bias, E, groups, top_groups, k, sigmoid, renormalize, scale};
-#define QG_ROUTE(EPL) k_route<EPL, T><<<grid, block, 0, st>>>(logits, tokens, a, expert, weight)
-  if (E <= 64) QG_ROUTE(1);
-  else if (E <= 128) QG_ROUTE(2);
-  else if (E <= 256) QG_ROUTE(4);
-  else if (E <= 512) QG_ROUTE(8);
-  else QG_ROUTE(16);
-#undef QG_ROUTE
+  auto go = [&](auto kernel, int tokens_per_wave) {
+    const int64_t per = kRouteWaves * tokens_per_wave;
+    kernel<<<dim3((unsigned)((tokens + per - 1) / per)), dim3(64 * kRouteWaves), 0, st>>>(logits, tokens, a, expert, weight);
+  };
+  if (E <= 256 && k <= 16 && groups <= 16) {
+    if (E <= 16) go(k_route<16, 1, T>, 4);
+    else if (E <= 64) go(k_route<16, 4, T>, 4);
+    else if (E <= 128) go(k_route<16, 8, T>, 4);
+    else go(k_route<16, 16, T>, 4);
+  } else {
+    if (E <= 256) go(k_route<64, 4, T>, 1);
+    else if (E <= 512) go(k_route<64, 8, T>, 1);
+    else go(k_route<64, 16, T>, 1);
+  }
   return hipGetLastError();
 }
 
@@ -345,49 +359,59 @@ hipError_t launch_route(const void* logits, int dtype, const float* bias, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Plan: a stable sort of the choices by expert in one launch without
-// workspace or atomics.  Workgroup e reads all choices twice: once to count
-// those of lower experts (where its rows start) and its own in each wave's
-// run, once to place its own in order.  Workgroup E does the same for the
-// entries that are no expert.
+// Plan: a stable sort of the choices by expert in one launch, without
+// workspace; counts are integers, so their order does not matter, and places
+// follow from counts and lane order alone.
+//
+// Few choices (up to 4096): workgroup e reads them all, counts those of lower
+// experts (where its rows start) and its own, and places its own in order.
+// Workgroup E does the same for the entries that are no expert.
 // ---------------------------------------------------------------------------
-constexpr int kPlanWaves = 8;
-
-__global__ __launch_bounds__(64 * kPlanWaves) void k_plan(const int32_t* __restrict__ expert,
-                                                          int n, int k, int E, int vec,
-                                                          int32_t* __restrict__ offsets,
-                                                          int32_t* __restrict__ row_token,
-                                                          int32_t* __restrict__ slot) {
-  __shared__ int below[kPlanWaves], own[kPlanWaves];
+template <int WAVES, int kPlanBatch>
+__global__ __launch_bounds__(64 * WAVES) void k_plan(const int32_t* __restrict__ expert, int n,
+                                                     int k, int E, int vec,
+                                                     int32_t* __restrict__ offsets,
+                                                     int32_t* __restrict__ row_token,
+                                                     int32_t* __restrict__ slot) {
+  __shared__ int below[WAVES], own[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const u32 me = blockIdx.x;   // E: entries outside 0 .. E-1
-  // four consecutive entries a lane; every wave a contiguous run of them
-  const int steps = (n + 255) / 256, per = (steps + kPlanWaves - 1) / kPlanWaves;
+  // four consecutive entries a lane; every wave a contiguous run of at most
+  // kPlanBatch steps, whose loads are all issued before the first is used
+  const int steps = (n + 255) / 256, per = (steps + WAVES - 1) / WAVES;
   const int s0 = wave * per, s1 = min(s0 + per, steps);
-  auto fetch = [&](int s, u32 (&id)[4]) {
-    const int at = s * 256 + 4 * lane;
-    if (vec && at + 4 <= n) {
-      const v4i v = ld16(expert + at);
+  struct Batch {
+    u32 id[kPlanBatch][4];     // past n: no one's (0xffffffff)
+  };
+  auto fetch = [&](int b, Batch& v) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) id[q] = (u32)v[q] < (u32)E ? (u32)v[q] : (u32)E;
-    } else {
+    for (int q = 0; q < kPlanBatch; ++q) {
+      const int at = (b + q) * 256 + 4 * lane;
+      if (vec && b + q < s1 && at + 4 <= n) {
+        const v4i w = ld16(expert + at);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const u32 v = at + q < n ? (u32)expert[at + q] : 0xffffffffu;
-        id[q] = at + q < n ? (v < (u32)E ? v : (u32)E) : 0xffffffffu;
+        for (int c = 0; c < 4; ++c) v.id[q][c] = (u32)w[c];
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v.id[q][c] = b + q < s1 && at + c < n ? (u32)expert[at + c] : 0xffffffffu;
       }
     }
-  };
-  int less = 0, mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    u32 id[4];
-    fetch(s, id);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      less += id[q] < me;
-      mine += id[q] == me;
+    for (int q = 0; q < kPlanBatch; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v.id[q][c] = b + q < s1 && (b + q) * 256 + 4 * lane + c < n ? min(v.id[q][c], (u32)E) : 0xffffffffu;
+  };
+  Batch v;
+  int less = 0, mine = 0;
+  fetch(s0, v);
+#pragma unroll
+  for (int q = 0; q < kPlanBatch; ++q)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      less += v.id[q][c] < me;
+      mine += v.id[q][c] == me;
     }
-  }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
     less += __shfl_xor(less, d, kWave);
@@ -396,39 +420,147 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_plan(const int32_t* __restr
   if (lane == 0) below[wave] = less, own[wave] = mine;
   __syncthreads();
   int start = 0, pos = 0;
-  for (int w = 0; w < kPlanWaves; ++w) {
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
     start += below[w];
     pos += w < wave ? own[w] : 0;
   }
   pos += start;
   if (threadIdx.x == 0) offsets[me] = start;
   const uint64_t before = (1ull << lane) - 1;
-  for (int s = s0; s < s1; ++s) {
-    u32 id[4];
-    fetch(s, id);
+#pragma unroll
+  for (int q = 0; q < kPlanBatch; ++q) {
+    uint64_t who[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) who[c] = __ballot(v.id[q][c] == me);
+    if (!(who[0] | who[1] | who[2] | who[3])) continue;
     int ahead = 0, all = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t b = __ballot(id[q] == me);
-      ahead += __popcll(b & before);
-      all += __popcll(b);
+    for (int c = 0; c < 4; ++c) {
+      ahead += __popcll(who[c] & before);
+      all += __popcll(who[c]);
     }
-    if (all == 0) continue;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (id[q] == me) {
-        const int at = s * 256 + 4 * lane + q, to = pos + ahead++;
+    for (int c = 0; c < 4; ++c)
+      if (v.id[q][c] == me) {
+        const int at = (s0 + q) * 256 + 4 * lane + c, to = pos + ahead++;
         slot[at] = me < (u32)E ? to : -1;
-        row_token[to] = me < (u32)E ? at / k : -1;
+        row_token[to] = me < (u32)E ? (int)((u32)at / (u32)k) : -1;
       }
     pos += all;
   }
 }
 
+// Many choices: workgroup s owns segment s, 1024 R of them, and counts all
+// choices by expert in LDS, those ahead of its segment apart.  A wave's 64 R
+// choices of the segment are ranked among equals by ballots over the bits of
+// the expert; the counts of the waves before it and of all segments before
+// give the row.  Slots leave as whole lines from one XCD and the rows of an
+// expert in runs (a workgroup for each expert, scattering its slots over lines
+// that other XCDs write too: 45 us for 131072 choices of 256 experts, 14.5
+// so).
+constexpr int kPlanWaves = 16;
+constexpr int kPlanBuckets = kRouteMaxExperts + 1;   // the last: no expert
+
+template <int R>
+__global__ __launch_bounds__(64 * kPlanWaves) void k_plan_segments(
+    const int32_t* __restrict__ expert, int n, int k, int E, int vec,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_token, int32_t* __restrict__ slot) {
+  __shared__ int ahead[kPlanBuckets], rest[kPlanBuckets], base[kPlanWaves][kPlanBuckets];
+  __shared__ int sums[kPlanWaves];
+  constexpr int kThreads = 64 * kPlanWaves;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // consecutive segments on one XCD, so that the runs they write meet in its L2
+  const int per = gridDim.x / 8, rem = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int64_t seg = (int64_t)(xcd * per + min(xcd, rem) + (int)blockIdx.x / 8) * (kThreads * R);
+  for (int e = tid; e <= E; e += kThreads) {
+    ahead[e] = rest[e] = 0;
+    for (int w = 0; w < kPlanWaves; ++w) base[w][e] = 0;
+  }
+  __syncthreads();
+  auto bucket = [&](int id) { return (u32)id < (u32)E ? id : E; };
+  // segments start at multiples of 4, so four consecutive entries lie on one
+  // side of seg
+  for (int64_t at = 4 * tid; at < n; at += 4 * kThreads) {
+    int* const to = at < seg ? ahead : rest;
+    if (vec && at + 4 <= n) {
+      const v4i v = ld16(expert + at);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) atomicAdd(&to[bucket(v[c])], 1);
+    } else {
+      for (int c = 0; c < 4 && at + c < n; ++c) atomicAdd(&to[bucket(expert[at + c])], 1);
+    }
+  }
+  // ranks of this wave's choices among its own of the same expert
+  int id[R], rank[R];
+  const int bits = 32 - __builtin_clz((u32)E);       // of 0 .. E
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t at = seg + (wave * R + r) * 64 + lane;
+    const bool in = at < n;
+    id[r] = in ? bucket(expert[at]) : 0;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot((id[r] >> b) & 1);
+      same &= (id[r] >> b) & 1 ? one : ~one;
+    }
+    const int mine = __popcll(same & ((1ull << lane) - 1));
+    // one wave's LDS accesses execute in order
+    rank[r] = in ? base[wave][id[r]] + mine : -1;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (in && mine == 0) base[wave][id[r]] += __popcll(same);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  __syncthreads();
+  // rows of each bucket: a scan over the totals; a thread has one bucket, and
+  // the last thread the one past 1023 too
+  const int total = tid <= E ? ahead[tid] + rest[tid] : 0;
+  int run = total;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int t = __shfl_up(run, d, kWave);
+    if (lane >= d) run += t;
+  }
+  if (lane == 63) sums[wave] = run;
+  __syncthreads();
+  int start = run - total;
+  for (int w = 0; w < wave; ++w) start += sums[w];
+  auto spread = [&](int e, int from) {
+    if (blockIdx.x == 0) offsets[e] = from;
+    from += ahead[e];
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int c = base[w][e];
+      base[w][e] = from;
+      from += c;
+    }
+  };
+  if (tid <= E) spread(tid, start);
+  if (tid == kThreads - 1 && E == kThreads) spread(E, start + total);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (rank[r] < 0) continue;
+    const int at = (int)(seg + (wave * R + r) * 64 + lane), to = base[wave][id[r]] + rank[r];
+    slot[at] = id[r] < E ? to : -1;
+    row_token[to] = id[r] < E ? (int)((u32)at / (u32)k) : -1;
+  }
+}
+
 hipError_t launch_plan(const int32_t* expert, int64_t T, int64_t k, int64_t E, int32_t* offsets,
                        int32_t* row_token, int32_t* slot, hipStream_t st) {
-  k_plan<<<dim3((unsigned)(E + 1)), dim3(64 * kPlanWaves), 0, st>>>(
-      expert, (int)(T * k), (int)k, (int)E, (uintptr_t)expert % 16 == 0, offsets, row_token, slot);
+  const int n = (int)(T * k), vec = (uintptr_t)expert % 16 == 0;
+  if (n <= 4096) {
+    const dim3 grid((unsigned)(E + 1)), block(256);
+    if (n <= 1024) k_plan<4, 1><<<grid, block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
+    else k_plan<4, 4><<<grid, block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
+  } else {
+    // every workgroup reads all choices: longer segments where there are many
+    const dim3 block(64 * kPlanWaves);
+    if (n <= 131072)
+      k_plan_segments<2><<<dim3((unsigned)((n + 2047) / 2048)), block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
+    else
+      k_plan_segments<16><<<dim3((unsigned)((n + 16383) / 16384)), block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
+  }
   return hipGetLastError();
 }
 

@@ -89,7 +89,8 @@ def test_route_decides_near_ties_in_binary64(E, groups, top):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 8, 8), (16, 6, 64), (37, 7, 33), (511, 8, 256), (512, 1, 1024),
-                                   (3000, 8, 60), (70, 64, 500)])
+                                   (3000, 8, 60), (70, 64, 500), (1025, 4, 1024), (513, 8, 7), (2049, 2, 1023),
+                                   (20000, 7, 256), (16385, 9, 1024)])
 def test_plan(T, k, E):
     rng = np.random.default_rng(T + k + E)
     for kind in range(3):
