@@ -590,11 +590,12 @@ def _call_on(device: torch.device, name: str, *args) -> None:
     """_call on `device`'s current stream, with `device` current.  (The stream's
     handle without a Stream object around it: 0.1 us a call instead of 1.9.)"""
     index = device.index
-    if index == torch.cuda.current_device():
-        _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
-    else:
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+            return _call_on(device, name, *args)
+    rc = getattr(_lib or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != 0:
+        raise RuntimeError(f"{name}: {status_string(rc)}")
 
 
 def quantize_f8_g128(x: torch.Tensor, out=None):

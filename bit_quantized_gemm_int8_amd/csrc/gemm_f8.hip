@@ -240,9 +240,14 @@ template <typename OutT>
 static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* wq,
                              const float* ws, const F8Rows& fr, int64_t E, int N, int K, OutT* y,
                              int vec, hipStream_t st) {
+  // Blocks of 16 weight rows: one a workgroup with its K in 8 parts while that
+  // gives every CU at most one (1 x 11008 x 4096: 12.5 us, two blocks in 4
+  // parts 15.6, four in 2 23.5), two up to 600 blocks, four beyond, which stage
+  // the token rows less often (8 x 4096 x 11008, 688 blocks: 12.0, two a workgroup
+  // 13.7; 96 rows over 64 experts of 4096 x 2752: 90.7 against 95.8).
   const int64_t blocks = E * ((N + 15) / 16);
   if (blocks <= 256) launch_f8_stream_nb<1, 8>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  else if (blocks <= 768) launch_f8_stream_nb<2, 4>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  else if (blocks <= 600) launch_f8_stream_nb<2, 4>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
   else launch_f8_stream_nb<4, 2>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
 }
 
