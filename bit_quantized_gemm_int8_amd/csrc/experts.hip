@@ -599,10 +599,10 @@ __global__ __launch_bounds__(kCombineThreads) void k_combine(
   if constexpr (VEC) {
     ovec o;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = Out<OutT>::cvt(acc[i]);
+    for (int i = 0; i < V; ++i) o[i] = round_to<OutT>(acc[i]);
     *reinterpret_cast<ovec*>(y + t * N + n) = o;
   } else {
-    y[t * N + n] = Out<OutT>::cvt(acc[0]);
+    y[t * N + n] = round_to<OutT>(acc[0]);
   }
 }
 

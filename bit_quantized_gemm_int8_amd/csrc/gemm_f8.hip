@@ -207,12 +207,12 @@ __global__ __launch_bounds__(64 * NB * KS) void k_f8_stream(
       OutT* dst = y + (int64_t)m * N + n;
       if (vec && n + 4 <= N) {
         typedef OutT o4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<o4*>(dst) = o4{Out<OutT>::cvt(acc[0]), Out<OutT>::cvt(acc[1]),
-                                         Out<OutT>::cvt(acc[2]), Out<OutT>::cvt(acc[3])};
+        *reinterpret_cast<o4*>(dst) = o4{round_to<OutT>(acc[0]), round_to<OutT>(acc[1]),
+                                         round_to<OutT>(acc[2]), round_to<OutT>(acc[3])};
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (n + i < N) dst[i] = Out<OutT>::cvt(acc[i]);
+          if (n + i < N) dst[i] = round_to<OutT>(acc[i]);
       }
     }
     // the next run of rows overwrites phase buffers and partial sums that
@@ -478,13 +478,15 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
   static_assert(kUnder + (EXPERTS ? kStores : 0) <= 63, "vmcnt counts to 63");
   static_assert(NW * 32 * IP * RB <= kRegion, "a region of LDS for each wave");
   auto four = [&](int i, int jj, int q) {
-    return o4{Out<OutT>::cvt(acc[i][jj][4 * q]), Out<OutT>::cvt(acc[i][jj][4 * q + 1]),
-              Out<OutT>::cvt(acc[i][jj][4 * q + 2]), Out<OutT>::cvt(acc[i][jj][4 * q + 3])};
+    return o4{round_to<OutT>(acc[i][jj][4 * q]), round_to<OutT>(acc[i][jj][4 * q + 1]),
+              round_to<OutT>(acc[i][jj][4 * q + 2]), round_to<OutT>(acc[i][jj][4 * q + 3])};
   };
   auto store_lines = [&](const F8Tile& at, int8_t* region) {
     int8_t* reg = region + wave * (32 * IP * RB);
     // rows past the run and columns past N go out of the resource's range:
-    // every store is issued, so their number is known to the next wait
+    // every store is issued, so their number is known to the next wait.
+    // Non-temporal: outputs would push operands out of L2 (4096 x 4096 x 11008:
+    // 188 us with the default policy, 176 so)
     const rsrc_t yr = make_rsrc_uniform(y + (int64_t)at.m0 * N, (u32)((at.hi - at.m0 < BM ? at.hi - at.m0 : BM) * N * E));
 #pragma unroll
     for (int ps = 0; ps < MI / IP * (NJ / JP); ++ps) {
@@ -506,7 +508,7 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
         const int row = it * (64 / CH) + lane / CH, ch = lane % CH;
         const int n = at.n0 + row_b + 32 * jp + ch * (16 / E);
         const v4i v = ld16(reg + row * RB + ((ch ^ (row & (CH - 1))) << 4));
-        __builtin_amdgcn_raw_buffer_store_b128(v, yr, n < N ? (u32)(((row_a + 32 * ip + row) * N + n) * E) : kOOB, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v, yr, n < N ? (u32)(((row_a + 32 * ip + row) * N + n) * E) : kOOB, 0, kAuxNonTemporal);
       }
       asm volatile("" ::: "memory");
     }
@@ -527,7 +529,7 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
           } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-              if (n + t < N) dst[t] = Out<OutT>::cvt(acc[i][jj][4 * q + t]);
+              if (n + t < N) dst[t] = round_to<OutT>(acc[i][jj][4 * q + t]);
           }
         }
     }
@@ -745,10 +747,10 @@ static void launch_f8_tile(const uint8_t* xq, const float* xs, const uint8_t* wq
 //  * 256 x 256 tiles, 16-bit outputs of one matrix, where their rounds (one
 //    workgroup on a CU) cost less than those of 128 x 128 (two on a CU, a round
 //    5/8 as long): 4096 x 4096 x 11008 187 against 225, 1024 x 4096 x 11008 57
-//    against 64, but 2048 x 4096 x 4096 53 against 40.
-// Of the two groups of products, binary32 outputs take more registers than a
-// 256 x 256 tile leaves; experts' rows seldom fill one (64 experts of 384 rows:
-// 310 against 268).
+//    against 64, but 2048 x 4096 x 4096 53 against 40 (before the stores went
+//    past L2, which took 6% off both).
+// Binary32 outputs take more registers than a 256 x 256 tile leaves, and
+// experts' rows seldom fill one (64 experts of 384 rows: 310 against 268).
 template <typename OutT>
 static hipError_t gemm_f8_t(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                             const F8Rows& fr, int64_t E, int N, int K, OutT* y, hipStream_t st) {

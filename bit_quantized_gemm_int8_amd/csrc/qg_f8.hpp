@@ -38,4 +38,15 @@ __device__ __forceinline__ v8h f8_to_f16x8(int lo, int hi) {
   return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Outputs, rounded to nearest even.  bfloat16 by the conversion instruction,
+// which keeps every NaN a NaN.
+template <typename OutT>
+__device__ __forceinline__ OutT round_to(float v) {
+  return (OutT)v;
+}
+template <>
+__device__ __forceinline__ uint16_t round_to<uint16_t>(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
 }  // namespace qg

@@ -98,6 +98,11 @@ def test_infinities_and_nan_reach_their_outputs_only(M):
     for out in (torch.float32, torch.bfloat16):
         y = qg.gemm_f8_b128(q, s, f8_dev(wq), to_dev(ws), out_dtype=out)
         assert y[:2].isnan().all() and y[2:].isfinite().all()
+    # a NaN of any payload stays one in 16-bit outputs
+    xs = s.clone()
+    xs[0, 1] = torch.tensor([0x7fffffff], dtype=torch.int32).view(torch.float32)[0]
+    for out in (torch.float16, torch.bfloat16):
+        assert qg.gemm_f8_b128(q, xs, f8_dev(wq), to_dev(ws), out_dtype=out)[:2].isnan().all()
     w[5, 7] = np.nan
     wq, ws = qg.quantize_weight_f8_b128(to_dev(w))
     wo, wso = f8.quantize_weight_f8_b128(w)
