@@ -5,7 +5,9 @@
  *   - per-token dynamic symmetric int8 activations,
  *   - per-output-channel symmetric int8 weights (W8A8), or
  *   - group-wise (128 along K) asymmetric uint4 weights dequantized inside the
- *     GEMM, with int8 activations (W4A8) or 16-bit float activations (W4A16).
+ *     GEMM, with int8 activations (W4A8) or 16-bit float activations (W4A16),
+ *   - or 8-bit float (e4m3) codes of both with a scale for each block of 128,
+ *     alone or with a weight matrix for each run of rows (routed experts).
  *
  * Sources, cited by page title and section:
  *   「第4章：量化」: §1.1 x_int = round(x/s) + z and x_hat = (x_int - z) s;
