@@ -9,9 +9,11 @@
 //  * stream (few rows for each weight matrix): bound by the weight bytes.
 //    16 weight rows per wave read as whole lines (qg_decode.hpp), the codes
 //    widened to binary16 in registers (exact) for the 16-bit matrix cores.
-//  * tile (many rows): bound by the matrix cores.  Stages of 128 k, one scale
-//    block, come into LDS by DMA.  The matrix core's sum over a stage starts
-//    at zero and is scaled into binary32 accumulators.
+//  * tile (many rows): bound by the way from L2 into LDS (copies without the
+//    matrix instructions take as long, without the loads 4096 x 4096 x 11008
+//    takes 153 us of 197).  Stages of 128 k, one scale block, come by DMA.  The
+//    matrix core's sum over a stage starts at zero and is scaled into binary32
+//    accumulators.
 //
 // What the matrix cores add up.  A product of two e4m3 codes has 8
 // significant bits.  The 16-bit matrix instructions keep them all and sum in
@@ -255,8 +257,8 @@ static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* 
 // Tile kernel: BM x BN outputs per workgroup of WM x WN waves, each wave
 // 32 MI x 32 NJ outputs of 32x32 matrix instructions.  A stage is the 128 k
 // of one scale block: BM token rows and BN weight rows of 128 bytes, and the
-// BM token scales, all by buffer-to-LDS DMA into one of two stage buffers
-// while the other is multiplied.  Chunks are XOR-swizzled as in the int8 tile
+// scales, all by buffer-to-LDS DMA into a ring of NB buffers, NB - 1 stages
+// ahead of the products.  Chunks are XOR-swizzled as in the int8 tile
 // kernel: row r's chunk c at slot c ^ ((r >> 1) & 7), so that 16 rows reading
 // one chunk hit 16 different bank groups.
 //
