@@ -267,10 +267,23 @@ static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* 
 // ---------------------------------------------------------------------------
 constexpr int kF8Stage = 128;   // bytes of a row in a stage = one scale block
 
-// Token rows, weight rows, token scales in runs of 64, and the weight scales of
-// the tile's column blocks.
+// Scales come SG stages at a time, SG of them for each token row and then for
+// each column block of the tile (a run of 64 lanes): a row's scales of one stage
+// are 4 bytes of a line, and a request for them costs L2 as much as one for 128
+// bytes of codes, a third of all requests with SG = 1.  4 for 128 x 128 tiles
+// (24576 rows over 64 experts of 4096 x 2752: 405 us, 422 with 1; 1024 x 4096 x
+// 4096: 28.5, 30.9).  A 256 x 256 tile has no registers left for it (4096 x 4096
+// x 11008: 221 us, 181 with 1), and rings deeper than two stages count loads.
+template <int BM>
+constexpr int f8_scale_stages(int NB) { return NB == 2 && BM <= 128 ? 4 : 1; }
+// LDS of a group of waves: NB buffers of token and weight rows, then the ring
+// of scales (two blocks of SG stages, or one for each stage).
 template <int BM, int BN>
-constexpr int f8_stage_bytes() { return (BM + BN) * kF8Stage + 4 * BM + 256; }
+constexpr int f8_rows_bytes() { return (BM + BN) * kF8Stage; }
+template <int BM>
+constexpr int f8_scales_bytes(int NB) { return f8_scale_stages<BM>(NB) * (4 * BM + 256); }
+template <int BM, int BN, int NB>
+constexpr int f8_ring_bytes() { return NB * (f8_rows_bytes<BM, BN>() + f8_scales_bytes<BM>(NB)); }
 
 // Direct loads into LDS, 16 and 4 bytes a lane at lds (wave-uniform) + 16 or
 // 4 lane, at byte voff + soff of the resource; out of range reads zeros.
@@ -293,7 +306,8 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
                                          const float* __restrict__ ws, const F8Rows& fr, int N,
                                          int K, OutT* __restrict__ y, int vec, Next next_tile) {
   constexpr int NW = WM * WN, MI = BM / WM / 32, NJ = BN / WN / 32;
-  constexpr int kStage = f8_stage_bytes<BM, BN>();
+  constexpr int kStage = f8_rows_bytes<BM, BN>(), SG = f8_scale_stages<BM>(NB), kScales = f8_scales_bytes<BM>(NB);
+  static_assert(SG == 1 || KS == 1, "blocks of scales are counted in stages");
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;      // 1 KB loads of 8 rows, of each wave
   static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && BM < 64 * NW && BM % 64 == 0,
                 "whole loads per wave");
@@ -302,7 +316,8 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
   // out of a ring of its own, and the sums meet at the end
   const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * NW));
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % NW);
-  int8_t* const lds = lds0 + kg * (NB * kStage);
+  int8_t* const lds = lds0 + kg * f8_ring_bytes<BM, BN, NB>();
+  int8_t* const slds = lds + NB * kStage;
   const int wm = wave / WN, wn = wave % WN;
   const int row_a = wm * 32 * MI, row_b = wn * 32 * NJ;
   const int G = (K + kF8Block - 1) / kF8Block, B = (N + kF8Block - 1) / kF8Block;
@@ -375,8 +390,10 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
     } else if (i < LA + LB) {
       const int q = wave * LB + i - LA;
       f8_dma16(br, buf + BM * kF8Stage + q * 1024, in.row[LB % 2 ? q & 1 : (i - LA) & 1] ? offb[i - LA] : kOOB, g * kF8Stage);
-    } else {
-      f8_dma4(sr, buf + (BM + BN) * kF8Stage + min(wave, BM / 64) * 256, in.scale ? offs : kOOB, 4 * g);
+    } else if constexpr (SG == 1) {
+      f8_dma4(sr, slds + (buf - lds) / kStage * kScales + min(wave, BM / 64) * 256, in.scale ? offs : kOOB, 4 * g);
+    } else if (g % SG == 0) {
+      f8_dma16(sr, slds + (g / SG & 1) * kScales + min(wave, BM / 64) * (64 * 4 * SG), in.scale ? offs : kOOB, 4 * g);
     }
   };
   constexpr int kLoads = LA + LB + 1;
@@ -414,11 +431,11 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
     frag(buf + row_a * kF8Stage, af[0]);
 #pragma unroll
     for (int jj = 0; jj < NJ; ++jj) frag(buf + BM * kF8Stage + (row_b + 32 * jj) * kF8Stage, bf[jj]);
-    const float* sc = reinterpret_cast<const float*>(buf + (BM + BN) * kF8Stage);
+    const float* sc = reinterpret_cast<const float*>(slds + (SG == 1 ? (int)(buf - lds) / kStage : g / SG & 1) * kScales) + g % SG;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sx[i] = sc[row_a + 32 * i + l31];
+    for (int i = 0; i < MI; ++i) sx[i] = sc[SG * (row_a + 32 * i + l31)];
     const StageIn in = stage_in(g + KS * (NB - 1));
-    const float sw = sc[BM + row_b / kF8Block];
+    const float sw = sc[SG * (BM + row_b / kF8Block)];
     constexpr int kEvery = (kLoads + kSteps - 1) / kSteps;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -589,7 +606,7 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
       constexpr int kSums = 4096;     // 16 sums of 64 lanes
       static_assert(NW * MI * NJ * kSums <= kStage, "a wave's sums in its ring's free buffer");
       auto part = [&](int k, int i, int jj, int c) {
-        int8_t* free = buffer(b + NB - 1) + (k - kg) * (NB * kStage);
+        int8_t* free = buffer(b + NB - 1) + (k - kg) * f8_ring_bytes<BM, BN, NB>();
         return free + ((wave * MI + i) * NJ + jj) * kSums + c * 1024 + 16 * lane;
       };
 #pragma unroll
@@ -631,7 +648,7 @@ template <int BM, int BN, int WM, int WN, int KS, int NB, bool EXACT, typename O
 __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, F8Rows fr, int N, int K, OutT* __restrict__ y, int vec) {
-  __shared__ __attribute__((aligned(16))) int8_t lds[KS * NB * f8_stage_bytes<BM, BN>()];
+  __shared__ __attribute__((aligned(16))) int8_t lds[KS * f8_ring_bytes<BM, BN, NB>()];
   const int M = fr.R;
   // Consecutive workgroups go to the 8 XCDs in turn: renumber so that each
   // XCD walks a contiguous run of tiles, in column-major groups of 4 tile
@@ -659,9 +676,9 @@ template <int BM, int BN, int WM, int WN, int KS, int NB, bool EXACT, typename O
 __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, F8Rows fr, int E, int N, int K, OutT* __restrict__ y, int vec) {
-  __shared__ __attribute__((aligned(16))) int8_t lds[KS * NB * f8_stage_bytes<BM, BN>()];
-  // tile rows ahead of each expert, and its rows
-  __shared__ int first[kF8MaxExperts + 1], low[kF8MaxExperts], high[kF8MaxExperts];
+  __shared__ __attribute__((aligned(16))) int8_t lds[KS * f8_ring_bytes<BM, BN, NB>()];
+  // tile rows ahead of each expert, and its number of rows
+  __shared__ int first[kF8MaxExperts + 1], count[kF8MaxExperts];
   const int tiles_n = (N + BN - 1) / BN;
   if (threadIdx.x < kWave) {
     // each lane counts a run of experts, the lanes' sums are scanned; offsets
@@ -672,8 +689,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
     for (int e = e0; e < min(e0 + per, E); ++e) {
       int lo, hi;
       f8_expert_rows(fr, e, lo, hi);
-      low[e] = lo;
-      high[e] = hi;
+      count[e] = hi - lo;
       sum += (hi - lo + BM - 1) / BM;
     }
     int64_t run = sum;
@@ -685,7 +701,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
     run -= sum;
     for (int e = e0; e < min(e0 + per, E); ++e) {
       first[e] = (int)min(run, most);
-      run += (high[e] - low[e] + BM - 1) / BM;
+      run += (count[e] + BM - 1) / BM;
     }
     if (threadIdx.x == kWave - 1) first[E] = (int)min(run, most);
   }
@@ -710,7 +726,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
       else b = mid - 1;
     }
     a = __builtin_amdgcn_readfirstlane(a);
-    const int lo = __builtin_amdgcn_readfirstlane(low[a]), hi = __builtin_amdgcn_readfirstlane(high[a]);
+    const int lo = min(max(fr.offsets[a], 0), fr.R), hi = lo + __builtin_amdgcn_readfirstlane(count[a]);
     const int in = t - __builtin_amdgcn_readfirstlane(first[a]) * tiles_n, rows = (hi - lo + BM - 1) / BM;
     to = F8Tile{a, lo + in % rows * BM, hi, in / rows * BN};
     t += gridDim.x / 8;
@@ -733,7 +749,7 @@ static void launch_f8_tile(const uint8_t* xq, const float* xs, const uint8_t* wq
   if (!fr.offsets)
     return launch_f8_tile<BM, BN, WM, WN, KS, NB>(xq, xs, wq, ws, fr, N, K, y, vec, st);
   // as many workgroups as can be resident, a multiple of the 8 XCDs
-  constexpr int kLds = KS * NB * f8_stage_bytes<BM, BN>() + 12 * kF8MaxExperts + 4;
+  constexpr int kLds = KS * f8_ring_bytes<BM, BN, NB>() + 8 * kF8MaxExperts + 4;
   const int64_t most = (((int64_t)fr.R + BM - 1) / BM + E) * ((N + BN - 1) / BN);
   const int64_t grid = std::min<int64_t>(256 * (int64_t)(kLdsBytesPerCU / kLds), (most + 7) / 8 * 8);
   k_f8_tile_experts<BM, BN, WM, WN, KS, NB, std::is_same<OutT, float>::value, OutT>
