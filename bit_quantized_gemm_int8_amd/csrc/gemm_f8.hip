@@ -32,6 +32,7 @@
 
 #include "qg_decode.hpp"
 #include "qg_f8.hpp"
+#include "qg_f8_index.hpp"
 #include "qg_launch.hpp"
 
 namespace qg {
@@ -352,10 +353,9 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
   auto aim = [&](const F8Tile& at, const Rows& r) {
     // Token rows come from one resource: of this tile's rows where they follow
     // each other, else of all of xq (whose size the host keeps under 2 GiB).
-    // (Never 0 rows long: a scalar offset past a resource's size is not in its
-    // range check; a row that does not exist has an offset past any size.)
+    // (A row that does not exist has a vector offset past any size.)
     const int row0 = gather ? 0 : at.m0;
-    const int rows_x = max(gather ? fr.T : min(BM, min(at.hi, fr.T) - at.m0), 1);
+    const int rows_x = gather ? fr.T : min(BM, at.hi - at.m0);
     ar = make_rsrc_uniform(xq + (int64_t)row0 * K, (u32)(rows_x * K));
     br = make_rsrc_uniform(wq + ((int64_t)at.e * N + at.n0) * K, (u32)(min(BN, N - at.n0) * K));
 #pragma unroll
@@ -390,10 +390,10 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
     } else if (i < LA + LB) {
       const int q = wave * LB + i - LA;
       f8_dma16(br, buf + BM * kF8Stage + q * 1024, in.row[LB % 2 ? q & 1 : (i - LA) & 1] ? offb[i - LA] : kOOB, g * kF8Stage);
-    } else if constexpr (SG == 1) {
-      f8_dma4(sr, slds + (buf - lds) / kStage * kScales + min(wave, BM / 64) * 256, in.scale ? offs : kOOB, 4 * g);
     } else if (g % SG == 0) {
-      f8_dma16(sr, slds + (g / SG & 1) * kScales + min(wave, BM / 64) * (64 * 4 * SG), in.scale ? offs : kOOB, 4 * g);
+      const F8ScaleLoad at = f8_scale_load(in.scale ? offs : kOOB, g, SG);
+      if constexpr (SG == 1) f8_dma4(sr, slds + (buf - lds) / kStage * kScales + min(wave, BM / 64) * 256, at.voffset, at.soffset);
+      else f8_dma16(sr, slds + (g / SG & 1) * kScales + min(wave, BM / 64) * (64 * 4 * SG), at.voffset, at.soffset);
     }
   };
   constexpr int kLoads = LA + LB + 1;

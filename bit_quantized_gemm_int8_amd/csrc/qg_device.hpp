@@ -41,6 +41,13 @@ __device__ __forceinline__ int sum_lanes8(int t) {
 // A buffer resource covers [base, base + bytes); a load whose offset lies past
 // the end returns zeros instead of touching memory, so edge tiles and masked
 // lanes need no branch: they pass kOOB (or any offset >= bytes).
+// The check takes each dword of a load by itself, at vector plus scalar offset,
+// in more than 32 bits (seen on MI355X with loads to registers and to LDS of 4
+// and 16 bytes, scalar offsets below, at and past the size, sizes down to 0; all
+// addresses inside one allocation).  The compiler's description leaves the
+// scalar offset out of the check, so code that needs the check on its own
+// account uses the vector offset; the int8 tile kernel counts on the scalar
+// offset for rows past the last one.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr u32 kOOB = 0x80000000u;
 constexpr int kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit data format

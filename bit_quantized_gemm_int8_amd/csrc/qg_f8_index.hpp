@@ -1,0 +1,22 @@
+// Index arithmetic of the e4m3 tile kernels, in plain C++ so that it can be
+// walked on the host (tests/test_f8_index.py).
+#pragma once
+
+#include <cstdint>
+
+namespace qg {
+
+// A lane's load of the scales of stages g .. g + stages - 1 (g < G, in rows of G
+// scales) for the row at byte `row` of the resource; an offset past any size
+// for a lane without a row.  Of several stages the last ones may lie past the
+// row: in the last row that is past the array, so their place goes into the
+// vector offset, which every reading of the range check counts, dword by dword.
+struct F8ScaleLoad {
+  uint32_t voffset;
+  int soffset;
+};
+constexpr F8ScaleLoad f8_scale_load(uint32_t row, int g, int stages) {
+  return stages == 1 ? F8ScaleLoad{row, 4 * g} : F8ScaleLoad{row + 4 * (uint32_t)g, 0};
+}
+
+}  // namespace qg
