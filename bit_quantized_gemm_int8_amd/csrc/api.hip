@@ -465,11 +465,11 @@ qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const 
                                  int64_t N, int64_t K, void* y, int y_dtype, void* stream) {
   if (qg_status_t s = check_f8_dims(R, N, K)) return s;
   if (T < 0 || T > kMaxF8Dim || E < 1 || E > kMaxExperts) return QG_ERR_SHAPE;
-  if (row_token ? T * K > kMaxDim : T != R) return QG_ERR_SHAPE;
+  if (row_token ? T * K > kMaxDim : R > 0 && T != R) return QG_ERR_SHAPE;
   if (!fits_grid(E * ((N + 15) / 16), 512)) return QG_ERR_SHAPE;
   if (!is_float_dtype(y_dtype)) return QG_ERR_DTYPE;
   if (R == 0 || N == 0) return QG_OK;
-  if (!xq || !x_scale || !wq || !w_scale || !offsets || !y) return QG_ERR_NULL;
+  if ((T > 0 && (!xq || !x_scale)) || !wq || !w_scale || !offsets || !y) return QG_ERR_NULL;
   if (!aligned16(xq) || !aligned16(wq) || !aligned4(x_scale) || !aligned4(w_scale) ||
       !aligned4(offsets) || !aligned4(row_token) || !aligned_to(y, y_dtype))
     return QG_ERR_ALIGN;

@@ -572,12 +572,13 @@ qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t*
  * experts of a routed layer), in one launch:
  *   for e < E and offsets[e] <= r < offsets[e+1], with t = row_token[r] (or
  *   t = r where row_token is NULL):  y[r] = x_t . W_e as in gemm_f8_b128.
- * xq [T][K], x_scale [T][G]; wq [E][N][K], w_scale [E][B][G]: read.
+ * xq [T][K], x_scale [T][G] (NULL where T is 0: no row has a token then); wq
+ * [E][N][K], w_scale [E][B][G]: read.
  * offsets:   [E + 1] int32, rising, offsets[E] <= R: read on the GPU.  Values
  *            outside 0 .. R are clamped to it, and a run that ends below its
  *            start is empty; in a row that two runs name each element is
  *            either's.
- * row_token: [R] int32 or NULL (then T must equal R): read.  A row whose
+ * row_token: [R] int32 or NULL (then T must equal R, unless R is 0): read.  A row whose
  *            token is outside 0 .. T-1 is written as zeros.  T * K < 2^31.
  * y:         [R][N]; rows ahead of offsets[0] and from offsets[E] on are left
  *            as they were.
