@@ -683,7 +683,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
   if (threadIdx.x < kWave) {
     // each lane counts a run of experts, the lanes' sums are scanned; offsets
     // that do not rise can name rows many times over, so the count saturates
-    const int64_t most = 0x7fffffff / tiles_n;
+    const int64_t most = f8_most_tile_rows(tiles_n, gridDim.x);
     const int per = (E + kWave - 1) / kWave, e0 = threadIdx.x * per;
     int64_t sum = 0;
     for (int e = e0; e < min(e0 + per, E); ++e) {

@@ -19,4 +19,8 @@ constexpr F8ScaleLoad f8_scale_load(uint32_t row, int g, int stages) {
   return stages == 1 ? F8ScaleLoad{row, 4 * g} : F8ScaleLoad{row + 4 * (uint32_t)g, 0};
 }
 
+// Most tile rows that the experts' joint list holds: `grid` workgroups step
+// through rows * tiles_n places in 31 bits, each up to grid / 8 + 1 past the end.
+constexpr int f8_most_tile_rows(int tiles_n, int grid) { return (INT32_MAX - grid) / tiles_n; }
+
 }  // namespace qg

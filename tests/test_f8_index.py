@@ -12,7 +12,7 @@ CSRC = os.path.join(ROOT, "bit_quantized_gemm_int8_amd", "csrc")
 def run_host(tmp_path, body):
     """Output of a C++ program that includes the header."""
     src, exe = tmp_path / "walk.cpp", tmp_path / "walk"
-    src.write_text('#include <cstdio>\n#include "qg_f8_index.hpp"\nusing namespace qg;\nint main() {\n' + body + "\n}\n")
+    src.write_text('#include <cstdio>\n#include <initializer_list>\n#include "qg_f8_index.hpp"\nusing namespace qg;\nint main() {\n' + body + "\n}\n")
     subprocess.run(["g++", "-std=c++17", "-O1", "-I", CSRC, str(src), "-o", str(exe)], check=True, capture_output=True, text=True)
     return subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
 
@@ -48,3 +48,19 @@ def test_scale_loads_stay_inside_by_their_vector_offset(tmp_path):
 def test_the_walk_sees_a_stage_in_the_scalar_offset(tmp_path):
     past, lost = run_host(tmp_path, WALK % f"(F8ScaleLoad{{{ROW}, 4 * g}})").split()
     assert int(past) > 0 and int(lost) == 0
+
+
+def test_places_in_the_tile_list_never_pass_31_bits(tmp_path):
+    """The list of the experts' tiles saturates (offsets that do not rise can
+    name rows many times over), and a workgroup that steps past its end still
+    holds a positive place."""
+    out = run_host(tmp_path, """
+  long bad = 0;
+  for (int tiles_n : {1, 2, 3, 7, 64, 1000, 8388608, 16777216})
+    for (int grid : {8, 16, 256, 512, 1024}) {
+      const int64_t end = (int64_t)f8_most_tile_rows(tiles_n, grid) * tiles_n;
+      bad += end < 1 || end + grid / 8 + 1 > INT32_MAX || end + grid + tiles_n < INT32_MAX;
+    }
+  printf("%ld", bad);
+""")
+    assert out == "0"
