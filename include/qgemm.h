@@ -600,6 +600,7 @@ qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const 
  *   expert[t] = the k experts of largest c, in falling order;
  *   weight[t,j] = scale * p[t, expert[t,j]], divided by the sum of the k
  *   chosen p first if renormalize is 1 (p unbiased; a sum of 0 gives 0).
+ *   p and the weights are binary64, rounded once.
  * The comparisons take c in binary64 whatever the type of the logits; equal
  * values go to the lowest expert (group).
  * A logit of -inf or NaN closes the expert for that token (softmax leaves it
