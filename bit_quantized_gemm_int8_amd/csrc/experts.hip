@@ -463,20 +463,23 @@ __global__ __launch_bounds__(64 * WAVES) void k_plan(const int32_t* __restrict__
   }
 }
 
-// Many choices: workgroup s owns segment s, 1024 R of them, and counts all
-// choices by expert in LDS, those ahead of its segment apart.  A wave's 64 R
-// choices of the segment are ranked among equals by ballots over the bits of
-// the expert; the counts of the waves before it and of all segments before
-// give the row.  Slots leave as whole lines from one XCD and the rows of an
-// expert in runs (a workgroup for each expert, scattering its slots over lines
-// that other XCDs write too: 45 us for 131072 choices of 256 experts, 14.5
-// so).
+// Many choices: a workgroup owns a segment of `chunks` chunks of 1024 R of them,
+// and counts all choices by expert in LDS, those ahead of its segment apart.
+// A wave's 64 R choices of a chunk are ranked among equals by ballots over the
+// bits of the expert; the counts of the waves before it, of the chunks and of
+// the segments before give the row.  Slots leave as whole lines from one XCD
+// and the rows of an expert in runs (a workgroup for each expert, scattering
+// its slots over lines that other XCDs write too: 45 us for 131072 choices of
+// 256 experts, 14.5 so).  Every workgroup reads all choices, so there are at
+// most as many as CUs, and the time grows with the choices (2^20: 112 us, 2^22:
+// 0.46 ms, 2^25: 4.0 ms; a workgroup for each chunk: 27.8 ms).
 constexpr int kPlanWaves = 16;
 constexpr int kPlanBuckets = kRouteMaxExperts + 1;   // the last: no expert
+constexpr int64_t kPlanSegments = 256;
 
 template <int R>
 __global__ __launch_bounds__(64 * kPlanWaves) void k_plan_segments(
-    const int32_t* __restrict__ expert, int n, int k, int E, int vec,
+    const int32_t* __restrict__ expert, int n, int k, int E, int chunks, int vec,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_token, int32_t* __restrict__ slot) {
   __shared__ int ahead[kPlanBuckets], rest[kPlanBuckets], base[kPlanWaves][kPlanBuckets];
   __shared__ int sums[kPlanWaves];
@@ -484,11 +487,13 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_plan_segments(
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // consecutive segments on one XCD, so that the runs they write meet in its L2
   const int per = gridDim.x / 8, rem = gridDim.x % 8, xcd = blockIdx.x % 8;
-  const int64_t seg = (int64_t)(xcd * per + min(xcd, rem) + (int)blockIdx.x / 8) * (kThreads * R);
-  for (int e = tid; e <= E; e += kThreads) {
-    ahead[e] = rest[e] = 0;
-    for (int w = 0; w < kPlanWaves; ++w) base[w][e] = 0;
-  }
+  const int64_t seg = (int64_t)(xcd * per + min(xcd, rem) + (int)blockIdx.x / 8) * chunks * (kThreads * R);
+  auto clear_base = [&] {
+    for (int e = tid; e <= E; e += kThreads)
+      for (int w = 0; w < kPlanWaves; ++w) base[w][e] = 0;
+  };
+  for (int e = tid; e <= E; e += kThreads) ahead[e] = rest[e] = 0;
+  clear_base();
   __syncthreads();
   auto bucket = [&](int id) { return (u32)id < (u32)E ? id : E; };
   // segments start at multiples of 4, so four consecutive entries lie on one
@@ -503,58 +508,76 @@ __global__ __launch_bounds__(64 * kPlanWaves) void k_plan_segments(
       for (int c = 0; c < 4 && at + c < n; ++c) atomicAdd(&to[bucket(expert[at + c])], 1);
     }
   }
-  // ranks of this wave's choices among its own of the same expert
-  int id[R], rank[R];
   const int bits = 32 - __builtin_clz((u32)E);       // of 0 .. E
+  int64_t first = seg;                               // of the chunk
+  for (int chunk = 0;;) {
+    // ranks of this wave's choices among its own of the same expert
+    int id[R], rank[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t at = seg + (wave * R + r) * 64 + lane;
-    const bool in = at < n;
-    id[r] = in ? bucket(expert[at]) : 0;
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t one = __ballot((id[r] >> b) & 1);
-      same &= (id[r] >> b) & 1 ? one : ~one;
+    for (int r = 0; r < R; ++r) {
+      const int64_t at = first + (wave * R + r) * 64 + lane;
+      const bool in = at < n;
+      id[r] = in ? bucket(expert[at]) : 0;
+      uint64_t same = __ballot(in);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t one = __ballot((id[r] >> b) & 1);
+        same &= (id[r] >> b) & 1 ? one : ~one;
+      }
+      const int mine = __popcll(same & ((1ull << lane) - 1));
+      // one wave's LDS accesses execute in order
+      rank[r] = in ? base[wave][id[r]] + mine : -1;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (in && mine == 0) base[wave][id[r]] += __popcll(same);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    const int mine = __popcll(same & ((1ull << lane) - 1));
-    // one wave's LDS accesses execute in order
-    rank[r] = in ? base[wave][id[r]] + mine : -1;
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (in && mine == 0) base[wave][id[r]] += __popcll(same);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
-  __syncthreads();
-  // rows of each bucket: a scan over the totals; a thread has one bucket, and
-  // the last thread the one past 1023 too
-  const int total = tid <= E ? ahead[tid] + rest[tid] : 0;
-  int run = total;
+    __syncthreads();
+    if (chunk == 0) {
+      // ahead becomes the first row of the segment's choices of each bucket: a
+      // scan over the totals; a thread has one bucket, and the last thread the
+      // one past 1023 too
+      const int total = tid <= E ? ahead[tid] + rest[tid] : 0;
+      int run = total;
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int t = __shfl_up(run, d, kWave);
-    if (lane >= d) run += t;
-  }
-  if (lane == 63) sums[wave] = run;
-  __syncthreads();
-  int start = run - total;
-  for (int w = 0; w < wave; ++w) start += sums[w];
-  auto spread = [&](int e, int from) {
-    if (blockIdx.x == 0) offsets[e] = from;
-    from += ahead[e];
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = base[w][e];
-      base[w][e] = from;
-      from += c;
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int t = __shfl_up(run, d, kWave);
+        if (lane >= d) run += t;
+      }
+      if (lane == 63) sums[wave] = run;
+      __syncthreads();
+      int start = run - total;
+      for (int w = 0; w < wave; ++w) start += sums[w];
+      auto begin = [&](int e, int from) {
+        if (blockIdx.x == 0) offsets[e] = from;
+        ahead[e] += from;
+      };
+      if (tid <= E) begin(tid, start);
+      if (tid == kThreads - 1 && E == kThreads) begin(E, start + total);
     }
-  };
-  if (tid <= E) spread(tid, start);
-  if (tid == kThreads - 1 && E == kThreads) spread(E, start + total);
-  __syncthreads();
+    // (a bucket's thread is the same here and above)
+    auto spread = [&](int e) {
+      int from = ahead[e];
+      for (int w = 0; w < kPlanWaves; ++w) {
+        const int c = base[w][e];
+        base[w][e] = from;
+        from += c;
+      }
+      ahead[e] = from;
+    };
+    if (tid <= E) spread(tid);
+    if (tid == kThreads - 1 && E == kThreads) spread(E);
+    __syncthreads();
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (rank[r] < 0) continue;
-    const int at = (int)(seg + (wave * R + r) * 64 + lane), to = base[wave][id[r]] + rank[r];
-    slot[at] = id[r] < E ? to : -1;
-    row_token[to] = id[r] < E ? (int)((u32)at / (u32)k) : -1;
+    for (int r = 0; r < R; ++r) {
+      if (rank[r] < 0) continue;
+      const int at = (int)(first + (wave * R + r) * 64 + lane), to = base[wave][id[r]] + rank[r];
+      slot[at] = id[r] < E ? to : -1;
+      row_token[to] = id[r] < E ? (int)((u32)at / (u32)k) : -1;
+    }
+    first += kThreads * R;
+    if (++chunk == chunks || first >= n) break;      // alike for the whole workgroup
+    __syncthreads();
+    clear_base();
+    __syncthreads();
   }
 }
 
@@ -568,10 +591,12 @@ hipError_t launch_plan(const int32_t* expert, int64_t T, int64_t k, int64_t E, i
   } else {
     // every workgroup reads all choices: longer segments where there are many
     const dim3 block(64 * kPlanWaves);
-    if (n <= 131072)
-      k_plan_segments<2><<<dim3((unsigned)((n + 2047) / 2048)), block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
-    else
-      k_plan_segments<16><<<dim3((unsigned)((n + 16383) / 16384)), block, 0, st>>>(expert, n, (int)k, (int)E, vec, offsets, row_token, slot);
+    if (n <= 131072) {
+      k_plan_segments<2><<<dim3((unsigned)((n + 2047) / 2048)), block, 0, st>>>(expert, n, (int)k, (int)E, 1, vec, offsets, row_token, slot);
+    } else {
+      const int64_t all = (n + (int64_t)16383) / 16384, chunks = (all + kPlanSegments - 1) / kPlanSegments;
+      k_plan_segments<16><<<dim3((unsigned)((all + chunks - 1) / chunks)), block, 0, st>>>(expert, n, (int)k, (int)E, (int)chunks, vec, offsets, row_token, slot);
+    }
   }
   return hipGetLastError();
 }
