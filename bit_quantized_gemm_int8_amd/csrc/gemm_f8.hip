@@ -756,48 +756,21 @@ static void launch_f8_tile(const uint8_t* xq, const float* xs, const uint8_t* wq
       <<<dim3((unsigned)grid), dim3(64 * WM * WN * KS), 0, st>>>(xq, xs, wq, ws, fr, (int)E, N, K, y, vec);
 }
 
-// Kernel by the rows of one weight matrix (of the mean expert) and the number
-// of tiles, measured on MI355X (us):
-//  * the stream kernel up to 16 rows (16 x 11008 x 4096: 15.5, tiles 21.6; it
-//    loses from 17 rows on wide layers, 17 x 4096 x 11008: 15.6, tiles 10.8, and
-//    gains 1.4 on 17 x 4096 x 4096), with experts up to a mean of 8, since an
-//    expert with more than 16 rows reads its weights again (16 experts of 1376 x
-//    4096, mean 16: 37.7, tiles 20.4; mean 8: 22.4 both);
-//  * 64 x 64 tiles, two groups of waves sharing K, while one round of
-//    workgroups holds them all (200 x 4096 x 4096: 11.2, one group 12.7), one
-//    group beyond (128 x 4096 x 11008: 17.9, two groups 20.7);
-//  * 128 x 128 tiles from 256 of them on (512 x 4096 x 11008: 32.6, 64 x 64 tiles
-//    48.5);
-//  * 256 x 256 tiles, 16-bit outputs of one matrix, where their rounds (one
-//    workgroup on a CU) cost less than those of 128 x 128 (two on a CU, a round
-//    5/8 as long): 4096 x 4096 x 11008 187 against 225, 1024 x 4096 x 11008 57
-//    against 64, but 2048 x 4096 x 4096 53 against 40 (before the stores went
-//    past L2, which took 6% off both).
-// Binary32 outputs take more registers than a 256 x 256 tile leaves, and
-// experts' rows seldom fill one (64 experts of 384 rows: 310 against 268).
 template <typename OutT>
 static hipError_t gemm_f8_t(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                             const F8Rows& fr, int64_t E, int N, int K, OutT* y, hipStream_t st) {
-  const int64_t rows = fr.offsets ? (fr.R + E - 1) / E : fr.R;   // of one weight matrix
   // how wide a store every row of y is aligned to: 2: 16 bytes (and a tile's
   // rows within reach of 32-bit offsets), 1: 4 outputs
   const int vec = (uintptr_t)y % 16 == 0 && N * sizeof(OutT) % 16 == 0 && N <= (1 << 20) ? 2
                   : (uintptr_t)y % (4 * sizeof(OutT)) == 0 && N % 4 == 0 ? 1 : 0;
-  auto tiles = [&](int64_t s) { return (rows + s - 1) / s * ((N + s - 1) / s) * E; };
-  auto rounds = [&](int64_t s, int64_t at_once) { return (tiles(s) + at_once - 1) / at_once; };
-  if (rows <= (fr.offsets ? 8 : 16)) {
-    launch_f8_stream(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  } else if (tiles(128) < 256) {
-    if (tiles(64) > 256) launch_f8_tile<64, 64, 2, 2, 1, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-    else launch_f8_tile<64, 64, 2, 2, 2, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
-  } else {
-    if constexpr (sizeof(OutT) == 2) {
-      if (!fr.offsets && 8 * rounds(256, 256) < 5 * rounds(128, 512)) {
-        launch_f8_tile<256, 256, 2, 4, 1, 2>(xq, xs, wq, ws, fr, N, K, y, vec, st);
-        return hipGetLastError();
-      }
-    }
-    launch_f8_tile<128, 128, 2, 2, 1, 2>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
+  switch (f8_kernel(fr.offsets != nullptr, fr.R, E, N, sizeof(OutT) > 2)) {
+    case F8Kernel::kStream: launch_f8_stream(xq, xs, wq, ws, fr, E, N, K, y, vec, st); break;
+    case F8Kernel::kTile64TwoGroups: launch_f8_tile<64, 64, 2, 2, 2, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st); break;
+    case F8Kernel::kTile64: launch_f8_tile<64, 64, 2, 2, 1, 3>(xq, xs, wq, ws, fr, E, N, K, y, vec, st); break;
+    case F8Kernel::kTile128: launch_f8_tile<128, 128, 2, 2, 1, 2>(xq, xs, wq, ws, fr, E, N, K, y, vec, st); break;
+    case F8Kernel::kTile256:
+      if constexpr (sizeof(OutT) == 2) launch_f8_tile<256, 256, 2, 4, 1, 2>(xq, xs, wq, ws, fr, N, K, y, vec, st);
+      break;
   }
   return hipGetLastError();
 }

@@ -1,5 +1,5 @@
-// Index arithmetic of the e4m3 tile kernels, in plain C++ so that it can be
-// walked on the host (tests/test_f8_index.py).
+// Index arithmetic and kernel choice of the e4m3 products, in plain C++ so that
+// they can be walked on the host (tests/test_f8_index.py, tests/f8_choice.py).
 #pragma once
 
 #include <cstdint>
@@ -22,5 +22,35 @@ constexpr F8ScaleLoad f8_scale_load(uint32_t row, int g, int stages) {
 // Most tile rows that the experts' joint list holds: `grid` workgroups step
 // through rows * tiles_n places in 31 bits, each up to grid / 8 + 1 past the end.
 constexpr int f8_most_tile_rows(int tiles_n, int grid) { return (INT32_MAX - grid) / tiles_n; }
+
+// Kernel by the rows of one weight matrix (of the mean expert) and the number
+// of tiles, measured on MI355X (us):
+//  * the stream kernel up to 16 rows (16 x 11008 x 4096: 15.5, tiles 21.6; it
+//    loses from 17 rows on wide layers, 17 x 4096 x 11008: 15.6, tiles 10.8, and
+//    gains 1.4 on 17 x 4096 x 4096), with experts up to a mean of 8, since an
+//    expert with more than 16 rows reads its weights again (16 experts of 1376 x
+//    4096, mean 16: 37.7, tiles 20.4; mean 8: 22.4 both);
+//  * 64 x 64 tiles, two groups of waves sharing K, while one round of
+//    workgroups holds them all (200 x 4096 x 4096: 11.2, one group 12.7), one
+//    group beyond (128 x 4096 x 11008: 17.9, two groups 20.7);
+//  * 128 x 128 tiles from 256 of them on (512 x 4096 x 11008: 32.6, 64 x 64 tiles
+//    48.5);
+//  * 256 x 256 tiles, 16-bit outputs of one matrix, where their rounds (one
+//    workgroup on a CU) cost less than those of 128 x 128 (two on a CU, a round
+//    5/8 as long): 4096 x 4096 x 11008 187 against 225, 1024 x 4096 x 11008 57
+//    against 64, but 2048 x 4096 x 4096 53 against 40 (before the stores went
+//    past L2, which took 6% off both).
+// Binary32 outputs take more registers than a 256 x 256 tile leaves, and
+// experts' rows seldom fill one (64 experts of 384 rows: 310 against 268).
+enum class F8Kernel { kStream, kTile64TwoGroups, kTile64, kTile128, kTile256 };
+constexpr F8Kernel f8_kernel(bool experts, int64_t R, int64_t E, int64_t N, bool wide_out) {
+  const int64_t rows = (R + E - 1) / E;   // of one weight matrix
+  auto tiles = [&](int64_t s) { return (rows + s - 1) / s * ((N + s - 1) / s) * E; };
+  auto rounds = [&](int64_t s, int64_t at_once) { return (tiles(s) + at_once - 1) / at_once; };
+  if (rows <= (experts ? 8 : 16)) return F8Kernel::kStream;
+  if (tiles(128) < 256) return tiles(64) > 256 ? F8Kernel::kTile64 : F8Kernel::kTile64TwoGroups;
+  if (!wide_out && !experts && 8 * rounds(256, 256) < 5 * rounds(128, 512)) return F8Kernel::kTile256;
+  return F8Kernel::kTile128;
+}
 
 }  // namespace qg
