@@ -9,9 +9,11 @@
 //  * stream (few rows for each weight matrix): bound by the weight bytes.
 //    16 weight rows per wave read as whole lines (qg_decode.hpp), the codes
 //    widened to binary16 in registers (exact) for the 16-bit matrix cores.
-//  * tile (many rows): bound by the way from L2 into LDS (copies without the
-//    matrix instructions take as long, without the loads 4096 x 4096 x 11008
-//    takes 153 us of 197).  Stages of 128 k, one scale block, come by DMA.  The
+//  * tile (many rows): bound by the way from L2 into LDS and by the matrix
+//    cores together on 256 x 256 tiles (4096 x 4096 x 11008: 184 us, a copy
+//    without the loads of later stages 144, one without the matrix instructions
+//    144), by the former on 128 x 128 (24576 rows over 64 experts of 1376 x 4096:
+//    258 us, 147 and 241).  Stages of 128 k, one scale block, come by DMA.  The
 //    matrix core's sum over a stage starts at zero and is scaled into binary32
 //    accumulators.
 //
@@ -244,10 +246,10 @@ static void launch_f8_stream(const uint8_t* xq, const float* xs, const uint8_t* 
                              const float* ws, const F8Rows& fr, int64_t E, int N, int K, OutT* y,
                              int vec, hipStream_t st) {
   // Blocks of 16 weight rows: one a workgroup with its K in 8 parts while that
-  // gives every CU at most one (1 x 11008 x 4096: 12.5 us, two blocks in 4
-  // parts 15.6, four in 2 23.5), two up to 600 blocks, four beyond, which stage
-  // the token rows less often (8 x 4096 x 11008, 688 blocks: 12.0, two a workgroup
-  // 13.7; 96 rows over 64 experts of 4096 x 2752: 90.7 against 95.8).
+  // gives every CU at most one (1 x 11008 x 4096: 12.8 us, two blocks in 4
+  // parts 15.5, four in 2 23.6), two up to 600 blocks, four beyond, which stage
+  // the token rows less often (8 x 4096 x 11008, 688 blocks: 12.2, two a workgroup
+  // 13.8; 96 rows over 64 experts of 4096 x 2752: 91.2 against 96.8).
   const int64_t blocks = E * ((N + 15) / 16);
   if (blocks <= 256) launch_f8_stream_nb<1, 8>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
   else if (blocks <= 600) launch_f8_stream_nb<2, 4>(xq, xs, wq, ws, fr, E, N, K, y, vec, st);
@@ -271,10 +273,15 @@ constexpr int kF8Stage = 128;   // bytes of a row in a stage = one scale block
 // Scales come SG stages at a time, SG of them for each token row and then for
 // each column block of the tile (a run of 64 lanes): a row's scales of one stage
 // are 4 bytes of a line, and a request for them costs L2 as much as one for 128
-// bytes of codes, a third of all requests with SG = 1.  4 for 128 x 128 tiles
-// (24576 rows over 64 experts of 4096 x 2752: 405 us, 422 with 1; 1024 x 4096 x
-// 4096: 28.5, 30.9).  A 256 x 256 tile has no registers left for it (4096 x 4096
-// x 11008: 221 us, 181 with 1), and rings deeper than two stages count loads.
+// bytes of codes, a third of all requests with SG = 1.  4 for 128 x 128 tiles:
+// 24576 rows over 64 experts of 4096 x 2752 417 us, 444 with 1; 1024 x 4096 x
+// 4096 28.3, 30.5; of 31 plain shapes of 256 .. 512 tiles those of K = 11008 take
+// 7% less on average and none takes more, those of K = 4096 between 7% less and
+// 11% more (768 x 4096 x 5504: 33.4, 30.0; 512 x 4096 x 11008: 35.4, 32.5), as
+// much on average; shapes of equal tile counts and widths lie on both sides, so
+// no rule on sizes divides them.  A 256 x 256 tile has no registers left for it
+// (4096 x 4096 x 11008: 221 us, 181 with 1), and rings deeper than two stages
+// count loads.
 template <int BM>
 constexpr int f8_scale_stages(int NB) { return NB == 2 && BM <= 128 ? 4 : 1; }
 // LDS of a group of waves: NB buffers of token and weight rows, then the ring
@@ -485,7 +492,7 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
   // would touch 32 rows with 16 bytes each, so where rows of y are 16-byte
   // aligned (vec 2) the outputs are turned in LDS, JP column blocks (up to 128
   // bytes of a row) at a time, and leave as 16-byte chunks of consecutive lanes
-  // (4096 x 4096 x 11008: 211 us with the direct stores, 197 so).
+  // (4096 x 4096 x 11008: 212 us with the direct stores, 184 so).
   typedef OutT o4 __attribute__((ext_vector_type(4)));
   constexpr int E = (int)sizeof(OutT);
   constexpr int kRegion = (EXPERTS || KS > 1 ? 1 : NB) * kStage;   // experts: the others hold the next tile's loads
@@ -505,7 +512,7 @@ __device__ __forceinline__ void f8_tiles(int8_t* lds0, const uint8_t* __restrict
     // rows past the run and columns past N go out of the resource's range:
     // every store is issued, so their number is known to the next wait.
     // Non-temporal: outputs would push operands out of L2 (4096 x 4096 x 11008:
-    // 188 us with the default policy, 176 so)
+    // 202 us with the default policy, 184 so)
     const rsrc_t yr = make_rsrc_uniform(y + (int64_t)at.m0 * N, (u32)((at.hi - at.m0 < BM ? at.hi - at.m0 : BM) * N * E));
 #pragma unroll
     for (int ps = 0; ps < MI / IP * (NJ / JP); ++ps) {
@@ -711,9 +718,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_f8_tile_experts(
   const int begin = xcd * per + min(xcd, rem), end = begin + per + (xcd < rem);
   // With several tile rows an expert, the two workgroups that share a CU (the
   // first and second half of an XCD's) take neighbours, which read the same
-  // weight rows (64 experts of 384 rows: 255 us, 264 without; with one tile row
+  // weight rows (64 experts of 384 rows: 258 us, 260 without; with one tile row
   // there is nothing to share and the order of the list is better, 16 experts
-  // of 64 rows: 22.6 us against 24).
+  // of 64 rows: 22.3 us against 23.2).
   const int slots = gridDim.x / 8, at = blockIdx.x / 8, half = (slots + 1) / 2;
   int t = begin + (fr.R <= (int64_t)E * BM ? at : at < half ? 2 * at : 2 * (at - half) + 1);
   f8_tiles<BM, BN, WM, WN, KS, NB, EXACT, OutT, true>(lds, xq, xs, wq, ws, fr, N, K, y, vec, [&](F8Tile& to) {

@@ -25,23 +25,25 @@ constexpr int f8_most_tile_rows(int tiles_n, int grid) { return (INT32_MAX - gri
 
 // Kernel by the rows of one weight matrix (of the mean expert) and the number
 // of tiles, measured on MI355X (us):
-//  * the stream kernel up to 16 rows (16 x 11008 x 4096: 15.5, tiles 21.6; it
-//    loses from 17 rows on wide layers, 17 x 4096 x 11008: 15.6, tiles 10.8, and
-//    gains 1.4 on 17 x 4096 x 4096), with experts up to a mean of 8, since an
-//    expert with more than 16 rows reads its weights again (16 experts of 1376 x
-//    4096, mean 16: 37.7, tiles 20.4; mean 8: 22.4 both);
+//  * the stream kernel up to 16 rows (16 x 11008 x 4096: 15.8, tiles 21.9; one
+//    expert's 17 rows read the weights twice, 17 x 4096 x 11008: 23.7, tiles 12.9,
+//    17 x 4096 x 4096: 12.0, 12.1), with experts up to a mean of 8, since the
+//    larger ones of a mean of 16 read theirs again (64 experts of 4096 x 2752,
+//    mean 8: 113, tiles 155; 16 of 1376 x 4096, mean 16: 37.3, tiles 19.9, and
+//    tiles ahead there from a mean of 2 on, 20.8 against 17.4);
 //  * 64 x 64 tiles, two groups of waves sharing K, while one round of
-//    workgroups holds them all (200 x 4096 x 4096: 11.2, one group 12.7), one
-//    group beyond (128 x 4096 x 11008: 17.9, two groups 20.7);
-//  * 128 x 128 tiles from 256 of them on (512 x 4096 x 11008: 32.6, 64 x 64 tiles
-//    48.5);
+//    workgroups holds them all (200 x 4096 x 4096: 11.8, one group 13.4), one
+//    group beyond (128 x 4096 x 11008: 17.9, two groups 20.9);
+//  * 128 x 128 tiles from 256 of them on (512 x 4096 x 11008: 35.8, 64 x 64 tiles
+//    46.0);
 //  * 256 x 256 tiles, 16-bit outputs of one matrix, where their rounds (one
 //    workgroup on a CU) cost less than those of 128 x 128 (two on a CU, a round
-//    5/8 as long): 4096 x 4096 x 11008 187 against 225, 1024 x 4096 x 11008 57
-//    against 64, but 2048 x 4096 x 4096 53 against 40 (before the stores went
-//    past L2, which took 6% off both).
+//    5/8 as long): 4096 x 4096 x 11008 184 against 199-208, 1024 x 4096 x 11008 57
+//    against 60, but 2048 x 4096 x 4096 56 against 38.
 // Binary32 outputs take more registers than a 256 x 256 tile leaves, and
-// experts' rows seldom fill one (64 experts of 384 rows: 310 against 268).
+// experts' rows seldom fill one (64 experts of 384 rows of 1376 x 4096: 282
+// against 258).  R counts rows of no expert too (choices of another GPU's): the
+// row counts in use are on the GPU.
 enum class F8Kernel { kStream, kTile64TwoGroups, kTile64, kTile128, kTile256 };
 constexpr F8Kernel f8_kernel(bool experts, int64_t R, int64_t E, int64_t N, bool wide_out) {
   const int64_t rows = (R + E - 1) / E;   // of one weight matrix

@@ -520,8 +520,12 @@ qg_status_t dequantize_kv_i8_segments(const int8_t* kv_q, const float* kv_scale,
  * The last block along K (and along N, for weights) is shorter where 128 does
  * not divide the size.  G = ceil(K / 128), B = ceil(N / 128).
  * In this part K is a positive multiple of 16 up to 2^20, and M, N, T and R go
- * up to 2^30.  Code arrays, x and w are 16-byte aligned; scales, indices, y,
- * logits and expert rows need the alignment of their element only.
+ * up to 2^30; a call that would launch 2^32 threads is QG_ERR_SHAPE (8 threads
+ * for each block of a row, 256 for each block of a weight matrix, 512 for each
+ * 64 x 64 outputs of a product and each 16 columns of an expert, 64 for each
+ * token of a choice, 256 for each 256 outputs of a weighted sum).
+ * Code arrays, x and w are 16-byte aligned; scales, indices, y, logits and
+ * expert rows need the alignment of their element only.
  */
 
 /*
@@ -562,6 +566,9 @@ qg_status_t quantize_weight_f8_b128(const void* w, int w_dtype, int64_t E, int64
  * and drop, of each product, what lies below 2^-13 of the largest of its 8:
  * a part of at most 7 * 2^-13 of the sum of those largest products, and
  * about 2^-14 of the result where the terms are spread as in a linear layer.
+ * So the bits of a row depend on the number of rows of its call: through these
+ * two ways to multiply, and beyond 16 rows through the order of the binary32
+ * sums, which goes by the tile that the number of rows selects.
  */
 qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
                          const float* w_scale, int64_t M, int64_t N, int64_t K, void* y,
@@ -583,7 +590,8 @@ qg_status_t gemm_f8_b128(const uint8_t* xq, const float* x_scale, const uint8_t*
  * y:         [R][N]; rows ahead of offsets[0] and from offsets[E] on are left
  *            as they were.
  * 1 <= E <= 1024.  The kernel is chosen by the mean number of rows, R / E:
- * up to 8 the products are exact as for M <= 16 above.
+ * up to 8 the products are exact as for M <= 16 above, beyond it 16-bit outputs
+ * take the 8-bit matrix cores.  R counts rows of no expert too.
  */
 qg_status_t gemm_f8_b128_experts(const uint8_t* xq, const float* x_scale, const uint8_t* wq,
                                  const float* w_scale, const int32_t* offsets,
