@@ -12,15 +12,15 @@ NAMES = ("stream", "64x64 by two groups", "64x64", "128x128", "256x256")
 
 @functools.lru_cache(None)
 def _rule():
-    at = tempfile.mkdtemp()
-    src, lib = os.path.join(at, "choice.cpp"), os.path.join(at, "choice.so")
-    with open(src, "w") as f:
-        f.write('#include "qg_f8_index.hpp"\n'
-                'extern "C" int choice(int experts, int64_t R, int64_t E, int64_t N, int wide) {\n'
-                "  return (int)qg::f8_kernel(experts, R, E, N, wide);\n}\n")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", os.path.join(ROOT, "bit_quantized_gemm_int8_amd", "csrc"),
-                    src, "-o", lib], check=True, capture_output=True, text=True)
-    f = ctypes.CDLL(lib).choice
+    with tempfile.TemporaryDirectory() as at:
+        src, lib = os.path.join(at, "choice.cpp"), os.path.join(at, "choice.so")
+        with open(src, "w") as f:
+            f.write('#include "qg_f8_index.hpp"\n'
+                    'extern "C" int choice(int experts, int64_t R, int64_t E, int64_t N, int wide) {\n'
+                    "  return (int)qg::f8_kernel(experts, R, E, N, wide);\n}\n")
+        subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", os.path.join(ROOT, "bit_quantized_gemm_int8_amd", "csrc"),
+                        src, "-o", lib], check=True, capture_output=True, text=True)
+        f = ctypes.CDLL(lib).choice
     f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     return f
 
