@@ -276,7 +276,7 @@ constexpr int kF8Stage = 128;   // bytes of a row in a stage = one scale block
 // bytes of codes, a third of all requests with SG = 1.  4 for 128 x 128 tiles:
 // 24576 rows over 64 experts of 4096 x 2752 417 us, 444 with 1; 1024 x 4096 x
 // 4096 28.3, 30.5; of 31 plain shapes of 256 .. 512 tiles those of K = 11008 take
-// 7% less on average and none takes more, those of K = 4096 between 7% less and
+// 7% less on average and at most 0.2% more, those of K = 4096 between 7% less and
 // 11% more (768 x 4096 x 5504: 33.4, 30.0; 512 x 4096 x 11008: 35.4, 32.5), as
 // much on average; shapes of equal tile counts and widths lie on both sides, so
 // no rule on sizes divides them.  A 256 x 256 tile has no registers left for it
