@@ -35,8 +35,13 @@ Entry points (same names as the C ABI):
   plan_experts(expert, E)                       -> (offsets int32 [E+1], row_token int32 [T*k], slot int32 [T,k])
   gemm_f8_b128_experts(xq, x_scale, wq, w_scale, offsets, row_token, out_dtype) -> y [R,N]
   combine_experts(rows, slot, weight, out_dtype) -> y [T,N]
-with G = ceil(K/128) and B = ceil(N/128); these seven run on the device of
-their first tensor, whichever device is current.
+  kv_u4_pages(P, H, page, D, device)            -> int32 [P, H, words]: an empty 4-bit paged KV cache
+  append_kv_u4_pages(k, v, pages, page_table, lengths, offsets, q, cos, sin, interleaved) -> rotated q [T,Hq,D]
+  attend_kv_u4_pages(q, pages, page_table, lengths, offsets, window, sinks, scale) -> [T,Hq,D]
+  attend_kv_u4_pages_workspace_bytes(...)       -> bytes of device workspace that call needs
+  dequantize_kv_u4_pages(pages, page_table, lengths, T, D, offsets, out_dtype) -> (k, v) [T,H,D]
+with G = ceil(K/128) and B = ceil(N/128); from quantize_f8_g128 on they run on
+the device of their first tensor, whichever device is current.
 """
 from __future__ import annotations
 
@@ -61,6 +66,8 @@ __all__ = [
     "quantize_weight_u4_g128_sparse24", "gemm_w4a8_g128_sparse24",
     "quantize_f8_g128", "quantize_weight_f8_b128", "gemm_f8_b128", "gemm_f8_b128_experts",
     "route_experts", "plan_experts", "combine_experts",
+    "kv_u4_pages", "kv_u4_page_bytes", "append_kv_u4_pages", "attend_kv_u4_pages",
+    "attend_kv_u4_pages_workspace_bytes", "dequantize_kv_u4_pages",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqgemm.so")
@@ -106,6 +113,12 @@ _SIGNATURES = {
                       _vp, _vp],
     "plan_experts": [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp],
     "combine_experts": [_vp, _int, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _int, _vp],
+    "append_kv_u4_pages": [_vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _i64, _int, _i64,
+                           _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp],
+    "dequantize_kv_u4_pages": [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp,
+                               _vp, _int, _vp],
+    "attend_kv_u4_pages": [_vp, _i64, _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp,
+                           _vp, _i64, _i64, _i64, ctypes.c_float, _vp, _vp, _i64, _vp],
 }
 
 # measurement probes (include/qgemm_peaks.h)
@@ -141,6 +154,10 @@ def load() -> ctypes.CDLL:
         lib.quantize_gemm_w4a8_g128_workspace_bytes.restype = ctypes.c_int64
         lib.quantize_per_token_i8_panel_bytes.argtypes = [_i64, _i64]
         lib.quantize_per_token_i8_panel_bytes.restype = ctypes.c_int64
+        lib.kv_u4_page_bytes.argtypes = [_i64, _i64]
+        lib.kv_u4_page_bytes.restype = ctypes.c_int64
+        lib.attend_kv_u4_pages_workspace_bytes.argtypes = [_i64] * 7 + [_int]
+        lib.attend_kv_u4_pages_workspace_bytes.restype = ctypes.c_int64
         lib.qg_status_string.argtypes = [ctypes.c_int]
         lib.qg_status_string.restype = ctypes.c_char_p
         lib.qg_abi_version.restype = ctypes.c_int
@@ -738,6 +755,164 @@ def combine_experts(rows, slot, weight, out_dtype=None, out=None):
     y = _out(out, (T, N), out_dtype, dev)
     _call_on(dev, "combine_experts", pr, _DTYPE_CODE[rows.dtype], ps, pw, T, k, R, N, y.data_ptr(),
              code)
+    return y
+
+
+# ------------------------------------------------- 4-bit paged KV cache
+
+def kv_u4_page_bytes(page: int, D: int) -> int:
+    """Bytes of one head of a page of `page` positions (0: sizes not covered)."""
+    return int(load().kv_u4_page_bytes(page, D))
+
+
+def kv_u4_pages(P: int, H: int, page: int, D: int, device="cuda") -> torch.Tensor:
+    """An empty (all zero) 4-bit paged KV cache of one layer: int32 [P, H, words]
+    for P pages of `page` positions, H kv heads of D channels."""
+    words = kv_u4_page_bytes(page, D) // 4
+    if words == 0:
+        raise ValueError(f"page must be 16, 32, 64, 128 or 256 and D 64, 128 or 256, got {page}, {D}")
+    return torch.zeros((P, H, words), dtype=torch.int32, device=device)
+
+
+def _kv4_where(pages, page_table, lengths, offsets, D):
+    """Checked operands that the calls on a paged cache share: device, pointers
+    and sizes (pages, P, page, H, page_table, W, lengths, offsets, B)."""
+    pp = _dev(pages, "pages", (torch.int32,))
+    if pages.dim() != 3:
+        raise ValueError("pages must be [P, H, words]")
+    P, H, words = pages.shape
+    per = D // 4 + max(2, D // 64)      # words of a position
+    if D not in (64, 128, 256):
+        raise ValueError(f"the head width must be 64, 128 or 256, got {D}")
+    page = words // per
+    if page * per != words or page not in (16, 32, 64, 128, 256):
+        raise ValueError(f"pages of {words} words do not hold 16, 32, 64, 128 or 256 positions of {D} channels")
+    dev = pages.device
+    B, W = _2d(page_table, "page_table")
+    pt = _dev(page_table, "page_table", (torch.int32,), None, dev)
+    pl = _dev(lengths, "lengths", (torch.int32,), (B,), dev)
+    po = _opt(offsets, "offsets", (torch.int32,), (B + 1,), dev)
+    return dev, pp, P, page, H, pt, W, pl, po, B
+
+
+def _heads(t, name, dtypes, device, T=None, D=None):
+    """Pointer and token stride of a [T, heads, D] tensor whose heads are
+    contiguous; tokens may be further apart (a view of a fused projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (D is not None and t.shape[2] != D):
+        raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, {'D' if D is None else D}], "
+                         f"got {tuple(t.shape)}")
+    rows, heads, d = t.shape
+    step, by_head, by_one = t.stride()
+    if (d > 1 and by_one != 1) or (heads > 1 and by_head != d):
+        raise ValueError(f"{name} must have contiguous heads")
+    if rows <= 1:
+        step = heads * d
+    if step < heads * d:
+        raise ValueError(f"{name} has tokens that overlap")
+    return t.data_ptr(), step
+
+
+def append_kv_u4_pages(k, v, pages, page_table, lengths, offsets=None, q=None, cos=None, sin=None,
+                       interleaved=False, out=None):
+    """Rotate k [T, H, D] (and q [T, Hq, D]) by their positions with the tables
+    cos, sin f32 [positions, rot / 2] (None: no rotation) and append k and v
+    (f32/f16/bf16, views of a fused projection allowed) to the 4-bit cache
+    `pages`.  lengths int32 [B] counts the new tokens; offsets int32 [B + 1]
+    gives each sequence's rows (None: T / B each).  Returns the rotated q (None
+    without q), in `out` if given."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T, H, D]")
+    T, _, D = k.shape
+    dev, pp, P, page, H, pt, W, pl, po, B = _kv4_where(pages, page_table, lengths, offsets, D)
+    pk, ks = _heads(k, "k", _FLOATS, dev)
+    pv, vs = _heads(v, "v", (k.dtype,), dev, T, D)
+    if k.shape[1] != H or v.shape[1] != H:
+        raise ValueError(f"k and v must have the {H} heads of pages")
+    if offsets is None and (T % B if B else T):
+        raise ValueError(f"{T} rows are no whole number for each of {B} sequences")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    pc = ps = None
+    rows = rot = 0
+    if cos is not None:
+        rows, half = _2d(cos, "cos")
+        rot = 2 * half
+        if rot % 16 or not 0 < rot <= D:
+            raise ValueError(f"cos must have a multiple of 8 columns up to {D // 2}, got {half}")
+        pc = _dev(cos, "cos", (torch.float32,), None, dev)
+        ps = _dev(sin, "sin", (torch.float32,), (rows, half), dev)
+    pq, qs, Hq, y = None, 0, 0, None
+    if q is not None:
+        pq, qs = _heads(q, "q", (k.dtype,), dev, T, D)
+        Hq = q.shape[1]
+        y = _out(out, (T, Hq, D), q.dtype, dev)
+    elif out is not None:
+        raise ValueError("out is for the rotated q, and there is no q")
+    _call_on(dev, "append_kv_u4_pages", pq, qs, pk, ks, pv, vs, _DTYPE_CODE[k.dtype], pc, ps, rows,
+             rot, int(bool(interleaved)), T, Hq, H, D, pp, P, page, pt, W, pl, po, B,
+             y.data_ptr() if y is not None else None)
+    return y
+
+
+def dequantize_kv_u4_pages(pages, page_table, lengths, T, D, offsets=None, out_dtype=torch.bfloat16,
+                           out=None):
+    """(k, v) [T, H, D]: the cached keys and values at the positions of T rows,
+    the last T / B (or offsets[b + 1] - offsets[b]) positions of each sequence.
+    Rows of no sequence are left as they were in `out` (without it: undefined)."""
+    dev, pp, P, page, H, pt, W, pl, po, B = _kv4_where(pages, page_table, lengths, offsets, D)
+    if offsets is None and (T % B if B else T):
+        raise ValueError(f"{T} rows are no whole number for each of {B} sequences")
+    code = _float_code(out_dtype)
+    k, v = out if out is not None else (None, None)
+    k = _out(k, (T, H, D), out_dtype, dev, "k out")
+    v = _out(v, (T, H, D), out_dtype, dev, "v out")
+    _call_on(dev, "dequantize_kv_u4_pages", pp, P, page, pt, W, pl, po, B, T, H, D, k.data_ptr(),
+             v.data_ptr(), code)
+    return k, v
+
+
+def attend_kv_u4_pages_workspace_bytes(T, B, Hq, H, D, page, W, ragged=False) -> int:
+    """Device workspace (bytes) attend_kv_u4_pages needs for T rows of Hq heads of
+    B sequences, pages of `page` positions and a page table of width W (ragged:
+    with offsets)."""
+    return int(load().attend_kv_u4_pages_workspace_bytes(T, B, Hq, H, D, page, W, int(bool(ragged))))
+
+
+def attend_kv_u4_pages(q, pages, page_table, lengths, offsets=None, window=0, sinks=0, scale=None,
+                       out=None, workspace=None):
+    """Attention of q [T, Hq, D] (f16/bf16, the newest tokens of their sequences)
+    over the 4-bit cache: the row at position p sees the positions j <= p, with
+    window > 0 only j > p - window and j < sinks.  scale None: D ** -0.5.
+    Returns [T, Hq, D] of q's dtype; rows that see nothing are zeros, rows of no
+    sequence as they were in `out` (without it: undefined).  workspace: a
+    contiguous uint8 tensor of attend_kv_u4_pages_workspace_bytes(...) bytes,
+    allocated here when None."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    dev, pp, P, page, H, pt, W, pl, po, B = _kv4_where(pages, page_table, lengths, offsets, D)
+    pq, qs = _heads(q, "q", (torch.float16, torch.bfloat16), dev)
+    if Hq == 0 or Hq % H:
+        raise ValueError(f"q has {Hq} heads, which the {H} heads of pages do not divide")
+    if offsets is None and (T % B if B else T):
+        raise ValueError(f"{T} rows are no whole number for each of {B} sequences")
+    y = _out(out, (T, Hq, D), q.dtype, dev)
+    need = (_lib or load()).attend_kv_u4_pages_workspace_bytes(T, B, Hq, H, D, page, W,
+                                                               0 if offsets is None else 1)
+    pw, size = None, 0
+    if workspace is not None:
+        pw, size = _dev(workspace, "workspace", (torch.uint8,), None, dev), workspace.numel()
+    elif need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        pw, size = workspace.data_ptr(), need
+    _call_on(dev, "attend_kv_u4_pages", pq, qs, _DTYPE_CODE[q.dtype], T, Hq, H, D, pp, P, page, pt, W,
+             pl, po, B, window, sinks, D ** -0.5 if scale is None else scale, y.data_ptr(), pw, size)
     return y
 
 

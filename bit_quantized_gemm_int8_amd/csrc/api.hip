@@ -57,6 +57,44 @@ inline bool aligned_to(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == QG_F32 ? 3u : 1u)) == 0;
 }
 
+// The 4-bit paged cache.  Capacity of a sequence and rows of a call stay below
+// 2^30, so that positions and their differences fit 32 bits.
+constexpr int64_t kMaxKv4 = (int64_t)1 << 30;
+constexpr int64_t kMaxKv4Heads = 1024;
+
+bool kv4_sizes(int64_t page, int64_t D) {
+  return (D == 64 || D == 128 || D == 256) && page >= 16 && page <= 256 && (page & (page - 1)) == 0;
+}
+
+// Sizes of a call, and its pointers once it has rows (T > 0).
+qg_status_t check_kv4(const int32_t* pages, const int32_t* page_table, const int32_t* lengths,
+                      const int32_t* offsets, int64_t T, int64_t B, int64_t H, int64_t D,
+                      int64_t P, int64_t page, int64_t W, qg::Kv4Seqs* s) {
+  if (!kv4_sizes(page, D)) return QG_ERR_SHAPE;
+  if (T < 0 || T > kMaxKv4 || B < 0 || B > kMaxKv4 || H < 1 || H > kMaxKv4Heads || P < 0 || P > kMaxKv4 ||
+      W < 0 || W > kMaxKv4 / page)
+    return QG_ERR_SHAPE;
+  if (T == 0) return QG_OK;
+  if (B < 1 || (!offsets && T % B)) return QG_ERR_SHAPE;
+  if (!lengths || (W > 0 && !page_table) || (P > 0 && !pages)) return QG_ERR_NULL;
+  if (!aligned16(pages) || (reinterpret_cast<uintptr_t>(page_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lengths) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+    return QG_ERR_ALIGN;
+  int shift = 0;
+  while (((int64_t)1 << shift) < page) ++shift;
+  *s = qg::Kv4Seqs{const_cast<int32_t*>(pages), page_table, lengths, offsets, (int)P, (int)H, (int)W,
+                   shift, (int)B, (int)T};
+  return QG_OK;
+}
+
+// A tensor [T][heads][D] with a free step from token to token.
+qg_status_t check_kv4_rows(const void* p, int64_t stride, int64_t heads, int64_t D, int dtype) {
+  if (stride < heads * D || stride > ((int64_t)1 << 40)) return QG_ERR_SHAPE;
+  if (!p) return QG_ERR_NULL;
+  if (!aligned16(p) || stride * (dtype == QG_F32 ? 4 : 2) % 16) return QG_ERR_ALIGN;
+  return QG_OK;
+}
+
 // A launch holds fewer than 2^32 threads.
 inline bool fits_grid(int64_t workgroups, int64_t threads) {
   return workgroups <= ((int64_t)1 << 32) / threads - 1;
@@ -523,6 +561,86 @@ qg_status_t combine_experts(const void* rows, int rows_dtype, const int32_t* slo
     return QG_ERR_ALIGN;
   return hip_status(qg::launch_combine(rows, rows_dtype, slot, weight, T, k, R, N, y, y_dtype,
                                        static_cast<hipStream_t>(stream)));
+}
+
+int64_t kv_u4_page_bytes(int64_t page, int64_t D) {
+  return kv4_sizes(page, D) ? page * (D / 4 + (D > 128 ? 2 * (D / 128) : 2)) * 4 : 0;
+}
+
+qg_status_t append_kv_u4_pages(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int dtype, const float* cos,
+                               const float* sin, int64_t table_rows, int64_t rot, int interleaved,
+                               int64_t T, int64_t Hq, int64_t H, int64_t D, int32_t* pages,
+                               int64_t P, int64_t page, const int32_t* page_table, int64_t W,
+                               const int32_t* lengths, const int32_t* offsets, int64_t B,
+                               void* q_out, void* stream) {
+  qg::Kv4Seqs s;
+  if (qg_status_t e = check_kv4(pages, page_table, lengths, offsets, T, B, H, D, P, page, W, &s)) return e;
+  if (Hq < 0 || Hq > kMaxKv4Heads || rot < 0 || rot > D || rot % 16 || table_rows < 0) return QG_ERR_SHAPE;
+  if (interleaved != 0 && interleaved != 1) return QG_ERR_ARG;
+  if (!is_float_dtype(dtype)) return QG_ERR_DTYPE;
+  if (!fits_grid(T * (((Hq + 2 * H) * (D / 16) + 255) / 256), 256)) return QG_ERR_SHAPE;
+  if (T == 0) return QG_OK;
+  if (rot > 0 && table_rows > 0 && (!cos || !sin)) return QG_ERR_NULL;
+  if (!aligned4(cos) || !aligned4(sin)) return QG_ERR_ALIGN;
+  if (qg_status_t e = check_kv4_rows(k, k_stride, H, D, dtype)) return e;
+  if (qg_status_t e = check_kv4_rows(v, v_stride, H, D, dtype)) return e;
+  if (Hq > 0) {
+    if (qg_status_t e = check_kv4_rows(q, q_stride, Hq, D, dtype)) return e;
+    if (!q_out) return QG_ERR_NULL;
+    if (!aligned16(q_out)) return QG_ERR_ALIGN;
+  }
+  const qg::Kv4Append a{q, k, v, q_stride, k_stride, v_stride, cos, sin, table_rows, (int)rot,
+                        interleaved, (int)Hq, (int)D, q_out};
+  return hip_status(qg::launch_kv4_append(s, a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+qg_status_t dequantize_kv_u4_pages(const int32_t* pages, int64_t P, int64_t page,
+                                   const int32_t* page_table, int64_t W, const int32_t* lengths,
+                                   const int32_t* offsets, int64_t B, int64_t T, int64_t H,
+                                   int64_t D, void* k, void* v, int out_dtype, void* stream) {
+  qg::Kv4Seqs s;
+  if (qg_status_t e = check_kv4(pages, page_table, lengths, offsets, T, B, H, D, P, page, W, &s)) return e;
+  if (!is_float_dtype(out_dtype)) return QG_ERR_DTYPE;
+  if (!fits_grid(T * ((2 * H * (D / 8) + 255) / 256), 256)) return QG_ERR_SHAPE;
+  if (T == 0) return QG_OK;
+  if (!k || !v) return QG_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v)) return QG_ERR_ALIGN;
+  return hip_status(qg::launch_kv4_dequant(s, (int)D, k, v, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+int64_t attend_kv_u4_pages_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
+                                           int64_t page, int64_t W, int ragged) {
+  if (!kv4_sizes(page, D) || T <= 0 || T > kMaxKv4 || B < 1 || B > kMaxKv4 || H < 1 || H > kMaxKv4Heads ||
+      Hq < H || Hq > kMaxKv4Heads || Hq % H || W < 0 || W > kMaxKv4 / page || (!ragged && T % B) ||
+      T * Hq > kMaxKv4)
+    return 0;
+  const int64_t need = qg::kv4_attend_workspace(T, B, Hq, H, D, W * page, !ragged);
+  return need > 0 ? need : 0;
+}
+
+qg_status_t attend_kv_u4_pages(const void* q, int64_t q_stride, int dtype, int64_t T, int64_t Hq,
+                               int64_t H, int64_t D, const int32_t* pages, int64_t P, int64_t page,
+                               const int32_t* page_table, int64_t W, const int32_t* lengths,
+                               const int32_t* offsets, int64_t B, int64_t window, int64_t sinks,
+                               float scale, void* out, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  qg::Kv4Seqs s;
+  if (qg_status_t e = check_kv4(pages, page_table, lengths, offsets, T, B, H, D, P, page, W, &s)) return e;
+  if (Hq < H || Hq > kMaxKv4Heads || Hq % H || T * Hq > kMaxKv4) return QG_ERR_SHAPE;
+  if (window < 0 || window > kMaxKv4 || sinks < 0 || sinks > kMaxKv4) return QG_ERR_SHAPE;
+  if (dtype != QG_F16 && dtype != QG_BF16) return QG_ERR_DTYPE;
+  if (!(scale - scale == 0.f)) return QG_ERR_ARG;   // not finite
+  if (T == 0) return QG_OK;
+  if (qg_status_t e = check_kv4_rows(q, q_stride, Hq, D, dtype)) return e;
+  if (!out) return QG_ERR_NULL;
+  const int64_t need = qg::kv4_attend_workspace(T, B, Hq, H, D, W * page, offsets == nullptr);
+  if (need < 0) return QG_ERR_SHAPE;
+  if (need > 0 && !workspace) return QG_ERR_NULL;
+  if (workspace_bytes < need) return QG_ERR_SHAPE;
+  if (!aligned16(out) || !aligned16(workspace)) return QG_ERR_ALIGN;
+  const qg::Kv4Attend a{q, q_stride, (int)Hq, (int)D, (int)window, (int)sinks, scale, out, workspace};
+  return hip_status(qg::launch_kv4_attend(s, a, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,84 @@
+// What the two attention kernels of the 4-bit cache share: which sequence and
+// rows a workgroup has, and which cached positions those rows can see.
+//
+// The rows of a sequence and kv head h are its n tokens times the G = Hq / H
+// query heads of h, row = token * G + head.  A tile is up to ROWS of them.
+#pragma once
+
+#include "qg_kv4.hpp"
+
+namespace qg {
+
+struct Kv4Tile {
+  int b;          // sequence, -1: no such tile
+  int token0, n;  // its first row of the call, and its tokens
+  int row0;       // the tile's first row
+};
+
+// Tile `idx` among the sequences with min_rows <= n G <= max_rows, ROWS rows each.
+// All lanes of a wave call it with the same arguments; the result is uniform.
+template <int ROWS>
+__device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, int G, int64_t min_rows,
+                                            int64_t max_rows, int idx) {
+  if (s.offsets == nullptr) {
+    const int n = s.T / s.B;
+    const int tiles = (n * G + ROWS - 1) / ROWS;
+    const int b = idx / tiles;
+    return {b < s.B ? b : -1, b * n, n, (idx - b * tiles) * ROWS};
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 64) {
+    int first = 0, n = 0;
+    if (b0 + lane < s.B) {
+      first = min(max(s.offsets[b0 + lane], 0), s.T);
+      n = min(max(s.offsets[b0 + lane + 1], first), s.T) - first;
+    }
+    const int64_t rows = (int64_t)n * G;
+    const int tiles = rows >= min_rows && rows <= max_rows ? (int)((rows + ROWS - 1) / ROWS) : 0;
+    int64_t upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t below = __shfl_up(upto, o, kWave);
+      if (lane >= o) upto += below;
+    }
+    const uint64_t behind = __ballot(base + upto > idx);
+    if (behind != 0) {
+      const int l = __ffsll((unsigned long long)behind) - 1;
+      const int64_t before = base + __shfl(upto, l, kWave) - __shfl(tiles, l, kWave);
+      return {__builtin_amdgcn_readfirstlane(b0 + l), __builtin_amdgcn_readfirstlane(__shfl(first, l, kWave)),
+              __builtin_amdgcn_readfirstlane(__shfl(n, l, kWave)),
+              __builtin_amdgcn_readfirstlane((int)(idx - before)) * ROWS};
+    }
+    base += __shfl(upto, 63, kWave);
+  }
+  return {-1, 0, 0, 0};
+}
+
+// The cached positions that rows at positions p0 .. p1 can see, in tiles of
+// STEP: tiles 0 .. first - 1 hold first positions that stay visible, the next
+// ones are tiles skip + first, ... of the cache.
+struct Kv4Span {
+  int tiles, first, skip;
+  __device__ __forceinline__ int tile(int u) const { return u < first ? u : u + skip; }
+};
+
+template <int STEP>
+__device__ __forceinline__ Kv4Span kv4_span(int p0, int p1, int window, int sinks, int capacity) {
+  const int end = min(p1 + 1, capacity);
+  if (end <= 0) return {0, 0, 0};
+  const int all = (end + STEP - 1) / STEP;
+  if (window <= 0) return {all, 0, 0};
+  const int low = max(p0 - window + 1, 0) / STEP;   // first tile of the window
+  if (low >= all) {                                 // the cache ends ahead of the window
+    const int first = min((min(sinks, end) + STEP - 1) / STEP, all);
+    return {first, first, 0};
+  }
+  const int first = min((sinks + STEP - 1) / STEP, low);
+  return {first + all - low, first, low - first};
+}
+
+// Position of row `row` of a tile's sequence (kPast: the row does not exist).
+constexpr int kKv4Past = -0x40000000;
+
+}  // namespace qg

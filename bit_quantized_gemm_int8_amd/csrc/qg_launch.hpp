@@ -104,4 +104,38 @@ hipError_t launch_combine(const void* rows, int dtype, const int32_t* slot, cons
                           int64_t tokens, int64_t k, int64_t R, int64_t N, void* y, int y_dtype,
                           hipStream_t st);
 
+// A paged 4-bit KV cache and the sequences of a call (sizes checked to fit).
+struct Kv4Seqs {
+  int32_t* pages;           // [P][H][words of a page's head]
+  const int32_t* table;     // [B][W]
+  const int32_t* lengths;   // [B]
+  const int32_t* offsets;   // [B + 1], or NULL: T / B rows of each
+  int P, H, W, shift;       // pages of 1 << shift positions
+  int B, T;
+};
+struct Kv4Append {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements from token to token
+  const float *cos, *sin;                 // [table_rows][rot / 2]
+  int64_t table_rows;
+  int rot, interleaved, Hq, D;
+  void* q_out;                            // [T][Hq][D]
+};
+struct Kv4Attend {
+  const void* q;
+  int64_t q_stride;
+  int Hq, D, window, sinks;
+  float scale;
+  void* out;                              // [T][Hq][D]
+  void* workspace;
+};
+hipError_t launch_kv4_append(const Kv4Seqs& s, const Kv4Append& a, int dtype, hipStream_t st);
+hipError_t launch_kv4_dequant(const Kv4Seqs& s, int D, void* k, void* v, int out_dtype,
+                              hipStream_t st);
+hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st);
+// Bytes of device workspace launch_kv4_attend needs (uniform: no offsets), -1
+// where a launch would not hold the call.
+int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
+                             int64_t capacity, bool uniform);
+
 }  // namespace qg

@@ -656,6 +656,114 @@ qg_status_t combine_experts(const void* rows, int rows_dtype, const int32_t* slo
                             const float* weight, int64_t T, int64_t k, int64_t R, int64_t N,
                             void* y, int y_dtype, void* stream);
 
+/*
+ * ---- 4-bit paged KV cache: filling it, attending over it, reading it ----
+ *
+ * The keys and values of one layer, 4 bits each, in pages of `page` positions
+ * that the sequences of a batch own through a page table.  In this part
+ *   D is 64, 128 or 256; page 16, 32, 64, 128 or 256; H kv heads, Hq query
+ *   heads, both up to 1024; groups are min(D, 128) channels, Gd = max(1, D / 128).
+ * Group code (the rule of quantize_weight_u4_g128 with zero in every range and
+ * a scale of 7 significant bits), over the channels of a group:
+ *   lo = min(0, min x);  hi = max(0, max x);  t = (hi - lo) / 15;
+ *   s = t rounded up to 7 significant bits;  z = rne(-lo / s);
+ *   q = clamp(rne(x / s) + z, 0, 15);        value = (q - z) s;
+ *   all binary32, quotients correctly rounded.  A group of zeros gets s = 0.
+ *   A group with a value that is not finite, or whose hi - lo is not, is stored
+ *   as NaN: rows that see it are NaN, rows that do not see it are not touched.
+ *   (q - z) s has at most 11 significant bits: exact in binary16 and binary32
+ *   wherever it is in their range.
+ * pages: [P][H][page (D / 4 + 2 Gd)] 32-bit words, 16-byte aligned; of one head
+ *   key codes    [page][D / 8]         packed uint4 format above
+ *   value codes  [page / 4][D / 8][4]  the same words, four positions side by side
+ *   key groups   [Gd][page]            s (its upper 16 bits) | z, one word each
+ *   value groups [Gd][page]
+ * page_table: [B][W] int32.  Position p of sequence b is in page
+ *   page_table[b][p / page]; an entry outside 0 .. P-1 is no page.  Entries of
+ *   pages that no call needs (behind the last position, out of a window's
+ *   sight) may hold anything.  W * page <= 2^30.
+ * lengths: [B] int32, cached positions of each sequence, the call's own tokens
+ *   among them.
+ * offsets: [B + 1] int32, rising: sequence b has the rows offsets[b] ..
+ *   offsets[b+1]-1 of the call; or NULL: T / B rows of each, B dividing T.
+ *   A row i of sequence b has the position lengths[b] - offsets[b+1] + i.
+ *   Rows of no sequence (ahead of offsets[0], from offsets[B] on) are left as
+ *   they were.  Offsets that do not rise, or leave 0 .. T, give undefined rows
+ *   but no access outside the buffers.
+ * page_table, lengths and offsets are read on the GPU: a captured graph replays
+ * with what they hold then.  T <= 2^30, B <= 2^30.
+ */
+
+/* Bytes of one head of a page; 0 where page or D is not one of the above. */
+int64_t kv_u4_page_bytes(int64_t page, int64_t D);
+
+/*
+ * Rotate queries and keys by their positions and append keys and values to the
+ * cache, in one launch.
+ *   For each row with a position p that the page table holds and, if rot > 0,
+ *   the tables too (0 <= p < table_rows):
+ *     the pairs (a, b) of the first rot channels of q and k become
+ *     (a c - b s, b c + a s), c = cos[p][i], s = sin[p][i], each product and
+ *     sum rounded to binary32; pair i is channels i and i + rot / 2, or 2 i and
+ *     2 i + 1 if interleaved is 1;
+ *     q_out = the rotated q in its own type;  k (rotated) and v are written
+ *     into the pages as the group codes of their binary32 values.
+ *   Other rows write nothing into the pages; their q_out is rotated as long as
+ *   the tables hold p, and zeros otherwise.
+ * q: [T][Hq][D] (NULL with Hq = 0: no queries), k, v: [T][H][D], of one dtype
+ * (QG_F32, QG_F16 or QG_BF16), read.  Heads are D elements apart, tokens
+ * q_stride, k_stride, v_stride elements (at least heads * D, a multiple of 16
+ * bytes): views of a fused projection's rows fit.  16-byte aligned.
+ * cos, sin: [table_rows][rot / 2] float, read; rot a multiple of 16 up to D,
+ * 0 for no rotation (then cos and sin may be NULL and q is copied).
+ * q_out: [T][Hq][D] of dtype, written; it may be q where q_stride is Hq * D.
+ * Two rows of one call for one position: either's codes.
+ */
+qg_status_t append_kv_u4_pages(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int dtype, const float* cos,
+                               const float* sin, int64_t table_rows, int64_t rot, int interleaved,
+                               int64_t T, int64_t Hq, int64_t H, int64_t D, int32_t* pages,
+                               int64_t P, int64_t page, const int32_t* page_table, int64_t W,
+                               const int32_t* lengths, const int32_t* offsets, int64_t B,
+                               void* q_out, void* stream);
+
+/*
+ * The cached keys and values at the rows' positions (the last T tokens of the
+ * sequences, whichever call appended them): k, v [T][H][D] of out_dtype
+ * (QG_F32, QG_F16 or QG_BF16, round to nearest even), 16-byte aligned, written.
+ * A row whose position has no page is zeros.
+ */
+qg_status_t dequantize_kv_u4_pages(const int32_t* pages, int64_t P, int64_t page,
+                                   const int32_t* page_table, int64_t W, const int32_t* lengths,
+                                   const int32_t* offsets, int64_t B, int64_t T, int64_t H,
+                                   int64_t D, void* k, void* v, int out_dtype, void* stream);
+
+/*
+ * Attention of the call's rows over their sequences' cached positions.
+ *   The row at position p sees the positions j <= p of its sequence that have a
+ *   page; with window > 0 only those with j > p - window or j < sinks.
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j), over the visible
+ *   j, for query head h with kv head h / (Hq / H); a row that sees nothing is
+ *   zeros.  What lies in positions out of sight has no influence, NaN included.
+ * q: [T][Hq][D] of dtype QG_F16 or QG_BF16, tokens q_stride elements apart (as
+ * in append_kv_u4_pages), read; H divides Hq; T * Hq <= 2^30; scale is finite.
+ * out: [T][Hq][D] of dtype, 16-byte aligned, written.
+ * workspace: attend_kv_u4_pages_workspace_bytes(...) bytes of device memory, 16-byte
+ * aligned (NULL where that is 0), free again when the call's work is done;
+ * calls that overlap on the GPU need one each.
+ * Scores, weights and sums are binary32; the weights times their value scales
+ * are rounded to binary16 (relative to the row's largest, 2^-11) for the matrix
+ * cores.  The order of a row's sums goes by the sizes of the call.
+ */
+int64_t attend_kv_u4_pages_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
+                                           int64_t page, int64_t W, int ragged /* offsets given */);
+qg_status_t attend_kv_u4_pages(const void* q, int64_t q_stride, int dtype, int64_t T, int64_t Hq,
+                               int64_t H, int64_t D, const int32_t* pages, int64_t P, int64_t page,
+                               const int32_t* page_table, int64_t W, const int32_t* lengths,
+                               const int32_t* offsets, int64_t B, int64_t window, int64_t sinks,
+                               float scale, void* out, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif
