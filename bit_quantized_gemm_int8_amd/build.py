@@ -20,7 +20,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "quant.hip", "fold.hip", "gemm_w8a8.hip", "gemm_w4a8.hip", "gemm_w4a8_fused.hip", "gemm_w4a16.hip",
            "kv.hip", "gemm_w4a8_sp24.hip", "gemm_w8a8_fq.hip", "quant_f8.hip",
-           "gemm_f8.hip", "experts.hip", "kv4.hip", "attn_kv4.hip", "peaks.hip"]
+           "gemm_f8.hip", "experts.hip", "kv4.hip", "attn_kv4.hip",
+           "attn_kv4_prompt.hip", "peaks.hip"]
 
 CFLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -82,8 +82,9 @@ qg_status_t check_kv4(const int32_t* pages, const int32_t* page_table, const int
     return QG_ERR_ALIGN;
   int shift = 0;
   while (((int64_t)1 << shift) < page) ++shift;
-  *s = qg::Kv4Seqs{const_cast<int32_t*>(pages), page_table, lengths, offsets, (int)P, (int)H, (int)W,
-                   shift, (int)B, (int)T};
+  // without pages no position has one: no kernel looks for any
+  *s = qg::Kv4Seqs{const_cast<int32_t*>(pages), page_table, lengths, offsets, (int)P, (int)H,
+                   P > 0 ? (int)W : 0, shift, (int)B, (int)T};
   return QG_OK;
 }
 

@@ -537,31 +537,55 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p) {
 
 namespace {
 
-// Row tiles of a call: sequences have n G rows, in tiles of `rows`.
-int64_t few_tiles(int64_t T, int64_t B, int64_t G, bool uniform, int rows) {
-  if (uniform) return B * ((T / B * G + rows - 1) / rows);
-  return std::min(T * G, T * G / rows + B);
-}
+// Sequences of up to kFewRows rows are this file's, longer ones the prompt
+// kernel's.  Without offsets the call's sequences are alike; with them the GPU
+// tells, so that both kernels are launched where either may have some.
+constexpr int64_t kFewRows = 64;
 
-// 16 rows a tile where a sequence has no more on average, else 32.
-int few_rows(int64_t T, int64_t B, int64_t G, int64_t D) { return D < 256 && T * G > 16 * B ? 32 : 16; }
+struct AttendPlan {
+  int64_t few_tiles, many_tiles;   // tiles of a kv head, 0: no launch
+  int few_rows, many_rows;         // rows of a tile
+  int splits;
+  bool fits;
+};
 
-// Splits of the cached positions: enough workgroups for the GPU, at least 256
-// positions each.
-int few_splits(int64_t tiles, int64_t capacity) {
-  const int64_t want = (2048 + tiles - 1) / tiles;
-  return (int)std::max<int64_t>(1, std::min(want, capacity / 256));
+AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t capacity, bool uniform) {
+  AttendPlan a = {};
+  const int64_t G = Hq / H, rows = T * G;
+  const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const auto tiles = [&](int64_t tile, int64_t most) {
+    // of sequences with at most `most` rows each, `rows` together
+    if (uniform) return B * up(rows / B, tile);
+    return std::min(std::min(rows, rows / tile + B), most == 0 ? rows : B * up(most, tile));
+  };
+  const bool few = !uniform || rows / B <= kFewRows, many = uniform ? !few : rows > kFewRows;
+  if (few) {
+    // 16 rows a tile where a sequence has no more on average, else 32
+    a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
+    a.few_tiles = tiles(a.few_rows, kFewRows);
+    // splits of the cached positions: enough workgroups for the GPU, at least 256 positions each
+    const int64_t want = up(2048, a.few_tiles * H);
+    a.splits = (int)std::max<int64_t>(1, std::min(want, capacity / 256));
+  }
+  if (many) {
+    const auto of = [&](int64_t tile) {
+      return uniform ? tiles(tile, 0) : rows / tile + std::min(B, rows / (kFewRows + 1));
+    };
+    a.many_rows = D < 256 && of(256) * H >= 512 ? 256 : 128;
+    a.many_tiles = of(a.many_rows);
+  }
+  // a launch holds fewer than 2^32 threads
+  a.fits = a.few_tiles * H * std::max(a.splits, 1) < (int64_t)1 << 24 && a.many_tiles * H < (int64_t)1 << 23;
+  return a;
 }
 
 }  // namespace
 
 int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
                              int64_t capacity, bool uniform) {
-  const int rows = few_rows(T, B, Hq / H, D);
-  const int64_t tiles = few_tiles(T, B, Hq / H, uniform, rows) * H;
-  const int64_t splits = few_splits(tiles, capacity);
-  if (tiles * splits >= (int64_t)1 << 24) return -1;   // 2^32 threads
-  return splits > 1 ? tiles * splits * rows * (D + 2) * 4 : 0;
+  const AttendPlan a = attend_plan(T, B, Hq, H, D, capacity, uniform);
+  if (!a.fits) return -1;
+  return a.splits > 1 ? a.few_tiles * H * a.splits * a.few_rows * (D + 2) * 4 : 0;
 }
 
 template <int DT, int D, int RT>
@@ -579,18 +603,23 @@ static hipError_t few_d(const Kv4FewArgs& p, int D, int rows, int64_t tiles, hip
 }
 
 hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st) {
+  const AttendPlan plan =
+      attend_plan(s.T, s.B, a.Hq, s.H, a.D, (int64_t)s.W << s.shift, s.offsets == nullptr);
+  if (plan.many_tiles > 0) {
+    const hipError_t e = launch_kv4_many(s, a, dtype, s.offsets == nullptr ? 1 : kFewRows + 1, plan.many_rows,
+                                         plan.many_tiles, st);
+    if (e != hipSuccess || plan.few_tiles == 0) return e;
+  }
   Kv4FewArgs p;
   p.s = s;
   p.a = a;
   p.G = a.Hq / s.H;
-  p.max_rows = (int64_t)1 << 40;
-  const int64_t capacity = (int64_t)s.W << s.shift;
-  const int rows = few_rows(s.T, s.B, p.G, a.D);
-  const int64_t tiles = few_tiles(s.T, s.B, p.G, s.offsets == nullptr, rows) * s.H;
-  p.splits = few_splits(tiles, capacity);
+  p.max_rows = kFewRows;
+  p.splits = plan.splits;
+  const int64_t tiles = plan.few_tiles * s.H;
   p.part_o = (float*)a.workspace;
-  p.part_ml = p.part_o + tiles * p.splits * rows * a.D;
-  return dtype == F16 ? few_d<F16>(p, a.D, rows, tiles, st) : few_d<BF16>(p, a.D, rows, tiles, st);
+  p.part_ml = p.part_o + tiles * p.splits * plan.few_rows * a.D;
+  return dtype == F16 ? few_d<F16>(p, a.D, plan.few_rows, tiles, st) : few_d<BF16>(p, a.D, plan.few_rows, tiles, st);
 }
 
 }  // namespace qg

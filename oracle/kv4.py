@@ -160,16 +160,16 @@ def visible(pos, n_keys, there, window, sinks):
 def attend(q, k, v, seen, scale):
     """q [n, Hq, D], k, v [L, H, D], seen [n, L], all float64 -> (out, weights [n, Hq, L])."""
     n, Hq, D = q.shape
-    G = Hq // k.shape[1]
-    out, weights = np.zeros((n, Hq, D)), np.zeros((n, Hq, k.shape[0]))
-    for i in range(n):
-        at = np.nonzero(seen[i])[0]
-        if len(at) == 0:
-            continue
-        for h in range(Hq):
-            x = scale * (k[at, h // G] @ q[i, h])
-            w = np.exp(x - x.max())
-            w /= w.sum()
-            out[i, h] = w @ v[at, h // G]
-            weights[i, h, at] = w
-    return out, weights
+    L, H, _ = k.shape
+    if L == 0:
+        return np.zeros((n, Hq, D)), np.zeros((n, Hq, 0))
+    G = Hq // H
+    any_sees = seen.any(0)
+    k, v = (np.where(any_sees[:, None, None], a, 0.0) for a in (k, v))
+    x = np.einsum("nhgd,lhd->nhgl", q.reshape(n, H, G, D), k).reshape(n, Hq, L) * scale
+    x = np.where(seen[:, None], x, -np.inf)
+    top = x.max(-1, keepdims=True)
+    w = np.where(seen[:, None], np.exp(x - np.where(np.isfinite(top), top, 0.0)), 0.0)
+    w /= np.maximum(w.sum(-1, keepdims=True), 1e-300)
+    out = np.einsum("nhgl,lhd->nhgd", w.reshape(n, H, G, L), v).reshape(n, Hq, D)
+    return out, w

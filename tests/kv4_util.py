@@ -72,26 +72,19 @@ def error_bound(q, k, v, p, seen, o, scale, G, w):
     sum p_t e_t (|v_t| + |o|).
     """
     n, Hq, D = q.shape
-    L = k.shape[0]
+    L, H, _ = k.shape
     u = 2.0 ** -24
-    out = np.zeros((n, Hq, D))
     if L == 0:
-        return out
-    sk = np.abs(k).reshape(L, -1, D // w, w).max(-1) / 7      # [L, H, Gd] at least the scales
-    sv = np.abs(v).reshape(L, -1, D // w, w).max(-1) / 7
-    for i in range(n):
-        for h in range(Hq):
-            pw = p[i, h]
-            if not seen[i].any():
-                continue
-            qa = np.abs(q[i, h]).reshape(D // w, w).sum(-1)   # [Gd]
-            at = seen[i]                                      # what is out of sight may be anything
-            pw, kh, vh = pw[at], sk[at, h // G], sv[at, h // G]
-            A = abs(scale) * 30 * (kh @ qa)
-            e = (2 * D + 12 + 4) * u * A + 2.0 ** -22
-            big = (pw[:, None] * vh).max(0)                   # [Gd]
-            va = np.abs(v[at, h // G])
-            per = (pw * (e + 2.0 ** -11)) @ va + (pw @ e) * np.abs(o[i, h])
-            flat = np.repeat(at.sum() * 2.0 ** -24 * 16 * big + (L + D) * u * 30 * (pw @ vh), w)
-            out[i, h] = per + flat
-    return out
+        return np.zeros((n, Hq, D))
+    any_sees = seen.any(0)                                    # what is out of sight may be anything
+    k, v = (np.where(any_sees[:, None, None], np.abs(a), 0.0) for a in (k, v))
+    sk, sv = (a.reshape(L, H, D // w, w).max(-1) / 7 for a in (k, v))       # at least the scales
+    qa = np.abs(q).reshape(n, H, G, D // w, w).sum(-1)
+    A = abs(scale) * 30 * np.einsum("nhgc,lhc->nhgl", qa, sk)
+    p = p.reshape(n, H, G, L)
+    e = (2 * D + 12 + 4) * u * A + 2.0 ** -22
+    big = (p[..., None] * sv.transpose(1, 0, 2)[None, :, None]).max(3)      # [n, H, G, Gd]
+    per = np.einsum("nhgl,lhd->nhgd", p * (e + 2.0 ** -11), v) + (p * e).sum(-1)[..., None] * np.abs(o).reshape(n, H, G, D)
+    seen_by = seen.sum(-1)[:, None, None, None]
+    flat = seen_by * 2.0 ** -24 * 16 * big + (L + D) * u * 30 * np.einsum("nhgl,lhc->nhgc", p, sv)
+    return (per + np.repeat(flat, w, -1)).reshape(n, Hq, D)

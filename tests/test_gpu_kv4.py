@@ -193,6 +193,21 @@ ATTEND = [
     (128, 64, 1, 4, "bf16", [257], None, 257, 0, 0),
     (64, 16, 1, 1, "f16", [130], None, 130, 1, 0),                        # only itself
     (128, 32, 1, 1, "bf16", [40], None, 1, 1, 64),
+    # many rows of a sequence: the prompt kernel's tiles, 128 rows or 256
+    (128, 16, 2, 2, "bf16", [333, 200], None, 190, 0, 0),
+    (128, 64, 1, 8, "f16", [100, 1000], None, 65, 0, 0),
+    (128, 256, 3, 3, "f16", [129], None, 129, 0, 0),
+    (64, 32, 2, 6, "bf16", [150, 400], None, 45, 0, 0),
+    (64, 64, 1, 2, "f16", [600], None, 300, 64, 8),
+    (256, 16, 1, 2, "f16", [260], None, 100, 0, 0),
+    (256, 64, 2, 4, "bf16", [300, 500], None, 77, 130, 70),
+    (128, 32, 1, 4, "f16", [2000], None, 50, 333, 4),                     # first positions far from the window
+    (128, 64, 1, 1, "bf16", [200], None, 200, 1, 0),
+    (128, 64, 1, 1, "f16", [700], None, 300, 100, 600),                   # first positions reach into the window
+    (128, 64, 2, 2, "bf16", [60, 500], None, 100, 0, 0),                  # rows ahead of position 0
+    (128, 32, 2, 4, "f16", [400, 9, 300, 50, 333], [0, 200, 201, 203, 253, 353], 0, 0, 0),   # rows for both kernels
+    (64, 16, 256, 256, "f16", [257], None, 257, 0, 0),
+    (128, 64, 256, 256, "bf16", [300], None, 257, 90, 3),
 ]
 
 
@@ -236,43 +251,47 @@ def test_attend(case):
 @pytest.mark.parametrize("q_scale,kv_scale", [(1e-6, 1.0), (300.0, 1e-3), (1.0, 1e-20), (1e-3, 1e4)])
 def test_attend_scales(q_scale, kv_scale):
     """Queries and values far from 1; the scores stay within a few hundred."""
-    case = (128, 32, 2, 4, "bf16", [300, 45], None, 2, 0, 0)
-    check_attend(*run_attend(case, q_scale=q_scale, kv_scale=kv_scale, scale=0.09 / (q_scale * kv_scale)))
+    for n in (2, 45):
+        case = (128, 32, 2, 4, "bf16", [300, 45], None, n, 0, 0)
+        check_attend(*run_attend(case, q_scale=q_scale, kv_scale=kv_scale, scale=0.09 / (q_scale * kv_scale)))
 
 
-def test_attend_sharp_and_negative_scale():
+@pytest.mark.parametrize("n", [3, 64])
+def test_attend_sharp_and_negative_scale(n):
     """Scores hundreds apart, both ways round: the running bound rises by large steps."""
     for scale in (20.0, -20.0):
-        got, want, bound, fin, own = run_attend((128, 16, 1, 4, "f16", [900, 64], None, 3, 0, 0), scale=scale)
+        got, want, bound, fin, own = run_attend((128, 16, 1, 4, "f16", [900, 64], None, n, 0, 0), scale=scale)
         # the weights' own errors grow with the scores and are in the bound; the norm's share is not
         worst = np.abs(got - want) - (fin.eps / 2 * (np.abs(want) + bound) + bound + 1e-7)
         assert (worst <= 0).all()
 
 
-def test_attend_large_values_with_small_weights():
+@pytest.mark.parametrize("D,n", [(128, 4), (128, 90), (256, 90)])
+def test_attend_large_values_with_small_weights(D, n):
     """Some positions have values 2^30 times the others' and next to no weight,
     ahead of and behind those that decide."""
     def edit(pages, table):
-        c = 128 // 8
+        c, groups = D // 8, 32 * (D // 128)
         for i in range(pages.shape[0]):
-            first = 2 * 32 * c + 32                       # value groups of 32 positions
-            w = pages[i, :, first:first + 32].copy()
+            first = 2 * 32 * c + groups                   # value groups of 32 positions
+            w = pages[i, :, first:first + groups].copy()
             s = (w & np.uint32(0xFFFF0000)).view(np.float32) * np.float32(2.0 ** (30 if i % 2 else -3))
-            pages[i, :, first:first + 32] = s.view(np.uint32) | (w & np.uint32(15))
+            pages[i, :, first:first + groups] = s.view(np.uint32) | (w & np.uint32(15))
             f = 2 * 32 * c                                # key groups: large-valued pages score far lower
-            w = pages[i, :, f:f + 32].copy()
+            w = pages[i, :, f:f + groups].copy()
             s = (w & np.uint32(0xFFFF0000)).view(np.float32) * np.float32(2.0 ** (-6 if i % 2 else 0))
-            pages[i, :, f:f + 32] = s.view(np.uint32) | (w & np.uint32(15))
-    got, want, bound, fin, own = run_attend((128, 32, 1, 4, "bf16", [600], None, 4, 0, 0), q_scale=30.0, edit=edit)
+            pages[i, :, f:f + groups] = s.view(np.uint32) | (w & np.uint32(15))
+    got, want, bound, fin, own = run_attend((D, 32, 1, 4, "bf16", [600], None, n, 0, 0), q_scale=30.0, edit=edit)
     worst = np.abs(got - want) - (fin.eps / 2 * (np.abs(want) + bound) + bound)
     assert (worst <= 0).all()
 
 
-def test_attend_out_of_sight():
+@pytest.mark.parametrize("n", [3, 40])
+def test_attend_out_of_sight(n):
     """NaN, infinite and huge groups, and table entries of no page, where no row
     may look: behind the last position, outside the window, in other pages."""
     D, page = 128, 32
-    case = (D, page, 2, 4, "bf16", [70, 400], None, 3, 50, 2)
+    case = (D, page, 2, 4, "bf16", [70, 400], None, n, 50, 2)
     c = D // 8
 
     def edit(pages, table):
@@ -282,18 +301,19 @@ def test_attend_out_of_sight():
                 pages[i, :, 2 * page * c + pos % page] = word
                 pages[i, :, 2 * page * c + page + pos % page] = word
         spoil(0, 70, 96, np.uint32(0x7FC00000))
-        spoil(0, 2, 70 - 3 - 50 + 1, np.uint32(0x7F800000))
+        spoil(0, 2, max(2, 70 - n - 50 + 1), np.uint32(0x7F800000))
         spoil(1, 400, 416, np.uint32(0x7F7F000F))
-        spoil(1, 2, 345, np.uint32(0xFFC00000))
-        table[1, 2:10] = np.array([-1, 10 ** 9, -7, 2 ** 31 - 1, -2 ** 31, 77, -1, 99], np.int64).astype(np.int32)
+        spoil(1, 2, 400 - n - 50 + 1, np.uint32(0xFFC00000))
+        table[1, 2:9] = np.array([-1, 10 ** 9, -7, 2 ** 31 - 1, -2 ** 31, 77, -1], np.int64).astype(np.int32)
         spare = set(range(pages.shape[0])) - set(table.flatten().tolist())
         for i in spare:
             pages[i] = 0xFFFFFFFF
     check_attend(*run_attend(case, edit=edit))
 
 
-def test_attend_rows_that_see_nothing_or_nan():
-    D, page = 64, 16
+@pytest.mark.parametrize("D,Hq", [(64, 1), (64, 2), (256, 2)])
+def test_attend_rows_that_see_nothing_or_nan(D, Hq):
+    page, gd = 16, max(1, D // 128)
     c = D // 8
 
     def edit(pages, table):
@@ -301,9 +321,10 @@ def test_attend_rows_that_see_nothing_or_nan():
         i = table[1, 1]
         pages[i, :, 2 * page * c + 3] = 0x7FC00000         # a key of position 19
         i = table[2, 2]
-        pages[i, :, 2 * page * c + page + 5] = 0x7FC00000  # a value of position 37
-    got, want, bound, fin, own = run_attend((D, page, 1, 2, "f16", [40, 40, 40], None, 40, 0, 0), edit=edit)
-    got, want = got.reshape(3, 40, 2, D), want.reshape(3, 40, 2, D)
+        for g in range(gd):
+            pages[i, :, 2 * page * c + (gd + g) * page + 5] = 0x7FC00000  # a value of position 37
+    got, want, bound, fin, own = run_attend((D, page, 1, Hq, "f16", [40, 40, 40], None, 40, 0, 0), edit=edit)
+    got, want = got.reshape(3, 40, Hq, D), want.reshape(3, 40, Hq, D)
     assert (got[0] == 0).all()
     for b, first in ((1, 19), (2, 37)):
         assert np.isnan(got[b, first:]).all() and np.isfinite(got[b, :first]).all()
@@ -328,3 +349,19 @@ def test_attend_past_the_page_table():
         for r in range(3, 6):
             want, _ = kv4.attend(q[r:r + 1].double().numpy(), k, v, seen, D ** -0.5)
             assert np.linalg.norm(got[r] - want[0]) <= (2.0 ** -8 + 2.0 ** -10) * np.linalg.norm(want[0])
+
+
+@pytest.mark.parametrize("n", [1, 80])
+def test_no_pages(n):
+    """An empty pool, and an empty page table: nothing is stored, seen or read back."""
+    D, H = 128, 2
+    for P, W in ((0, 3), (2, 0)):
+        pages = qg.kv_u4_pages(P, H, 32, D)
+        table, lengths = torch.zeros((1, W), dtype=torch.int32, device=DEV), torch.tensor([96], dtype=torch.int32, device=DEV)
+        x = torch.randn((n, 4 * H, D), device=DEV).half()
+        q, k, v = x.split([2 * H, H, H], 1)
+        got = qg.append_kv_u4_pages(k, v, pages, table, lengths, q=q)
+        assert torch.equal(got, q) and (pages == 0).all()
+        assert (qg.attend_kv_u4_pages(got, pages, table, lengths) == 0).all()
+        for x in qg.dequantize_kv_u4_pages(pages, table, lengths, n, D):
+            assert (x == 0).all()
