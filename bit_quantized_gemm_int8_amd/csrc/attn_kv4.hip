@@ -558,11 +558,12 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     if (uniform) return B * up(rows / B, tile);
     return std::min(std::min(rows, rows / tile + B), most == 0 ? rows : B * up(most, tile));
   };
-  const bool few = !uniform || rows / B <= kFewRows, many = uniform ? !few : rows > kFewRows;
+  const bool wide = D == 256;   // all rows here
+  const bool few = wide || !uniform || rows / B <= kFewRows, many = !wide && (uniform ? !few : rows > kFewRows);
   if (few) {
     // 16 rows a tile where a sequence has no more on average, else 32
     a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
-    a.few_tiles = tiles(a.few_rows, kFewRows);
+    a.few_tiles = tiles(a.few_rows, wide ? 0 : kFewRows);
     // splits of the cached positions: enough workgroups for the GPU, at least 256 positions each
     const int64_t want = up(2048, a.few_tiles * H);
     a.splits = (int)std::max<int64_t>(1, std::min(want, capacity / 256));
@@ -614,7 +615,7 @@ hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hi
   p.s = s;
   p.a = a;
   p.G = a.Hq / s.H;
-  p.max_rows = kFewRows;
+  p.max_rows = plan.many_tiles > 0 || s.offsets != nullptr && a.D < 256 ? kFewRows : (int64_t)1 << 40;
   p.splits = plan.splits;
   const int64_t tiles = plan.few_tiles * s.H;
   p.part_o = (float*)a.workspace;

@@ -1,25 +1,33 @@
 // Attention of many query rows over the 4-bit paged KV cache (qg_kv4.hpp):
-// prompts and chunks of them.  The mathematics is that of attn_kv4.hip; here the
-// codes of 64 positions become binary16 values once for all rows of a workgroup.
+// prompts and chunks of them, heads of 64 and 128 channels.  The mathematics is
+// that of attn_kv4.hip; here the codes of 64 positions become binary16 values once
+// for all rows of a workgroup.
 //
-// A value (q - z) s has 11 significant bits.  Scaled by the power of two that
-// takes the tile's largest scale to [2^-9, 2^-8) it is exact in binary16 as long
-// as its own scale is no less than 2^-9 of that; and since a nibble masked out of
-// a code word is the binary16 subnormal n 2^-24, one packed fma makes two values,
-// n 2^-24 (s 2^24) - z s.  Positions with a smaller scale take their own power of
-// two, and a factor for the scores (keys) or weights (values) that the step's
-// general form applies.
+// A value (q - z) s has 11 significant bits.  Scaled by a power of two that takes s
+// to [2^-18, 2^-8) it is exact in binary16, and since a nibble masked out of a code
+// word is the binary16 subnormal n 2^-24, one packed fma makes two values,
+// n 2^-24 (s 2^24) - z s.  The power of two comes from the first tile's largest
+// scale (that one goes to [2^-13, 2^-12)); a position whose scale does not fit takes
+// its own, and the tile's weights are made in a general form that knows the factor.
 //
 // Both products have the query rows as columns, so that a lane has one query row
 // throughout: scores^T = K Q^T, outputs^T = V^T P^T, with the scores' registers
 // the second product's operand as they are (positions in the order of the lane).
-// Running bound and power of two of the weights as in attn_kv4.hip.  A step whose
-// positions all rows of a wave see, with no odd scales, takes the short form: one
-// fma, one exponential, one addition and half a conversion for each score, and a
-// check of the sums that sends what passed the bound to the general form.
+// A tile that all rows see, with no odd scales, costs one fma, one exponential, one
+// addition and half a conversion for each score; the weights' common factor changes
+// only where a row's sum of a tile passes 2^14.
+//
+// Two halves of the workgroup, one wave of each on every SIMD, take turns: while one
+// has the matrix cores (outputs of the last tile, scores of this one, and between
+// the products the unpacking of a later tile) the other makes weights.
+#include "qg_decode.hpp"
 #include "qg_kv4_attn.hpp"
 
 #include <algorithm>
+#include <type_traits>
+
+// a lambda that is called more than once is still part of the kernel: its captures stay in registers
+#define QG_INLINE __attribute__((always_inline))
 
 namespace qg {
 
@@ -30,22 +38,39 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 64;      // positions of a tile
+constexpr int kVBufs = 3;      // tiles of values at hand (two of keys)
 constexpr float kLow = -3.402823466e38f;
+constexpr float kUnset = 1e30f;
+constexpr u32 kHidden = 0xFFFFFFFFu;   // group word of a position that no row sees
 
-// What a tile's positions need besides their codes.
-template <int Gd>
-struct Kv4Marks {
-  // keys: 16 n 2^-24 and n 2^-24 to values, and -z s, each twice (two channels)
-  v4i key[kTile][Gd];
-  // values: the same for single positions
-  _Float16 s24[Gd][kTile], s20[Gd][kTile], z[Gd][kTile];
-  float fk[kTile];             // factor of the scores, -1: no page
-  float fv[Gd][kTile];         // factor of the weights
-  float ek, ev[Gd];            // powers of two of the tile's keys and values (exponents)
-  int odd[1 + Gd];             // some factor is not 1
+__device__ __forceinline__ int float_exp(u32 bits) { return (int)((bits >> 23) & 255u) - 127; }
+// 2^e for -252 <= e <= 254, in two factors where one would not be normal
+__device__ __forceinline__ float scale_by(float x, int e) { return ldexpf(x, e); }
+
+// A group's scale as the unpacked values have it: times 2^-(e + 9), or with its own
+// exponent in the place of e where that leaves [2^-18, 2^-8).  Scales below 2^-126
+// count as zero.
+struct Kv4Fit {
+  float v;
+  bool odd;
 };
+__device__ __forceinline__ Kv4Fit kv4_fit(u32 word, float f /* 2^-(e + 9) */) {
+  const u32 bits = word & 0xFFFF0000u;
+  const float a = __uint_as_float(bits) * f;
+  const bool zero = bits < 0x00800000u;
+  const bool fits = __float_as_uint(a) - 0x36800000u < 0x3B800000u - 0x36800000u;   // 2^-18 <= a < 2^-8
+  const float own = __uint_as_float((bits & 0x007FFFFFu) | 0x3B000000u);
+  return {zero ? 0.f : fits ? a : own, !(fits | zero)};
+}
 
-__device__ __forceinline__ int float_exp(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+// f(0), f(1), ... with constants for arguments
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    for_each<N, I + 1>(f);
+  }
+}
 
 }  // namespace
 
@@ -57,17 +82,18 @@ struct Kv4ManyArgs {
 };
 
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_kv4_attend_many(Kv4ManyArgs p) {
-  constexpr int NT = 64 * NW, kRows = 32 * NW, kGd = kv4_groups(D), kC = D / 8;   // code words of a position
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv4ManyArgs p) {
+  constexpr int NT = 64 * NW, kRows = 32 * NW, kC = D / 8;   // code words of a position
   constexpr int kSt = D / 16;        // steps of the first product
   constexpr int kDt = D / 32;        // channel tiles of the second
-  constexpr int kKl = (kTile * kC / 4 + NT - 1) / NT;   // 16-byte loads of key codes of a thread
-  constexpr int kVl = (kTile / 4 * kC + NT - 1) / NT;   // and of value codes
-  // [2][position / 32][word][position % 32] and [2][position / 32][step][half][channel], 16 bytes each
+  // values: [tile % bufs][position / 32][step][half][channel], keys: [tile % 2][position / 32]
+  // [word][position % 32], 16 bytes each; group words and flags of tiles
   extern __shared__ __align__(16) char lds[];
-  v4i* const kbuf = (v4i*)lds;
-  v4i* const vbuf = kbuf + 2 * kTile * kC;
-  Kv4Marks<kGd>* const marks = (Kv4Marks<kGd>*)(vbuf + 2 * kTile * kC);
+  v4i* const vbuf = (v4i*)lds;
+  v4i* const kbuf = vbuf + kVBufs * kTile * kC;
+  u32(*const kraw)[kTile] = (u32(*)[kTile])(kbuf + 2 * kTile * kC);   // [4]
+  u32(*const vraw)[kTile] = kraw + 4;
+  int* const flags = (int*)(vraw + 4);                                // [8], then the largest scales
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = p.s.H;
@@ -122,383 +148,435 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_kv4_attend_many(K
   for (int j = 0; j < kDt; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
-  float m = kLow, l = 0.f, rinv[kGd], lim[kGd];
-#pragma unroll
-  for (int g = 0; g < kGd; ++g) rinv[g] = lim[g] = 0.f;
+  float l = 0.f, sh = there ? kUnset : -kUnset;   // sum of the weights, exponent added to the scores
 
   // ---- loads of later tiles ----------------------------------------------------
-  // key codes: thread i of a tile has position i % 64 and words 4 (i / 64) ..;
-  // value codes: four positions 4 (i / kC) .. and word i % kC
+  // The first half of the workgroup brings the keys, the other half the values.
+  // Load n of a tile: key codes of position n % 64, words 4 (n / 64) ..; value codes
+  // of positions 4 (n / kC) .., word n % kC.
+  constexpr int NH = NT / 2, kN = kTile * kC / 4, kL = (kN + NH - 1) / NH;
+  const bool keys = wave < NW / 2;
+  const int htid = keys ? tid : tid - NH;
   const int n_tiles = span.tiles;
-  auto page_id = [&](int tile, int off) {
-    const int pi = (tile * kTile + off) >> shift;
-    return pi < W ? table[pi] : -1;
-  };
-  auto page_of = [&](int id) {
-    return (const char*)(p.s.pages + ((int64_t)((u32)id < (u32)p.s.P ? id : 0) * H + h) * page_words);
-  };
-  int kid[kKl], vid[kVl], mid = -1;
-  v4i kc[kKl], vc[kVl];
-  u32 mw[kGd];
-  const bool mark_k = wave == 0, mark_v = wave >= 1 && wave <= kGd;   // who makes the marks
-  auto fetch_ids = [&](int u) {
-    const int tile = span.tile(min(u, n_tiles - 1));
+  const char* const pool = (const char*)(p.s.pages + (int64_t)h * page_words);
+  const u32 page_step = (u32)H * (u32)page_words * 4u;   // < 2^32: 1024 heads of 256 positions of 136 bytes
+  const int inside = S < kTile ? S - 1 : kTile - 1;      // bits of a position that the thread holds
+  int off[kL], wat[kL];                                  // position in the tile; where its values go
+  u32 at_code[kL], at_word[kL];
 #pragma unroll
-    for (int i = 0; i < kKl; ++i) kid[i] = page_id(tile, (tid + i * NT) % kTile);
-#pragma unroll
-    for (int i = 0; i < kVl; ++i) vid[i] = page_id(tile, (tid + i * NT) / kC * 4 % kTile);
-  };
-  auto fetch_codes = [&](int u) {
-    const int tile = span.tile(min(u, n_tiles - 1));
-#pragma unroll
-    for (int i = 0; i < kKl; ++i) {
-      const int n = tid + i * NT, off = n % kTile;
-      if (kTile * kC / 4 % NT == 0 || n < kTile * kC / 4)
-        kc[i] = ld16(page_of(kid[i]) + ((tile * kTile + off) & (S - 1)) * (D / 2) + n / kTile * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kVl; ++i) {
-      const int n = tid + i * NT, off = n / kC * 4;
-      if (kTile / 4 * kC % NT == 0 || n < kTile / 4 * kC)
-        vc[i] = ld16(page_of(vid[i]) + S * (D / 2) + ((tile * kTile + off) & (S - 1)) * (D / 2) + n % kC * 16);
-    }
-  };
-  auto fetch_mark_id = [&](int u) {
-    if (mark_k || mark_v) mid = page_id(span.tile(min(u, n_tiles - 1)), lane);
-  };
-  int mid_now = -1;   // page of the words in mw
-  auto fetch_words = [&](int u) {
-    mid_now = mid;
-    if (!(mark_k || mark_v)) return;
-    const int slot = (span.tile(min(u, n_tiles - 1)) * kTile + lane) & (S - 1);
-    const u32* g = (const u32*)page_of(mid) + S * (D / 4) + slot;
-    if (mark_k) {
-#pragma unroll
-      for (int i = 0; i < kGd; ++i) mw[i] = g[i * S];
+  for (int i = 0; i < kL; ++i) {
+    const int n = (htid + i * NH) % kN;   // threads past the tile repeat it
+    off[i] = keys ? n % kTile : n / kC * 4;
+    at_code[i] = (off[i] & inside) * (D / 2) + (keys ? n / kTile * 16 : S * (D / 2) + n % kC * 16);
+    at_word[i] = S * D + (keys ? 0 : 4 * S) + (off[i] & inside) * 4;
+    if (keys) {
+      wat[i] = ((off[i] >> 5) * kC + n / kTile * 4) * 32 + (off[i] & 31);
     } else {
-      mw[0] = g[(kGd + wave - 1) * S];
+      // of 32 positions: quads 4 step + half and 4 step + 2 + half side by side; channel
+      // 8 w + j at place 8 j + w (64 channels) or 16 j + w
+      const int quad = n / kC, qq = quad & 7;
+      wat[i] = 2 * ((((quad >> 3) * 2 + (qq >> 2)) * 2 + (qq & 1)) * D + n % kC) + (qq >> 1 & 1);
+    }
+  }
+  int id[kL];
+  v4i code[kL], word[kL];   // word: of one position (keys) or four
+  bool page_ok[kL];
+  auto fetch_ids = [&](int tile) QG_INLINE {
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      const int pi = ((tile * kTile) >> shift) + (S < kTile ? off[i] >> shift : 0);
+      id[i] = table[min(pi, W - 1)];   // past the table: any page, the capacity hides it
     }
   };
-  // The marks of tile u from the words in mw.
-  auto mark = [&](int u) {
-    if (!(mark_k || mark_v)) return;
-    Kv4Marks<kGd>& out = marks[u % 3];
-    const int at = span.tile(min(u, n_tiles - 1)) * kTile + lane;
-    const bool page = (u32)mid_now < (u32)p.s.P && at < capacity;
-    const bool some = page && at <= p1 && (window <= 0 || at > p0 - window || at < sinks);   // some row sees it
-    float s[kGd];
-    u32 z[kGd];
-    bool nan = false;
-    float mine = 0.f;
+  auto fetch = [&](int tile) QG_INLINE {
+    const u32 slot0 = (u32)(tile * kTile) & (u32)(S - 1);
 #pragma unroll
-    for (int i = 0; i < kGd; ++i) {
-      s[i] = 0.f;
-      z[i] = 0;
-      if (i > 0 && !mark_k) continue;
-      const float v = some ? kv4_scale(mw[i]) : 0.f;
-      const bool bad = !(v < __builtin_inff());
-      nan |= bad;
-      s[i] = bad ? 0.f : v;
-      z[i] = some ? mw[i] & 15u : 0u;
-      mine = fmaxf(mine, s[i]);
+    for (int i = 0; i < kL; ++i) {
+      page_ok[i] = (u32)id[i] < (u32)p.s.P;
+      const char* page = pool + (uint64_t)(page_ok[i] ? (u32)id[i] : 0u) * page_step;
+      code[i] = ld16(page + (slot0 * (D / 2) + at_code[i]));
+      // keys: the word of the position and three more, of which none is past the page's words
+      if (keys) word[i][0] = *(const int*)(page + (slot0 * 4 + at_word[i]));
+      else word[i] = ld16(page + (slot0 * 4 + at_word[i]));
     }
-    const float top = wave_max_nonneg(mine);
-    // scales below 2^-9 of the largest by their own power of two
-    const bool own = mine > 0.f && mine * 512.f < top;
-    const int et = float_exp(fmaxf(top, 0x1p-126f)), e = own ? float_exp(fmaxf(mine, 0x1p-126f)) : et;
-    const float f = own ? ldexpf(1.f, e - et) : 1.f;
-    const bool odd = __any(own || nan || !page);
-    if (mark_k) {
-#pragma unroll
-      for (int i = 0; i < kGd; ++i) {
-        const float v = nan ? __builtin_nanf("") : ldexpf(s[i], -e - 9);
-        const u32 a = f32_to_f16_bits(v * 0x1p24f), b = f32_to_f16_bits(v * 0x1p20f), d = f32_to_f16_bits(-(float)z[i] * v);
-        out.key[lane][i] = v4i{(int)(a * 0x10001u), (int)(b * 0x10001u), (int)(d * 0x10001u), 0};
-      }
-      out.fk[lane] = page ? f : -1.f;
-      if (lane == 0) {
-        out.ek = (float)et;
-        out.odd[0] = odd;
+  };
+  // positions of a tile that some row sees, or that lie between such
+  auto seen_from = [&](int tile) QG_INLINE {
+    const int t0 = tile * kTile;
+    return window > 0 && t0 >= sinks ? max(p0 - window + 1 - t0, 0) : 0;
+  };
+  auto seen_to = [&](int tile) QG_INLINE { return min(p1 + 1, capacity) - tile * kTile; };
+  float kf = 0.f, vf_ = 0.f;   // 2^-(e + 9) of keys and values
+  // The thread's codes -> values of a tile, number u.  True where a scale is odd.
+  const auto fma2 = [](u32 n, u32 s, u32 z) QG_INLINE {
+    return __builtin_bit_cast(int, __builtin_elementwise_fma(__builtin_bit_cast(v2h, n), __builtin_bit_cast(v2h, s),
+                                                             __builtin_bit_cast(v2h, z)));
+  };
+  const auto pair = [](float a, float b) QG_INLINE { return __builtin_bit_cast(u32, v2h{(_Float16)a, (_Float16)b}); };
+  // In pieces, for the places between the products: piece k of kPieces.
+  constexpr int kPieces = 4 * kDt + 2 * kSt;
+  u32 ks24[kL], ks20[kL], kz[kL];              // keys' constants
+  float sv[kL][4], sz[kL][4];                  // values'
+  v4i raw[kL];
+  bool odd = false;
+  int low = 0, high = 0;   // positions of the tile that some row sees
+  // scale and zero point of the key's position, or of one of the values' four
+  auto fit_key = [&](int i, int u) QG_INLINE {
+    const bool some = page_ok[i] & (off[i] >= low) & (off[i] < high);
+    const u32 w = (u32)word[i][0];
+    const Kv4Fit fit = kv4_fit(some ? w : 0u, kf);
+    odd |= fit.odd | !page_ok[i];
+    kraw[u & 3][off[i]] = some ? w : kHidden;
+    const float z = -(float)(w & 15u) * fit.v;
+    ks24[i] = pair(fit.v * 0x1p24f, fit.v * 0x1p24f);
+    ks20[i] = pair(fit.v * 0x1p20f, fit.v * 0x1p20f);
+    kz[i] = pair(z, z);
+  };
+  auto word_of_key = [&](int i, int j, int u) QG_INLINE {
+    const u32 x = (u32)code[i][j], hi = x >> 8;
+    (kbuf + (u & 1) * kTile * kC)[wat[i] + 32 * j] =
+        v4i{fma2(x & 0x000F000Fu, ks24[i], kz[i]), fma2(x & 0x00F000F0u, ks20[i], kz[i]),
+            fma2(hi & 0x000F000Fu, ks24[i], kz[i]), fma2(hi & 0x00F000F0u, ks20[i], kz[i])};
+  };
+  auto fit_value = [&](int i, int e) QG_INLINE {
+    const bool some = page_ok[i] & (off[i] + e >= low) & (off[i] + e < high);
+    const u32 w = (u32)word[i][e];
+    const Kv4Fit fit = kv4_fit(some ? w : 0u, vf_);
+    odd |= fit.odd;
+    raw[i][e] = (int)(some ? w : kHidden);
+    sv[i][e] = some & ((w & 0x7F800000u) == 0x7F800000u) ? 0.f : fit.v;   // NaN is the weights' business
+    sz[i][e] = -(float)(w & 15u) * sv[i][e];
+  };
+  // channels 4 hf .. 4 hf + 3 of the values' word, two of four (e) positions at a time
+  auto half_of_value = [&](int i, int hf, int j, int vb_at) QG_INLINE {
+    v2i* const vb = (v2i*)(vbuf + vb_at * kTile * kC);
+    constexpr int kStep = D == 64 ? 8 : 16;
+    const float up = j & 1 ? 0x1p20f : 0x1p24f;
+    const u32 sel = hf ? 0x07060302u : 0x05040100u, mask = j & 1 ? 0x00F000F0u : 0x000F000Fu;
+    const u32 x = __builtin_amdgcn_perm((u32)code[i][1], (u32)code[i][0], sel);
+    const u32 y = __builtin_amdgcn_perm((u32)code[i][3], (u32)code[i][2], sel);
+    vb[wat[i] + 2 * kStep * (4 * hf + j)] =
+        v2i{fma2((j & 2 ? x >> 8 : x) & mask, pair(sv[i][0] * up, sv[i][1] * up), pair(sz[i][0], sz[i][1])),
+            fma2((j & 2 ? y >> 8 : y) & mask, pair(sv[i][2] * up, sv[i][3] * up), pair(sz[i][2], sz[i][3]))};
+  };
+  auto piece = [&](auto role, auto at, int vb_at, int u) QG_INLINE {
+    constexpr bool KEYS = decltype(role)::value;
+    constexpr int k = decltype(at)::value;
+    if constexpr (KEYS) {
+      // a fit, then its four words, two places apart
+      constexpr int kEvery = kPieces / (5 * kL);
+      if constexpr (k % kEvery == 0 && k / kEvery < 5 * kL) {
+        constexpr int i = k / kEvery / 5, w = k / kEvery % 5;
+        if constexpr (w == 0) fit_key(i, u);
+        else word_of_key(i, w - 1, u);
       }
     } else {
-      const int g = wave - 1;
-      const float v = ldexpf(s[0], -e - 9);
-      out.s24[g][lane] = (_Float16)(v * 0x1p24f);
-      out.s20[g][lane] = (_Float16)(v * 0x1p20f);
-      out.z[g][lane] = (_Float16)(-(float)z[0] * v);
-      out.fv[g][lane] = nan ? __builtin_nanf("") : f;
-      if (lane == 0) {
-        out.ev[g] = (float)et;
-        out.odd[1 + g] = odd;
-      }
-    }
-  };
-  // Codes in kc, vc -> values of tile u.
-  auto unpack = [&](int u) {
-    const Kv4Marks<kGd>& mk = marks[u % 3];
-    v4i* const kb = kbuf + (u & 1) * kTile * kC;
-    v2i* const vb = (v2i*)(vbuf + (u & 1) * kTile * kC);
-    const auto fma2 = [](u32 n, u32 s, u32 z) {
-      return __builtin_bit_cast(int, __builtin_elementwise_fma(__builtin_bit_cast(v2h, n), __builtin_bit_cast(v2h, s),
-                                                               __builtin_bit_cast(v2h, z)));
-    };
-#pragma unroll
-    for (int i = 0; i < kKl; ++i) {
-      const int n = tid + i * NT, off = n % kTile, w0 = n / kTile * 4;
-      if (kTile * kC / 4 % NT != 0 && n >= kTile * kC / 4) continue;
-      const v4i par = mk.key[off][kGd > 1 ? w0 / 16 : 0];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32 w = (u32)kc[i][j], hi = w >> 8;
-        kb[((off >> 5) * kC + w0 + j) * 32 + (off & 31)] =
-            v4i{fma2(w & 0x000F000Fu, par[0], par[2]), fma2(w & 0x00F000F0u, par[1], par[2]),
-                fma2(hi & 0x000F000Fu, par[0], par[2]), fma2(hi & 0x00F000F0u, par[1], par[2])};
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kVl; ++i) {
-      const int n = tid + i * NT, quad = n / kC, word = n % kC;
-      if (kTile / 4 * kC % NT != 0 && n >= kTile / 4 * kC) continue;
-      const int g = kGd > 1 ? word / 16 : 0;
-      const v2i a = *(const v2i*)&mk.s24[g][4 * quad], b = *(const v2i*)&mk.s20[g][4 * quad], d = *(const v2i*)&mk.z[g][4 * quad];
-      // of 32 positions: quads 4 step + half and 4 step + 2 + half side by side
-      const int qq = quad & 7;
-      v2i* const to = vb + 2 * (((((quad >> 3) * 2 + (qq >> 2)) * 2 + (qq & 1)) * D + word % 16) + (kGd > 1 ? g * 128 : 0)) + (qq >> 1 & 1);
-      constexpr int kStep = D == 64 ? 8 : 16;   // channel 8 w + j at place kStep j + w of its 64 or 128
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const u32 sel = hf ? 0x07060302u : 0x05040100u;
-        const u32 x = __builtin_amdgcn_perm((u32)vc[i][1], (u32)vc[i][0], sel);
-        const u32 y = __builtin_amdgcn_perm((u32)vc[i][3], (u32)vc[i][2], sel);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32 mask = j & 1 ? 0x00F000F0u : 0x000F000Fu;
-          const v2i sc = j & 1 ? b : a;
-          to[2 * kStep * (4 * hf + j)] = v2i{fma2((j & 2 ? x >> 8 : x) & mask, sc[0], d[0]), fma2((j & 2 ? y >> 8 : y) & mask, sc[1], d[1])};
+      // four fits, then eight channels
+      constexpr int kEvery = kPieces / (12 * kL);
+      if constexpr (k % kEvery == 0 && k / kEvery < 12 * kL) {
+        constexpr int i = k / kEvery / 12, w = k / kEvery % 12;
+        if constexpr (w < 4) {
+          fit_value(i, w);
+          if constexpr (w == 3) *(v4i*)&vraw[u & 3][off[i]] = raw[i];
+        } else {
+          half_of_value(i, (w - 4) / 4, (w - 4) % 4, vb_at);
         }
       }
     }
+  };
+  auto unpack = [&](auto role, int tile, int vb_at, int u) QG_INLINE {
+    low = seen_from(tile);
+    high = seen_to(tile);
+    odd = false;
+    for_each<kPieces>([&](auto k) QG_INLINE { piece(role, k, vb_at, u); });
   };
 
-  // ---- one half tile of 32 positions ------------------------------------------------
-  auto half_tile = [&](int u, int sub, const Kv4Marks<kGd>& mk, bool simple) {
-    const v4i* const kb = kbuf + (u & 1) * kTile * kC + sub * kC * 32;
-    v16f s;
+  // ---- the products of a tile ------------------------------------------------------
+  v16f s[2];     // scores of the tile at hand
+  v8h pf[2][2];  // weights of the one before it
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = 0.f;
+  for (int i = 0; i < 4; ++i) pf[i >> 1][i & 1] = v8h{};
+  auto outputs = [&](int vb_at) QG_INLINE {
+    const v4i* const vb = vbuf + vb_at * kTile * kC + half * D + c;
 #pragma unroll
-    for (int j = 0; j < kSt; ++j)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, kb[(2 * j + half) * 32 + c]), q[j], s, 0, 0, 0);
-    const float ct = ldexpf(cc, (int)mk.ek);
-    v8h pf[kGd][2];
-    bool done = false;
-    if (simple) {
-      float rs[kGd];   // exponent of the weights' unit
-      bool fits = true;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int g = 0; g < kGd; ++g) {
-        rs[g] = mk.ev[g] + (float)float_exp(rinv[g]);
-        fits &= rinv[g] > 0.f && fabsf(rs[g]) <= 60.f;
+      for (int t = 0; t < 2 * kDt; ++t)
+        o[t % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(v8h, vb[i * kC * 32 + 2 * (t / kDt) * D + 32 * (t % kDt)]), pf[i][t / kDt], o[t % kDt], 0, 0, 0);
+  };
+
+  // Outputs of the last tile and scores of this one with the unpacking of a later one
+  // between the products.  Operands are read kAhead products ahead; the order is
+  // pinned, since the compiler's own reads each operand right before its product
+  // and waits for it (3300 cycles for the 32 products' 1024).
+  constexpr int kAhead = 6;
+  auto fused = [&](auto role, int tile, int vlast, int vb_at, int u) QG_INLINE {
+    const v4i* const vb = vbuf + vlast * kTile * kC + half * D + c;
+    const v4i* const kb = kbuf + (u & 1) * kTile * kC + half * 32 + c;
+    low = seen_from(tile);
+    high = seen_to(tile);
+    odd = false;
+    v4i ring[kAhead];
+    auto read = [&](auto at) QG_INLINE {
+      constexpr int k = decltype(at)::value;
+      if constexpr (k < 4 * kDt) {
+        constexpr int i = k / (2 * kDt), t = k % (2 * kDt);
+        ring[k % kAhead] = vb[i * kC * 32 + 2 * (t / kDt) * D + 32 * (t % kDt)];
+      } else if constexpr (k < kPieces) {
+        constexpr int i = (k - 4 * kDt) & 1, j = (k - 4 * kDt) >> 1;
+        ring[k % kAhead] = kb[(i * kC + 2 * j) * 32];
       }
-      if (__all(fits || !there)) {   // columns of no row may hold anything
-        const float shift0 = rs[0] - m;
-        float w[16], sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], ct, shift0));
-          sum += w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pf[0][e >> 3][e & 7] = (_Float16)w[e];
-        bool small = sum <= 0x1p14f;
-        if constexpr (kGd > 1) {
-          const float more = __builtin_amdgcn_exp2f(rs[kGd - 1] - rs[0]);
-          small &= sum * more <= 0x1p14f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pf[kGd - 1][e >> 3][e & 7] = (_Float16)(w[e] * more);
-        }
-        done = __all(small || !there);
-        if (done) l += sum * __builtin_amdgcn_exp2f(-rs[0]);
+    };
+    for_each<kAhead - 1>([&](auto k) QG_INLINE { read(k); });
+    __builtin_amdgcn_sched_barrier(0);
+    for_each<kPieces>([&](auto at) QG_INLINE {
+      constexpr int k = decltype(at)::value;
+      read(std::integral_constant<int, k + kAhead - 1>());
+      const v8h x = __builtin_bit_cast(v8h, ring[k % kAhead]);
+      if constexpr (k < 4 * kDt) {
+        constexpr int i = k / (2 * kDt), t = k % (2 * kDt);
+        o[t % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pf[i][t / kDt], o[t % kDt], 0, 0, 0);
+      } else {
+        constexpr int i = (k - 4 * kDt) & 1, j = (k - 4 * kDt) >> 1;
+        const v16f zero = {};
+        s[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[j], j ? s[i] : zero, 0, 0, 0);
       }
-    }
-    if (!done) {
+      piece(role, at, vb_at, u + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // ---- scores of a tile to weights -------------------------------------------------
+  // With x the scores in base 2 and e the exponents of the values' powers of two, the
+  // weights are exp2(x + e - ev + sh) for one sh of a row, which falls where their sum
+  // would pass 2^14, outputs and sum with it:  out = 2^(9 + ev) o / l.
+  int ek = 0, ev = 0;   // exponents of the common powers of two
+  float ct = 0.f;
+  // The row's sh down to `to`, where that is below it.
+  auto lower = [&](float to) QG_INLINE {
+    const float by = to < sh ? __builtin_amdgcn_exp2f(to - sh) : 1.f;   // 0 for a row's first tile
+    sh = fminf(sh, to);
+    l *= by;
+#pragma unroll
+    for (int j = 0; j < kDt; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[j][e] *= by;
+  };
+  auto both = [](float v) QG_INLINE { return fmaxf(v, __shfl_xor(v, 32, kWave)); };
+  auto weights = [&](int tile, int u, bool all, bool odd) QG_INLINE {
+    const int t0 = tile * kTile + 4 * half;
+    const u32 reach = window > 0 ? (u32)window : 0x7FFFFFFFu;
+    float by = ct;
+    if (odd) {
+      // any position may be out of sight, of no page, or of another power of two
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const v4i w = *(const v4i*)&kraw[u & 3][32 * i + 8 * a + 4 * half];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int at = t0 + 32 * i + 8 * a + b, e = 4 * a + b;
+            const bool seen = ((u32)w[b] != kHidden) & (((u32)(pos - at) < reach) | ((at < sinks) & (at <= pos)));
+            const bool nan = ((u32)w[b] & 0x7F800000u) == 0x7F800000u;
+            const float f = nan ? __builtin_nanf("") : kv4_fit((u32)w[b], kf).odd ? scale_by(1.f, float_exp((u32)w[b]) - ek) : 1.f;
+            s[i][e] = seen ? s[i][e] * ct * f : -__builtin_inff();
+          }
+          __builtin_amdgcn_sched_barrier(0);   // few words at a time: registers
+        }
+      // the sum of the exponentials here, since the values' powers of two differ
       float top = kLow;
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const v4f f = *(const v4f*)&mk.fk[32 * sub + 8 * a + 4 * half];
-        const int t0 = span.tile(u) * kTile + 32 * sub + 8 * a + 4 * half;
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
+      if (__any(top + sh > 60.f)) lower(60.f - both(top));
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int at = t0 + b;
-          const bool seen = f[b] >= 0.f && at <= pos && (window <= 0 || at > pos - window || at < sinks);
-          s[4 * a + b] = seen ? s[4 * a + b] * ct * f[b] : -__builtin_inff();
-          top = fmaxf(top, s[4 * a + b]);
-        }
-      }
-      float alpha = 1.f;
-      if (__any(top > m + 8.f)) {
-        const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, kWave)));
-        alpha = __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= alpha;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int g = 0; g < kGd; ++g) lim[g] = -1.f;
-      }
-      float w[kGd][16];
+        for (int a = 0; a < 4; ++a) {
+          const v4i w = *(const v4i*)&vraw[u & 3][32 * i + 8 * a + 4 * half];
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int e = 4 * a + b;
-          const bool seen = s[e] != -__builtin_inff();
-          const float pe = __builtin_amdgcn_exp2f(s[e] - m);
-          l += pe;
-#pragma unroll
-          for (int g = 0; g < kGd; ++g) {
-            const float f = mk.fv[g][32 * sub + 8 * a + 4 * half + b];
-            w[g][e] = seen ? pe * f : 0.f;
+          for (int b = 0; b < 4; ++b) {
+            const int e = 4 * a + b;
+            l += __builtin_amdgcn_exp2f(s[i][e] + sh);
+            const bool nan = ((u32)w[b] & 0x7F800000u) == 0x7F800000u;
+            const float f = nan ? __builtin_nanf("") : kv4_fit((u32)w[b], vf_).odd ? (float)(float_exp((u32)w[b]) - ev) : 0.f;
+            s[i][e] = s[i][e] == -__builtin_inff() ? s[i][e] : s[i][e] + f;   // whatever lies out of sight
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
+      by = 1.f;
+    } else if (!all) {
+      // some position is outside a row's window
+      const int back = pos - t0;
 #pragma unroll
-      for (int g = 0; g < kGd; ++g) {
-        const float tev = ldexpf(1.f, (int)mk.ev[g]);
-        float most = 0.f;
+      for (int e = 0; e < 32; ++e) {
+        const u32 d = (u32)(back - (32 * (e >> 4) + 8 * (e % 16 / 4) + e % 4));
+        s[e >> 4][e & 15] = d < reach ? s[e >> 4][e & 15] * ct : -__builtin_inff();
+      }
+      by = 1.f;
+    }
+#pragma unroll 1
+    while (true) {
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          w[g][e] *= tev;
-          most = fmaxf(most, w[g][e]);
-        }
-        if (__any(most > lim[g])) {
-          const bool set = rinv[g] > 0.f;
-          const float ref = set ? alpha / rinv[g] : 0.f;
-          const float all = fmaxf(fmaxf(most, __shfl_xor(most, 32, kWave)), ref);
-          const float big = fminf(fmaxf(all, 0x1p-100f), 0x1p100f);
-          const float f = __uint_as_float(0x7F000000u - (__float_as_uint(big) & 0x7F800000u));
-          const float by = set ? f * ref : 1.f;
-          rinv[g] = all > 0.f ? f : 0.f;
-          lim[g] = all > 0.f ? 0x1p12f / f : 0.f;
-#pragma unroll
-          for (int j = 0; j < kDt / kGd; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[g * (kDt / kGd) + j][e] *= by;
+          w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][e], by, sh));
+          part[e & 3] += w[e];
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) pf[g][e >> 3][e & 7] = (_Float16)(w[g][e] * rinv[g]);
+        for (int e = 0; e < 16; ++e) pf[i][e >> 3][e & 7] = (_Float16)w[e];
       }
+      const float sum = (part[0] + part[1]) + (part[2] + part[3]);
+      if (!__any(sum > 0x1p14f)) {   // a NaN stays one
+        if (!odd) l += sum;
+        break;
+      }
+      float top = kLow;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15] * by);
+      lower(-floorf(both(top)));
     }
-    const v4i* const vb = vbuf + (u & 1) * kTile * kC + sub * kC * 32;
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int j = 0; j < kDt; ++j) {
-        const v8h v = __builtin_bit_cast(v8h, vb[(2 * st + half) * D + 32 * j + c]);
-        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[kGd > 1 ? j / (kDt / kGd) : 0][st], o[j], 0, 0, 0);
-      }
   };
 
+  auto tile_at = [&](int u) QG_INLINE { return span.tile(min(u, n_tiles - 1)); };
   if (n_tiles > 0) {
-    fetch_ids(0);
-    fetch_mark_id(0);
-    fetch_codes(0);
-    fetch_words(0);
-    fetch_mark_id(1);
-    mark(0);
-    fetch_words(1);
-    fetch_mark_id(2);
-    __syncthreads();
-    unpack(0);
-    mark(1);
-    fetch_ids(1);
-    fetch_codes(1);
-    fetch_ids(2);
-    fetch_words(2);
-    fetch_mark_id(3);
-    __syncthreads();
-  }
-  for (int u = 0; u < n_tiles; ++u) {
-    if (u + 1 < n_tiles) {
-      unpack(u + 1);
-      mark(u + 2);
-      fetch_codes(u + 2);
-      fetch_ids(u + 3);
-      fetch_words(u + 3);
-      fetch_mark_id(u + 4);
-    }
-    const int t0 = span.tile(u) * kTile;
-    // something of the tile is in some row's sight
-    if (alive && t0 <= wp1 && (window <= 0 || t0 + kTile - 1 > wp0 - window || t0 < sinks)) {
-      const Kv4Marks<kGd>& mk = marks[u % 3];
-      bool odd = false;
+    // the first tile, and from its largest scales the common powers of two
+    fetch_ids(tile_at(0));
+    fetch(tile_at(0));
+    fetch_ids(tile_at(1));
+    if (tid < 8) flags[tid] = 0;
+    // the values ahead of the first tile's, which zero weights meet
+    for (int i = tid; i < kTile * kC; i += NT) vbuf[(kVBufs - 1) * kTile * kC + i] = v4i{0, 0, 0, 0};
+    float most = 0.f;
+    low = seen_from(tile_at(0));
+    high = seen_to(tile_at(0));
 #pragma unroll
-      for (int i = 0; i < 1 + kGd; ++i) odd |= mk.odd[i] != 0;
+    for (int i = 0; i < kL; ++i)
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int a = t0 + 32 * sub;
-        const bool simple = !odd && a + 31 <= wp0 && (window <= 0 || a > wp1 - window || a + 32 <= sinks);
-        half_tile(u, sub, mk, __builtin_amdgcn_readfirstlane(simple));
+      for (int e = 0; e < 4; ++e) {
+        if (keys && e > 0) continue;
+        const float v = kv4_scale((u32)word[i][e]);
+        if (page_ok[i] & (off[i] + e >= low) & (off[i] + e < high) & (v < __builtin_inff())) most = fmaxf(most, v);
       }
+    most = wave_max_nonneg(most);
+    float* const tops = (float*)(flags + 8);
+    if (lane == 0) tops[wave] = most;
+    __syncthreads();
+    float top_k = 0.f, top_v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW / 2; ++w) {
+      top_k = fmaxf(top_k, tops[w]);
+      top_v = fmaxf(top_v, tops[NW / 2 + w]);
     }
+    // room for scales 16 times as large and 64 times as small
+    ek = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_k))), -100), 100) + 4;
+    ev = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_v))), -100), 100) + 4;
+    kf = scale_by(1.f, -ek - 9);
+    vf_ = scale_by(1.f, -ev - 9);
+    ct = scale_by(cc, ek);
+    if (keys) unpack(std::true_type(), tile_at(0), 0, 0);
+    else unpack(std::false_type(), tile_at(0), 0, 0);
+    if (odd) flags[0] = 1;
+    fetch(tile_at(1));
+    fetch_ids(tile_at(2));
     __syncthreads();
   }
+  // In turn 2 u the first half has the products of tile u, in turn 2 u + 1 its
+  // weights; the second half runs one turn behind.  Keys of tile u + 1 are written by
+  // the first half between its products of tile u, into the buffer that the second
+  // half read last in the turn before; values of tile u + 1 by the second half
+  // between its products of tile u, into that of tile u - 2.
+  // Every turn has both products, so that the outputs stay in one place: where the
+  // wave sees nothing of a tile its weights are zeros (and the values are finite).
+  int vnow = 0;   // buffer of the tile's values
+  auto loop = [&](auto role) QG_INLINE {
+    constexpr bool KEYS = decltype(role)::value;
+    if constexpr (!KEYS) lds_barrier();
+    int now = tile_at(0), next = tile_at(1), third = tile_at(2);
+#pragma unroll 1
+    for (int u = 0; u < n_tiles; ++u) {
+      const int t0 = now * kTile, fourth = tile_at(u + 3);
+      const int vlast = vnow == 0 ? kVBufs - 1 : vnow - 1, vnext = vnow == kVBufs - 1 ? 0 : vnow + 1;
+      fused(role, next, vlast, vnext, u);
+      fetch(third);
+      fetch_ids(fourth);
+      if (odd) flags[(u + 1) & 7] = 1;
+      if (KEYS && tid == 0) flags[(u + 4) & 7] = 0;
+      const int is_odd = __builtin_amdgcn_readfirstlane(flags[u & 7]);
+      lds_barrier();
+      // something of the tile is in some row's sight
+      if (alive && t0 <= wp1 && (window <= 0 || t0 + kTile - 1 > wp0 - window || t0 < sinks)) {
+        const bool all = t0 + kTile - 1 <= wp0 && (window <= 0 || t0 > wp1 - window || t0 + kTile <= sinks);
+        // first positions that stay visible take the general form
+        weights(now, u, all, is_odd != 0 || (!all && window > 0 && t0 < sinks));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[i >> 1][i & 1] = v8h{};
+      }
+      now = next;
+      next = third;
+      third = fourth;
+      vnow = vnext;
+      lds_barrier();
+    }
+    if constexpr (KEYS) lds_barrier();
+  };
+  if (keys) loop(std::true_type());
+  else loop(std::false_type());
+  if (n_tiles > 0) outputs(vnow == 0 ? kVBufs - 1 : vnow - 1);
 
   // ---- outputs: lane (c, half) has, of row c, eight runs of 8 channels ---------------
   l += __shfl_xor(l, 32, kWave);
   if (!there) return;
   const int64_t to = ((int64_t)(t.token0 + row / p.G) * p.a.Hq + h * p.G + row % p.G) * D;
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const float f = ldexpf(inv, 9 + ev);
+  if constexpr (D == 64) {
+    // place 32 j + 8 a + 4 half + b holds channel 8 (place % 8) + place / 8
 #pragma unroll
-  for (int g = 0; g < kGd; ++g) {
-    const float f = rinv[g] > 0.f ? 512.f / rinv[g] * inv : 0.f;
-    constexpr int kPer = kDt / kGd;   // channel tiles of a group: 4, or 2 of 64 channels
-    if constexpr (D == 64) {
-      // place 32 j + 8 a + 4 half + b holds channel 8 (place % 8) + place / 8
+    for (int b = 0; b < 4; ++b) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) x[4 * j + a] = o[j][4 * a + b] * f;
+      kv4_store8<DT>(p.a.out, to + 32 * half + 8 * b, x);
+    }
+  } else {
+    // place 32 j + 8 a + 4 half + b holds channel 8 (place % 16) + place / 16
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) x[4 * j + a] = o[j][4 * a + b] * f;
-        kv4_store8<DT>(p.a.out, to + 32 * half + 8 * b, x);
-      }
-    } else {
-      // place 32 j + 8 a + 4 half + b holds channel 8 (place % 16) + place / 16
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            x[2 * j] = o[kPer * g + j][4 * a + b] * f;
-            x[2 * j + 1] = o[kPer * g + j][4 * (a + 2) + b] * f;
-          }
-          kv4_store8<DT>(p.a.out, to + 128 * g + 64 * a + 32 * half + 8 * b, x);
+        for (int j = 0; j < 4; ++j) {
+          x[2 * j] = o[j][4 * a + b] * f;
+          x[2 * j + 1] = o[j][4 * (a + 2) + b] * f;
         }
-    }
+        kv4_store8<DT>(p.a.out, to + 64 * a + 32 * half + 8 * b, x);
+      }
   }
 }
 
 namespace {
 
 template <int D>
-constexpr int many_lds() { return 2 * 2 * kTile * (D / 8) * 16 + 3 * (int)sizeof(Kv4Marks<kv4_groups(D)>); }
+constexpr int many_lds() { return (kVBufs + 2) * kTile * (D / 8) * 16 + 8 * kTile * 4 + 8 * 4 + 8 * 4; }
 
 template <int DT, int D, int NW>
 hipError_t many_t(Kv4ManyArgs p, hipStream_t st) {
-  constexpr int bytes = many_lds<D>();
-  static_assert(bytes <= 160 * 1024, "");
-  k_kv4_attend_many<DT, D, NW><<<(unsigned)(p.tiles * p.s.H), 64 * NW, bytes, st>>>(p);
+  k_kv4_attend_many<DT, D, NW><<<(unsigned)(p.tiles * p.s.H), 64 * NW, many_lds<D>(), st>>>(p);
   return hipGetLastError();
 }
 
 template <int DT, int NW>
 hipError_t many_d(const Kv4ManyArgs& p, hipStream_t st) {
-  switch (p.a.D) {
-    case 64: return many_t<DT, 64, NW>(p, st);
-    case 128: return many_t<DT, 128, NW>(p, st);
-    default: return many_t<DT, 256, 4>(p, st);
-  }
+  return p.a.D == 64 ? many_t<DT, 64, NW>(p, st) : many_t<DT, 128, NW>(p, st);
 }
 
 }  // namespace
