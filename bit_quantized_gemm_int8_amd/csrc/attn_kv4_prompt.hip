@@ -47,21 +47,24 @@ __device__ __forceinline__ int float_exp(u32 bits) { return (int)((bits >> 23) &
 // 2^e for -252 <= e <= 254, in two factors where one would not be normal
 __device__ __forceinline__ float scale_by(float x, int e) { return ldexpf(x, e); }
 
-// A group's scale as the unpacked values have it: times 2^-(e + 9), or with its own
-// exponent in the place of e where that leaves [2^-18, 2^-8).  Scales below 2^-126
-// count as zero.
+// A group's scale as the unpacked values have it, times 2^24: s 2^(15 - e), or with
+// its own exponent in the place of e where that leaves [2^6, 2^16).  A group of zeros
+// and one that is NaN have zero codes and zero points: any finite scale will do.
 struct Kv4Fit {
   float v;
   bool odd;
 };
-__device__ __forceinline__ Kv4Fit kv4_fit(u32 word, float f /* 2^-(e + 9) */) {
-  const u32 bits = word & 0xFFFF0000u;
-  const float a = __uint_as_float(bits) * f;
-  const bool zero = bits < 0x00800000u;
-  const bool fits = __float_as_uint(a) - 0x36800000u < 0x3B800000u - 0x36800000u;   // 2^-18 <= a < 2^-8
-  const float own = __uint_as_float((bits & 0x007FFFFFu) | 0x3B000000u);
-  return {zero ? 0.f : fits ? a : own, !(fits | zero)};
+__device__ __forceinline__ Kv4Fit kv4_fit(u32 word, float f /* 2^(15 - e) */) {
+  const float a = __uint_as_float(word & 0xFFFF0000u) * f;
+  const bool odd = __float_as_uint(a) - 0x42800000u >= 0x47800000u - 0x42800000u;   // 2^6 <= a < 2^16
+  return {odd ? __uint_as_float((word & 0x007F0000u) | 0x47000000u) : a, odd};
 }
+// two values in binary16
+__device__ __forceinline__ u32 pair_of(float a, float b) { return __builtin_bit_cast(u32, v2h{(_Float16)a, (_Float16)b}); }
+__device__ __forceinline__ u32 mul2(u32 a, u32 b) {
+  return __builtin_bit_cast(u32, __builtin_bit_cast(v2h, a) * __builtin_bit_cast(v2h, b));
+}
+constexpr u32 kSixteenth2 = 0x2C002C00u;   // 2^-4 twice
 
 // f(0), f(1), ... with constants for arguments
 template <int N, int I = 0, typename F>
@@ -206,58 +209,68 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     return window > 0 && t0 >= sinks ? max(p0 - window + 1 - t0, 0) : 0;
   };
   auto seen_to = [&](int tile) QG_INLINE { return min(p1 + 1, capacity) - tile * kTile; };
-  float kf = 0.f, vf_ = 0.f;   // 2^-(e + 9) of keys and values
+  float kf = 0.f, vf_ = 0.f;   // 2^(15 - e) of keys and values
   // The thread's codes -> values of a tile, number u.  True where a scale is odd.
   const auto fma2 = [](u32 n, u32 s, u32 z) QG_INLINE {
     return __builtin_bit_cast(int, __builtin_elementwise_fma(__builtin_bit_cast(v2h, n), __builtin_bit_cast(v2h, s),
                                                              __builtin_bit_cast(v2h, z)));
   };
-  const auto pair = [](float a, float b) QG_INLINE { return __builtin_bit_cast(u32, v2h{(_Float16)a, (_Float16)b}); };
   // In pieces, for the places between the products: piece k of kPieces.
   constexpr int kPieces = 4 * kDt + 2 * kSt;
-  u32 ks24[kL], ks20[kL], kz[kL];              // keys' constants
-  float sv[kL][4], sz[kL][4];                  // values'
-  v4i raw[kL];
+  u32 s24[kL][2], s20[kL][2], zz[kL][2];   // constants: of the keys' position, or of the values' two pairs
+  float sv[kL][4];
   bool odd = false;
-  int low = 0, high = 0;   // positions of the tile that some row sees
-  // scale and zero point of the key's position, or of one of the values' four
+  // Positions that no row sees, or of no page, ahead of the unpacking: their words are
+  // marked (and read as a scale that is odd).
+  auto mark = [&](auto role, int tile) QG_INLINE {
+    constexpr bool KEYS = decltype(role)::value;
+    const int low = seen_from(tile), high = seen_to(tile);
+    bool pages = true;
+#pragma unroll
+    for (int i = 0; i < kL; ++i) pages &= page_ok[i];
+    if (low <= 0 && high >= kTile && __all(pages)) return;
+#pragma unroll
+    for (int i = 0; i < kL; ++i)
+#pragma unroll
+      for (int e = 0; e < (KEYS ? 1 : 4); ++e)
+        if (!(page_ok[i] & (off[i] + e >= low) & (off[i] + e < high))) word[i][e] = (int)kHidden;
+  };
   auto fit_key = [&](int i, int u) QG_INLINE {
-    const bool some = page_ok[i] & (off[i] >= low) & (off[i] < high);
     const u32 w = (u32)word[i][0];
-    const Kv4Fit fit = kv4_fit(some ? w : 0u, kf);
-    odd |= fit.odd | !page_ok[i];
-    kraw[u & 3][off[i]] = some ? w : kHidden;
-    const float z = -(float)(w & 15u) * fit.v;
-    ks24[i] = pair(fit.v * 0x1p24f, fit.v * 0x1p24f);
-    ks20[i] = pair(fit.v * 0x1p20f, fit.v * 0x1p20f);
-    kz[i] = pair(z, z);
+    const Kv4Fit fit = kv4_fit(w, kf);
+    odd |= fit.odd;
+    kraw[u & 3][off[i]] = w;
+    s24[i][0] = pair_of(fit.v, fit.v);
+    s20[i][0] = mul2(s24[i][0], kSixteenth2);
+    zz[i][0] = mul2(s24[i][0], (w & 15u) * 0x10001u) ^ 0x80008000u;   // z is z 2^-24 as it stands
   };
   auto word_of_key = [&](int i, int j, int u) QG_INLINE {
     const u32 x = (u32)code[i][j], hi = x >> 8;
     (kbuf + (u & 1) * kTile * kC)[wat[i] + 32 * j] =
-        v4i{fma2(x & 0x000F000Fu, ks24[i], kz[i]), fma2(x & 0x00F000F0u, ks20[i], kz[i]),
-            fma2(hi & 0x000F000Fu, ks24[i], kz[i]), fma2(hi & 0x00F000F0u, ks20[i], kz[i])};
+        v4i{fma2(x & 0x000F000Fu, s24[i][0], zz[i][0]), fma2(x & 0x00F000F0u, s20[i][0], zz[i][0]),
+            fma2(hi & 0x000F000Fu, s24[i][0], zz[i][0]), fma2(hi & 0x00F000F0u, s20[i][0], zz[i][0])};
   };
   auto fit_value = [&](int i, int e) QG_INLINE {
-    const bool some = page_ok[i] & (off[i] + e >= low) & (off[i] + e < high);
-    const u32 w = (u32)word[i][e];
-    const Kv4Fit fit = kv4_fit(some ? w : 0u, vf_);
+    const Kv4Fit fit = kv4_fit((u32)word[i][e], vf_);
     odd |= fit.odd;
-    raw[i][e] = (int)(some ? w : kHidden);
-    sv[i][e] = some & ((w & 0x7F800000u) == 0x7F800000u) ? 0.f : fit.v;   // NaN is the weights' business
-    sz[i][e] = -(float)(w & 15u) * sv[i][e];
+    sv[i][e] = fit.v;
+    if (e & 1) {
+      const int t = e >> 1;
+      s24[i][t] = pair_of(sv[i][e - 1], sv[i][e]);
+      s20[i][t] = mul2(s24[i][t], kSixteenth2);
+      zz[i][t] = mul2(s24[i][t], ((u32)word[i][e - 1] & 15u) | (((u32)word[i][e] & 15u) << 16)) ^ 0x80008000u;
+    }
   };
-  // channels 4 hf .. 4 hf + 3 of the values' word, two of four (e) positions at a time
-  auto half_of_value = [&](int i, int hf, int j, int vb_at) QG_INLINE {
+  // channel 4 hf + j of the values' word, at four positions
+  auto channel_of_value = [&](int i, int hf, int j, int vb_at) QG_INLINE {
     v2i* const vb = (v2i*)(vbuf + vb_at * kTile * kC);
     constexpr int kStep = D == 64 ? 8 : 16;
-    const float up = j & 1 ? 0x1p20f : 0x1p24f;
     const u32 sel = hf ? 0x07060302u : 0x05040100u, mask = j & 1 ? 0x00F000F0u : 0x000F000Fu;
     const u32 x = __builtin_amdgcn_perm((u32)code[i][1], (u32)code[i][0], sel);
     const u32 y = __builtin_amdgcn_perm((u32)code[i][3], (u32)code[i][2], sel);
     vb[wat[i] + 2 * kStep * (4 * hf + j)] =
-        v2i{fma2((j & 2 ? x >> 8 : x) & mask, pair(sv[i][0] * up, sv[i][1] * up), pair(sz[i][0], sz[i][1])),
-            fma2((j & 2 ? y >> 8 : y) & mask, pair(sv[i][2] * up, sv[i][3] * up), pair(sz[i][2], sz[i][3]))};
+        v2i{fma2((j & 2 ? x >> 8 : x) & mask, j & 1 ? s20[i][0] : s24[i][0], zz[i][0]),
+            fma2((j & 2 ? y >> 8 : y) & mask, j & 1 ? s20[i][1] : s24[i][1], zz[i][1])};
   };
   auto piece = [&](auto role, auto at, int vb_at, int u) QG_INLINE {
     constexpr bool KEYS = decltype(role)::value;
@@ -277,16 +290,15 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
         constexpr int i = k / kEvery / 12, w = k / kEvery % 12;
         if constexpr (w < 4) {
           fit_value(i, w);
-          if constexpr (w == 3) *(v4i*)&vraw[u & 3][off[i]] = raw[i];
+          if constexpr (w == 3) *(v4i*)&vraw[u & 3][off[i]] = word[i];
         } else {
-          half_of_value(i, (w - 4) / 4, (w - 4) % 4, vb_at);
+          channel_of_value(i, (w - 4) / 4, (w - 4) % 4, vb_at);
         }
       }
     }
   };
   auto unpack = [&](auto role, int tile, int vb_at, int u) QG_INLINE {
-    low = seen_from(tile);
-    high = seen_to(tile);
+    mark(role, tile);
     odd = false;
     for_each<kPieces>([&](auto k) QG_INLINE { piece(role, k, vb_at, u); });
   };
@@ -311,11 +323,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   // pinned, since the compiler's own reads each operand right before its product
   // and waits for it (3300 cycles for the 32 products' 1024).
   constexpr int kAhead = 6;
-  auto fused = [&](auto role, int tile, int vlast, int vb_at, int u) QG_INLINE {
+  auto fused = [&](auto role, int tile, int third, int fourth, int vlast, int vb_at, int u) QG_INLINE {
     const v4i* const vb = vbuf + vlast * kTile * kC + half * D + c;
     const v4i* const kb = kbuf + (u & 1) * kTile * kC + half * 32 + c;
-    low = seen_from(tile);
-    high = seen_to(tile);
     odd = false;
     v4i ring[kAhead];
     auto read = [&](auto at) QG_INLINE {
@@ -343,6 +353,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
         s[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[j], j ? s[i] : zero, 0, 0, 0);
       }
       piece(role, at, vb_at, u + 1);
+      if constexpr (k == kPieces - 2) {   // the codes are used: the next ones
+        fetch(third);
+        fetch_ids(fourth);
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -416,8 +430,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       }
       by = 1.f;
     }
+    // The second round's sums pass: then s + sh is below 1 for every score, and the
+    // rounding of the largest one's is the same here as in `top`.
 #pragma unroll 1
-    while (true) {
+    for (int round = 0; round < 2; ++round) {
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -431,13 +447,17 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
         for (int e = 0; e < 16; ++e) pf[i][e >> 3][e & 7] = (_Float16)w[e];
       }
       const float sum = (part[0] + part[1]) + (part[2] + part[3]);
-      if (!__any(sum > 0x1p14f)) {   // a NaN stays one
+      if (round > 0 || !__any(sum > 0x1p14f)) {   // a NaN stays one
         if (!odd) l += sum;
         break;
       }
       float top = kLow;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15] * by);
+      for (int e = 0; e < 32; ++e) {
+        s[e >> 4][e & 15] *= by;
+        top = fmaxf(top, s[e >> 4][e & 15]);
+      }
+      by = 1.f;
       lower(-floorf(both(top)));
     }
   };
@@ -452,8 +472,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     // the values ahead of the first tile's, which zero weights meet
     for (int i = tid; i < kTile * kC; i += NT) vbuf[(kVBufs - 1) * kTile * kC + i] = v4i{0, 0, 0, 0};
     float most = 0.f;
-    low = seen_from(tile_at(0));
-    high = seen_to(tile_at(0));
+    const int low = seen_from(tile_at(0)), high = seen_to(tile_at(0));
 #pragma unroll
     for (int i = 0; i < kL; ++i)
 #pragma unroll
@@ -475,12 +494,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     // room for scales 16 times as large and 64 times as small
     ek = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_k))), -100), 100) + 4;
     ev = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_v))), -100), 100) + 4;
-    kf = scale_by(1.f, -ek - 9);
-    vf_ = scale_by(1.f, -ev - 9);
+    kf = scale_by(1.f, 15 - ek);
+    vf_ = scale_by(1.f, 15 - ev);
     ct = scale_by(cc, ek);
     if (keys) unpack(std::true_type(), tile_at(0), 0, 0);
     else unpack(std::false_type(), tile_at(0), 0, 0);
-    if (odd) flags[0] = 1;
+    if (__any(odd)) flags[0] = 1;
     fetch(tile_at(1));
     fetch_ids(tile_at(2));
     __syncthreads();
@@ -501,12 +520,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     for (int u = 0; u < n_tiles; ++u) {
       const int t0 = now * kTile, fourth = tile_at(u + 3);
       const int vlast = vnow == 0 ? kVBufs - 1 : vnow - 1, vnext = vnow == kVBufs - 1 ? 0 : vnow + 1;
-      fused(role, next, vlast, vnext, u);
-      fetch(third);
-      fetch_ids(fourth);
-      if (odd) flags[(u + 1) & 7] = 1;
+      mark(role, next);
+      __builtin_amdgcn_s_setprio(1);
+      const int flag = flags[u & 7];   // complete since the last turn
+      fused(role, next, third, fourth, vlast, vnext, u);
+      __builtin_amdgcn_s_setprio(0);
+      if (__any(odd)) flags[(u + 1) & 7] = 1;
       if (KEYS && tid == 0) flags[(u + 4) & 7] = 0;
-      const int is_odd = __builtin_amdgcn_readfirstlane(flags[u & 7]);
+      const int is_odd = __builtin_amdgcn_readfirstlane(flag);
       lds_barrier();
       // something of the tile is in some row's sight
       if (alive && t0 <= wp1 && (window <= 0 || t0 + kTile - 1 > wp0 - window || t0 < sinks)) {

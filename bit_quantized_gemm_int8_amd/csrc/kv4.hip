@@ -34,7 +34,10 @@ __device__ __forceinline__ u32 kv4_group(float lo, float hi, float& s, float& r)
     s = 0.f;
     return kKv4Nan;
   }
-  if (!(s > 0.f)) return 0u;
+  if (!(s >= 0x1p-126f)) {   // subnormal scales count as zero: no kernel has to know them
+    s = 0.f;
+    return 0u;
+  }
   r = 1.f / s;
   const float z = fminf(rintf(-lo / s), 15.f);
   return __float_as_uint(s) | (u32)z;
@@ -45,7 +48,10 @@ __device__ __forceinline__ u32 kv4_group(float lo, float hi, float& s, float& r)
 // correctly rounded division there (as in sym_code_t, whose bound on the two's
 // distance holds here too).
 __device__ __forceinline__ u32 kv4_codes(const float (&x)[8], float s, float r, u32 word) {
-  if (!(s > 0.f)) return 0u;
+  if (!(s >= 0x1p-126f)) {   // subnormal scales count as zero: no kernel has to know them
+    s = 0.f;
+    return 0u;
+  }
   const float z = (float)(word & 15u);
   u32 out = 0;
 #pragma unroll

@@ -668,7 +668,8 @@ qg_status_t combine_experts(const void* rows, int rows_dtype, const int32_t* slo
  *   lo = min(0, min x);  hi = max(0, max x);  t = (hi - lo) / 15;
  *   s = t rounded up to 7 significant bits;  z = rne(-lo / s);
  *   q = clamp(rne(x / s) + z, 0, 15);        value = (q - z) s;
- *   all binary32, quotients correctly rounded.  A group of zeros gets s = 0.
+ *   all binary32, quotients correctly rounded.  A group of zeros, and one with s
+ *   below 2^-126, gets s = 0, z = 0 and q = 0.
  *   A group with a value that is not finite, or whose hi - lo is not, is stored
  *   as NaN: rows that see it are NaN, rows that do not see it are not touched.
  *   (q - z) s has at most 11 significant bits: exact in binary16 and binary32

@@ -7,7 +7,8 @@ grows.  Readings:
     group's range, so 0 <= z <= 15; the scale is rounded up to 7 significant
     bits, which keeps (q - z) s exact in 11;
   * decisions in binary32 with correctly rounded quotients, as everywhere here;
-  * a group with a value that is not finite is NaN;
+  * a scale below 2^-126 counts as zero; a group with a value that is not
+    finite is NaN;
   * pages, page table, lengths and offsets as the C header describes them.
 Attention and values are binary64.
 """
@@ -48,7 +49,7 @@ def quantize_groups(x: np.ndarray):
         bad |= ~np.isfinite(t)
         s = round_up_7(np.where(bad, np.float32(0), t))
     bad |= ~np.isfinite(s)
-    s = np.where(bad, np.float32(0), s)
+    s = np.where(bad | (s < np.float32(2.0 ** -126)), np.float32(0), s)
     d = np.where(s > 0, s, np.float32(1))
     z = np.where(s > 0, np.clip(np.rint(-lo / d), 0, 15), 0).astype(np.float32)
     q = np.clip(np.rint(g / d[..., None]) + z[..., None], 0, 15)
