@@ -97,6 +97,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   u32(*const kraw)[kTile] = (u32(*)[kTile])(kbuf + 2 * kTile * kC);   // [4]
   u32(*const vraw)[kTile] = kraw + 4;
   int* const flags = (int*)(vraw + 4);                                // [8], then the largest scales
+  float(*const own)[kTile] = (float(*)[kTile])(flags + 16) + 2 * (threadIdx.x >> 6);   // [2] of each wave
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = p.s.H;
@@ -165,13 +166,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   const u32 page_step = (u32)H * (u32)page_words * 4u;   // < 2^32: 1024 heads of 256 positions of 136 bytes
   const int inside = S < kTile ? S - 1 : kTile - 1;      // bits of a position that the thread holds
   int off[kL], wat[kL];                                  // position in the tile; where its values go
-  u32 at_code[kL], at_word[kL];
+  const char *code_at[kL], *word_at[kL];                 // of page 0
 #pragma unroll
   for (int i = 0; i < kL; ++i) {
     const int n = (htid + i * NH) % kN;   // threads past the tile repeat it
     off[i] = keys ? n % kTile : n / kC * 4;
-    at_code[i] = (off[i] & inside) * (D / 2) + (keys ? n / kTile * 16 : S * (D / 2) + n % kC * 16);
-    at_word[i] = S * D + (keys ? 0 : 4 * S) + (off[i] & inside) * 4;
+    code_at[i] = pool + ((off[i] & inside) * (D / 2) + (keys ? n / kTile * 16 : S * (D / 2) + n % kC * 16));
+    word_at[i] = pool + (S * D + (keys ? 0 : 4 * S) + (off[i] & inside) * 4);
     if (keys) {
       wat[i] = ((off[i] >> 5) * kC + n / kTile * 4) * 32 + (off[i] & 31);
     } else {
@@ -181,14 +182,15 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       wat[i] = 2 * ((((quad >> 3) * 2 + (qq >> 2)) * 2 + (qq & 1)) * D + n % kC) + (qq >> 1 & 1);
     }
   }
-  int id[kL];
+  int id[kL], page_of[kL];   // page of the thread's position; of it, in the tile
+#pragma unroll
+  for (int i = 0; i < kL; ++i) page_of[i] = S < kTile ? off[i] >> shift : 0;
   v4i code[kL], word[kL];   // word: of one position (keys) or four
   bool page_ok[kL];
   auto fetch_ids = [&](int tile) QG_INLINE {
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
-      const int pi = ((tile * kTile) >> shift) + (S < kTile ? off[i] >> shift : 0);
-      id[i] = table[min(pi, W - 1)];   // past the table: any page, the capacity hides it
+      id[i] = table[min(((tile * kTile) >> shift) + page_of[i], W - 1)];   // past the table: any page, the capacity hides it
     }
   };
   auto fetch = [&](int tile) QG_INLINE {
@@ -196,11 +198,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
       page_ok[i] = (u32)id[i] < (u32)p.s.P;
-      const char* page = pool + (uint64_t)(page_ok[i] ? (u32)id[i] : 0u) * page_step;
-      code[i] = ld16(page + (slot0 * (D / 2) + at_code[i]));
-      // keys: the word of the position and three more, of which none is past the page's words
-      if (keys) word[i][0] = *(const int*)(page + (slot0 * 4 + at_word[i]));
-      else word[i] = ld16(page + (slot0 * 4 + at_word[i]));
+      const uint64_t page = (uint64_t)(page_ok[i] ? (u32)id[i] : 0u) * page_step;
+      code[i] = ld16(code_at[i] + page + slot0 * (D / 2));
+      if (keys) word[i][0] = *(const int*)(word_at[i] + page + slot0 * 4);
+      else word[i] = ld16(word_at[i] + page + slot0 * 4);
     }
   };
   // positions of a tile that some row sees, or that lie between such
@@ -323,32 +324,36 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   // pinned, since the compiler's own reads each operand right before its product
   // and waits for it (3300 cycles for the 32 products' 1024).
   constexpr int kAhead = 6;
-  auto fused = [&](auto role, int tile, int third, int fourth, int vlast, int vb_at, int u) QG_INLINE {
-    const v4i* const vb = vbuf + vlast * kTile * kC + half * D + c;
-    const v4i* const kb = kbuf + (u & 1) * kTile * kC + half * 32 + c;
-    odd = false;
-    v4i ring[kAhead];
-    auto read = [&](auto at) QG_INLINE {
-      constexpr int k = decltype(at)::value;
-      if constexpr (k < 4 * kDt) {
-        constexpr int i = k / (2 * kDt), t = k % (2 * kDt);
-        ring[k % kAhead] = vb[i * kC * 32 + 2 * (t / kDt) * D + 32 * (t % kDt)];
-      } else if constexpr (k < kPieces) {
-        constexpr int i = (k - 4 * kDt) & 1, j = (k - 4 * kDt) >> 1;
-        ring[k % kAhead] = kb[(i * kC + 2 * j) * 32];
-      }
-    };
+  v4i ring[kAhead];
+  const v4i *vb = vbuf, *kb = kbuf;
+  auto read = [&](auto at) QG_INLINE {
+    constexpr int k = decltype(at)::value;
+    if constexpr (k < kPieces && k % 2 == 0) {
+      constexpr int i = k / 2 / (2 * kDt), t = k / 2 % (2 * kDt);
+      ring[k % kAhead] = vb[i * kC * 32 + 2 * (t / kDt) * D + 32 * (t % kDt)];
+    } else if constexpr (k < kPieces) {
+      constexpr int i = k / 2 & 1, j = k / 4;
+      ring[k % kAhead] = kb[(i * kC + 2 * j) * 32];
+    }
+  };
+  // The first operands of tile u's turn, ahead of the barrier in front of it.
+  auto read_ahead = [&](int vlast, int u) QG_INLINE {
+    vb = vbuf + vlast * kTile * kC + half * D + c;
+    kb = kbuf + (u & 1) * kTile * kC + half * 32 + c;
     for_each<kAhead - 1>([&](auto k) QG_INLINE { read(k); });
+  };
+  auto fused = [&](auto role, int third, int fourth, int vb_at, int u) QG_INLINE {
+    odd = false;
     __builtin_amdgcn_sched_barrier(0);
     for_each<kPieces>([&](auto at) QG_INLINE {
       constexpr int k = decltype(at)::value;
       read(std::integral_constant<int, k + kAhead - 1>());
       const v8h x = __builtin_bit_cast(v8h, ring[k % kAhead]);
-      if constexpr (k < 4 * kDt) {
-        constexpr int i = k / (2 * kDt), t = k % (2 * kDt);
+      if constexpr (k % 2 == 0) {
+        constexpr int i = k / 2 / (2 * kDt), t = k / 2 % (2 * kDt);
         o[t % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pf[i][t / kDt], o[t % kDt], 0, 0, 0);
       } else {
-        constexpr int i = (k - 4 * kDt) & 1, j = (k - 4 * kDt) >> 1;
+        constexpr int i = k / 2 & 1, j = k / 4;
         const v16f zero = {};
         s[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[j], j ? s[i] : zero, 0, 0, 0);
       }
@@ -383,21 +388,27 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     const u32 reach = window > 0 ? (u32)window : 0x7FFFFFFFu;
     float by = ct;
     if (odd) {
-      // any position may be out of sight, of no page, or of another power of two
+      // any position may be out of sight, of no page, or of another power of two:
+      // a lane finds its position's factors, for all lanes to read
+      {
+        const u32 wk = kraw[u & 3][lane], wv = vraw[u & 3][lane];
+        const float ke = (float)float_exp(wk), ve = (float)float_exp(wv);   // 128: not finite
+        const float nan = __builtin_nanf("");
+        own[0][lane] = wk == kHidden ? -1.f : ke == 128.f ? nan : kv4_fit(wk, kf).odd ? __builtin_amdgcn_exp2f(ke - (float)ek) : 1.f;
+        own[1][lane] = ve == 128.f ? nan : kv4_fit(wv, vf_).odd ? ve - (float)ev : 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const v4i w = *(const v4i*)&kraw[u & 3][32 * i + 8 * a + 4 * half];
+          const v4f f = *(const v4f*)&own[0][32 * i + 8 * a + 4 * half];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int at = t0 + 32 * i + 8 * a + b, e = 4 * a + b;
-            const bool seen = ((u32)w[b] != kHidden) & (((u32)(pos - at) < reach) | ((at < sinks) & (at <= pos)));
-            const bool nan = ((u32)w[b] & 0x7F800000u) == 0x7F800000u;
-            const float f = nan ? __builtin_nanf("") : kv4_fit((u32)w[b], kf).odd ? scale_by(1.f, float_exp((u32)w[b]) - ek) : 1.f;
-            s[i][e] = seen ? s[i][e] * ct * f : -__builtin_inff();
+            const bool seen = !(f[b] < 0.f) & (((u32)(pos - at) < reach) | ((at < sinks) & (at <= pos)));
+            s[i][e] = seen ? s[i][e] * ct * f[b] : -__builtin_inff();
           }
-          __builtin_amdgcn_sched_barrier(0);   // few words at a time: registers
+          __builtin_amdgcn_sched_barrier(0);   // few factors at a time: registers
         }
       // the sum of the exponentials here, since the values' powers of two differ
       float top = kLow;
@@ -408,14 +419,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const v4i w = *(const v4i*)&vraw[u & 3][32 * i + 8 * a + 4 * half];
+          const v4f f = *(const v4f*)&own[1][32 * i + 8 * a + 4 * half];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int e = 4 * a + b;
             l += __builtin_amdgcn_exp2f(s[i][e] + sh);
-            const bool nan = ((u32)w[b] & 0x7F800000u) == 0x7F800000u;
-            const float f = nan ? __builtin_nanf("") : kv4_fit((u32)w[b], vf_).odd ? (float)(float_exp((u32)w[b]) - ev) : 0.f;
-            s[i][e] = s[i][e] == -__builtin_inff() ? s[i][e] : s[i][e] + f;   // whatever lies out of sight
+            s[i][e] = s[i][e] == -__builtin_inff() ? s[i][e] : s[i][e] + f[b];   // whatever lies out of sight
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -430,8 +439,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       }
       by = 1.f;
     }
-    // The second round's sums pass: then s + sh is below 1 for every score, and the
-    // rounding of the largest one's is the same here as in `top`.
+    // The second round's sums pass: sh is then below minus the largest score, by more
+    // than rounding takes from either.
 #pragma unroll 1
     for (int round = 0; round < 2; ++round) {
       float part[4] = {0.f, 0.f, 0.f, 0.f};
@@ -453,12 +462,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       }
       float top = kLow;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        s[e >> 4][e & 15] *= by;
-        top = fmaxf(top, s[e >> 4][e & 15]);
-      }
-      by = 1.f;
-      lower(-floorf(both(top)));
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15] * by);
+      top = both(top);
+      lower(-floorf(top) - fabsf(top) * 0x1p-21f);
     }
   };
 
@@ -512,28 +518,33 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   // Every turn has both products, so that the outputs stay in one place: where the
   // wave sees nothing of a tile its weights are zeros (and the values are finite).
   int vnow = 0;   // buffer of the tile's values
+  // Tiles of this wave by their first position: from act0 on (or below sinks0) some
+  // row sees something; between all0 and all1 every row sees everything.
+  const int act0 = window > 0 ? wp0 - window + 2 - kTile : -0x7FFFFFFF, sinks0 = window > 0 ? sinks : 0;
+  const int all0 = window > 0 ? wp1 - window + 1 : 0, all1 = wp0 - kTile + 1;
+  const int act1 = alive ? wp1 : -1;
   auto loop = [&](auto role) QG_INLINE {
     constexpr bool KEYS = decltype(role)::value;
     if constexpr (!KEYS) lds_barrier();
     int now = tile_at(0), next = tile_at(1), third = tile_at(2);
+    read_ahead(kVBufs - 1, 0);
 #pragma unroll 1
     for (int u = 0; u < n_tiles; ++u) {
       const int t0 = now * kTile, fourth = tile_at(u + 3);
-      const int vlast = vnow == 0 ? kVBufs - 1 : vnow - 1, vnext = vnow == kVBufs - 1 ? 0 : vnow + 1;
+      const int vnext = vnow == kVBufs - 1 ? 0 : vnow + 1;
       mark(role, next);
       __builtin_amdgcn_s_setprio(1);
       const int flag = flags[u & 7];   // complete since the last turn
-      fused(role, next, third, fourth, vlast, vnext, u);
+      fused(role, third, fourth, vnext, u);
       __builtin_amdgcn_s_setprio(0);
       if (__any(odd)) flags[(u + 1) & 7] = 1;
-      if (KEYS && tid == 0) flags[(u + 4) & 7] = 0;
-      const int is_odd = __builtin_amdgcn_readfirstlane(flag);
+      if (KEYS && wave == 0) flags[(u + 4) & 7] = 0;
+      const bool is_odd = __builtin_amdgcn_readfirstlane(flag) != 0;
       lds_barrier();
-      // something of the tile is in some row's sight
-      if (alive && t0 <= wp1 && (window <= 0 || t0 + kTile - 1 > wp0 - window || t0 < sinks)) {
-        const bool all = t0 + kTile - 1 <= wp0 && (window <= 0 || t0 > wp1 - window || t0 + kTile <= sinks);
+      const bool all = t0 >= all0 && t0 <= all1;
+      if (t0 <= act1 && (t0 >= act0 || t0 < sinks0)) {
         // first positions that stay visible take the general form
-        weights(now, u, all, is_odd != 0 || (!all && window > 0 && t0 < sinks));
+        weights(now, u, all, is_odd || (!all && t0 < sinks0));
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) pf[i >> 1][i & 1] = v8h{};
@@ -541,8 +552,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       now = next;
       next = third;
       third = fourth;
+      read_ahead(vnow, u + 1);
       vnow = vnext;
-      lds_barrier();
+      asm volatile("s_barrier" ::: "memory");   // nothing was written since the last one
     }
     if constexpr (KEYS) lds_barrier();
   };
@@ -587,7 +599,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
 namespace {
 
 template <int D>
-constexpr int many_lds() { return (kVBufs + 2) * kTile * (D / 8) * 16 + 8 * kTile * 4 + 8 * 4 + 8 * 4; }
+constexpr int many_lds() { return (kVBufs + 2) * kTile * (D / 8) * 16 + 8 * kTile * 4 + 16 * 4 + 8 * 2 * kTile * 4; }
 
 template <int DT, int D, int NW>
 hipError_t many_t(Kv4ManyArgs p, hipStream_t st) {
