@@ -9,17 +9,18 @@
 // n 2^-20 one nibble up), which gfx950's matrix cores take exactly: unpacking
 // costs one AND for two codes.  Queries are scaled to binary16's upper range by
 // a power of two of their row, exactly for bfloat16 and binary16 inputs; the
-// weights p s are scaled by a power of two of their row and rounded to binary16
-// (half a step: 2^-11), the codes' sum and the zero points' sum taking the same
-// rounded weights, both through the matrix cores.  Softmax and sums: binary32.
+// weights p s are rounded to binary16 (half a step: 2^-11), the codes' sum and
+// the zero points' sum taking the same rounded weights, both through the matrix
+// cores.  Binary16 outputs, whose own rounding is no larger, get what the rounding
+// left over in a second product (2^-22).  Softmax and sums: binary32.
 //
-// Layout.  A wave takes 32 positions a step: the scores' product has positions
-// as rows and query rows as columns, so that a lane holds 4 neighbouring
-// positions of one query row for each half of the step -- which is the operand
-// the second product needs, with the positions in that order.  Value codes of 4
-// positions of a word are neighbours in the cache for the same reason.  No
-// lane exchange per step: the running maximum is a bound that is raised only
-// where a score passes it by 2^8.
+// Layout.  A wave takes 32 positions a step.  Both products have the query rows
+// as columns, so that a lane has one query row throughout: a lane's scores, 4
+// neighbouring positions in each half of the step, are the operand that the second
+// product needs, with the positions in that order.  Value codes of 4 positions of a
+// word are neighbours in the cache for the same reason.  No lane exchange per
+// step: the weights are exp2(x + sh) for an sh of the row that falls only where a
+// weight passes 2^13, outputs and sum with it.
 #include "qg_kv4_attn.hpp"
 
 #include <algorithm>
@@ -30,10 +31,10 @@ namespace {
 
 constexpr int kStep = 32;            // positions of a wave's step
 constexpr int kAttnWaves = 4;
-constexpr float kLowest = -3.402823466e38f;
+constexpr float kLowest = -3.402823466e38f, kUnset = 1e30f;
 
 typedef int v2i __attribute__((ext_vector_type(2)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float max16(float v) {   // over the four lanes of one column
   v = fmaxf(v, __shfl_xor(v, 16, kWave));
@@ -44,158 +45,242 @@ __device__ __forceinline__ float sum16(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
-// One step's codes and group words, as a lane holds them.
-template <int D>
-struct Kv4Step {
-  static constexpr int kGd = kv4_groups(D), kKw = D / 32;   // key words of a position
-  int k[2][kKw];
-  v4i v[2][kGd];
-  v4i kp[2][kGd], vp[2][kGd];
-};
-
 }  // namespace
 
+struct Kv4FewArgs {
+  Kv4Seqs s;
+  Kv4Attend a;
+  int G, splits;
+  Kv4Divs by;
+  Kv4Div by_splits;
+  int64_t max_rows;   // sequences of more rows are another kernel's
+  float* part_o;
+  float* part_ml;
+};
+
 // Workspace of a call with several splits: outputs [tile][split][row][D] and
-// (maximum, sum) [tile][split][row], binary32, where tile counts row tiles
-// times kv heads.
+// (sh, sum) [tile][split][row], binary32, where tile counts row tiles times kv
+// heads; outputs and sums are in the unit of their sh.
+
+// Steps of split `split` of a tile with `tiles` steps.
+__device__ __forceinline__ int kv4_per_split(int tiles, const Kv4Div& splits) {
+  return max(splits((int)(tiles + splits.d - 1)), kAttnWaves);
+}
+
+// Positions of a tile's first row's sequence and of the tile's first and last row.
+template <int ROWS>
+__device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile& t, int& p0, int& p1,
+                                              int& first, int& rows) {
+  rows = min(t.n * p.G - t.row0, ROWS);
+  const int len = min(p.s.lengths[t.b], 0x3FFFFFFF);
+  first = max(len, -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
+  p0 = first + p.by.G(t.row0);
+  p1 = first + p.by.G(t.row0 + rows - 1);
+}
 
 template <int DT, int D, int RT>
-struct Kv4Few {
-  static constexpr int kRows = 16 * RT, kGd = kv4_groups(D), kKw = D / 32, kTd = D / 16;
-  typedef Kv4Step<D> Step;
-
-  // uniform
-  Kv4Seqs s;
-  const int32_t* table;   // the sequence's
-  int h, page_words, window, sinks, capacity;
-  int p0, p1;             // positions of the tile's first and last row
-  Kv4Span span;
-  // per lane
-  int c, g;
-  u32 off_k, off_v, off_p;
-  int pos[RT];            // position of the lane's query row
-  v8h q[RT][kKw];
-  float cc[RT], qs[RT][kGd];
-  v4f o[RT][kTd], oz[RT][kGd];
-  float m[RT], l[RT], rinv[RT][kGd], lim[RT][kGd];
-
-  // Pages of the two halves of cache tile `tile` (-1: none).
-  __device__ __forceinline__ void ids(int tile, int (&id)[2]) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int pi = (tile * kStep + 16 * i) >> s.shift;
-      int v = -1;
-      if (pi < s.W) v = table[pi];
-      v = __builtin_amdgcn_readfirstlane(v);
-      id[i] = (u32)v < (u32)s.P ? v : -1;
-    }
+__global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3 : 2) void k_kv4_attend_few(Kv4FewArgs p) {
+  constexpr int kRows = 16 * RT, kGd = kv4_groups(D), kKw = D / 32, kTd = D / 16;   // key words, channel tiles
+  constexpr bool kTwice = DT == F16;   // weights in two parts
+  // outputs of the waves, 16 rows and up to 128 channels at a time
+  constexpr int kCols = D < 128 ? D : 128;
+  __shared__ float red[kAttnWaves][16][kCols + 4];
+  __shared__ float stat[kAttnWaves][kRows][2];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int th = p.by_splits((int)blockIdx.x), split = blockIdx.x - th * p.splits;
+  const int tile_n = p.by.H(th), h = th - tile_n * p.s.H;
+  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, 1, p.max_rows, tile_n);
+  if (t.b < 0) return;
+  int p0, p1, first, rows;
+  kv4_positions<kRows>(p, t, p0, p1, first, rows);
+  const int shift = p.s.shift, S = 1 << shift, W = p.s.W, window = p.a.window, sinks = p.a.sinks;
+  const int capacity = (int)min((int64_t)W << shift, (int64_t)0x40000000);
+  const Kv4Span span = kv4_span<kStep>(p0, p1, window, sinks, capacity);
+  const int per = kv4_per_split(span.tiles, p.by_splits);
+  const int u0 = split * per, u1 = min(u0 + per, span.tiles);
+  if (u0 >= u1 && p.splits > 1) {   // a split without steps: the join leaves it out
+    if (threadIdx.x < kRows) *(v2f*)(p.part_ml + (((int64_t)th * p.splits + split) * kRows + threadIdx.x) * 2) = v2f{kUnset, 0.f};
+    return;
   }
+  const int32_t* const table = p.s.table + (int64_t)t.b * W;
+  const int page_words = (int)kv4_words(S, D);
+  const char* const pool = (const char*)(p.s.pages + (int64_t)h * page_words);
+  const uint32_t page_step = (uint32_t)p.s.H * (uint32_t)page_words * 4u;   // < 2^32: 1024 heads of 256 positions of 272 bytes
 
-  __device__ __forceinline__ void load(int tile, const int (&id)[2], Step& t) const {
-    const int S = 1 << s.shift;
+  // ---- codes and group words of a step, as a lane holds them -------------------
+  const int c = lane & 15, g = lane >> 4;
+  const u32 off_k = c * (D / 2) + g * (D == 64 ? 8 : 16);
+  const u32 off_v = (g * (D / 8) + (D == 64 ? c >> 1 : c)) * 16;
+  const u32 off_p = 16 * g;
+  int kc[2][kKw];
+  v4i vc[2][kGd], kp[2][kGd], vp[2][kGd];
+  int id[2], id_next[2];
+  const char* at[2];
+  // pages of the halves of step u; any where there is none
+  auto fetch_ids = [&](int u) QG_INLINE {
+    const int tile = span.tile(min(u, u1 - 1));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) id_next[i] = __builtin_amdgcn_readfirstlane(table[min((tile * kStep + 16 * i) >> shift, W - 1)]);
+  };
+  auto load_keys = [&](int u) QG_INLINE {
+    const int tile = span.tile(min(u, u1 - 1));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int slot = (tile * kStep + 16 * i) & (S - 1);
-      const char* page = (const char*)(s.pages + ((int64_t)max(id[i], 0) * s.H + h) * page_words);
-      const char* kb = page + slot * (D / 2);
-      const char* vb = kb + S * (D / 2);
-      const char* pb = page + S * D + slot * 4;
+      id[i] = id_next[i];
+      const u32 slot = (u32)(tile * kStep + 16 * i) & (u32)(S - 1);
+      at[i] = pool + (uint64_t)((u32)id[i] < (u32)p.s.P ? (u32)id[i] : 0u) * page_step;
+      const char* const kb = at[i] + slot * (D / 2);
+      const char* const pb = at[i] + (S * D + slot * 4);
 #pragma unroll
       for (int gd = 0; gd < kGd; ++gd) {
         if constexpr (D == 64) {
           const v2i a = *(const v2i*)(kb + off_k);
-          t.k[i][0] = a[0];
-          t.k[i][1] = a[1];
+          kc[i][0] = a[0];
+          kc[i][1] = a[1];
         } else {
-          const v4i a = ld16(kb + off_k + 64 * gd);
+          const v4i a = ld16(kb + (off_k + 64 * gd));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t.k[i][4 * gd + j] = a[j];
+          for (int j = 0; j < 4; ++j) kc[i][4 * gd + j] = a[j];
         }
-        t.v[i][gd] = ld16(vb + off_v + 256 * gd);
-        t.kp[i][gd] = ld16(pb + off_p + gd * 4 * S);
-        t.vp[i][gd] = ld16(pb + off_p + (kGd + gd) * 4 * S);
+        kp[i][gd] = ld16(pb + gd * 4 * S + off_p);
       }
     }
-  }
-
-  __device__ __forceinline__ void start() {
+  };
+  auto load_values = [&](int u) QG_INLINE {   // of the pages that load_keys took
+    const int tile = span.tile(min(u, u1 - 1));
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-      for (int j = 0; j < kTd; ++j) o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
-      m[r] = kLowest;
-      l[r] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const u32 slot = (u32)(tile * kStep + 16 * i) & (u32)(S - 1);
+      const char* const vb = at[i] + (S + slot) * (D / 2);
+      const char* const pb = at[i] + (S * D + (kGd * S + slot) * 4);
 #pragma unroll
       for (int gd = 0; gd < kGd; ++gd) {
-        oz[r][gd] = v4f{0.f, 0.f, 0.f, 0.f};
-        rinv[r][gd] = 0.f;
-        lim[r][gd] = 0.f;
+        vc[i][gd] = ld16(vb + (off_v + 256 * gd));
+        vp[i][gd] = ld16(pb + gd * 4 * S + off_p);
       }
     }
-  }
+  };
 
-  // A query row: its lane's words in the order of the unpacked codes (nibbles
-  // 0 4 1 5 2 6 3 7, the second of each byte 16 times as large), their sum.
-  __device__ __forceinline__ void query(int r, const void* base, int64_t at, bool there, float scale) {
-    float x[kKw][8];
-    float top = 0.f;
+  // ---- queries -------------------------------------------------------------------
+  // A lane's words in the order of the unpacked codes (nibbles 0 4 1 5 2 6 3 7, the
+  // second of each byte 16 times as large), and their sum.
+  int pos[RT];
+  v8h q[RT][kKw];
+  float cc[RT], qs[RT][kGd];
+  v4i qw[RT][kKw];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const bool there = 16 * r + c < rows;
+    const int row = t.row0 + (there ? 16 * r + c : 0), token = p.by.G(row);
+    pos[r] = there ? first + token : kKv4Past;
+    const uint16_t* const from = (const uint16_t*)p.a.q + (int64_t)(t.token0 + token) * p.a.q_stride +
+                                 (int64_t)(h * p.G + row - token * p.G) * D;
 #pragma unroll
     for (int j = 0; j < kKw; ++j) {
       const int d = D == 64 ? 16 * g + 8 * j : 128 * (j / 4) + 32 * g + 8 * (j % 4);
-      const v4i a = there ? ld16((const uint16_t*)base + at + d) : v4i{0, 0, 0, 0};
+      qw[r][j] = ld16(from + d);
+      if (!there) qw[r][j] = v4i{0, 0, 0, 0};
+    }
+  }
+  // the first step's codes come in meanwhile
+  const int n_steps = u1 - u0;   // of the workgroup, at least 1 where there is anything to load
+  int u = u0 + wave;
+  if (n_steps > 0) {
+    fetch_ids(u);
+    load_keys(u);
+    load_values(u);
+    fetch_ids(u + kAttnWaves);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float x[kKw][8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kKw; ++j) {
+      const v4i a = qw[r][j];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const u32 u = ((u32)a[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-        x[j][e] = DT == BF16 ? bf16_bits_to_f32(u) : f16_bits_to_f32((uint16_t)u);
+        const u32 v = ((u32)a[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+        x[j][e] = DT == BF16 ? bf16_bits_to_f32(v) : f16_bits_to_f32((uint16_t)v);
         top = fmaxf(top, fabsf(x[j][e]));
       }
     }
     top = max16(top);
     // top 2^e in [2^14, 2^15); not for zero rows and infinities
-    const int e = top > 0.f && top < __builtin_inff() ? 14 - (ilogbf(top)) : 0;
+    // (subnormal tops fall short of it)
+    const int e2 = top > 0.f && top < __builtin_inff() ? 141 - (int)(__float_as_uint(top) >> 23) : 0;
 #pragma unroll
     for (int gd = 0; gd < kGd; ++gd) qs[r][gd] = 0.f;
 #pragma unroll
     for (int j = 0; j < kKw; ++j) {
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-      v8h w;
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = ldexpf(x[j][order[i]], e);
+        const float v = ldexpf(x[j][order[i]], e2);
         sum += v;
-        w[i] = (_Float16)((i & 2) ? v * 0.0625f : v);
+        q[r][j][i] = (_Float16)((i & 2) ? v * 0.0625f : v);
       }
-      q[r][j] = w;
       qs[r][j / 4] += sum;
     }
-    // scores in units of 2^(e - 24), exponents in base 2
+    // scores in units of 2^(e2 - 24), exponents in base 2
 #pragma unroll
     for (int gd = 0; gd < kGd; ++gd) qs[r][gd] = sum16(qs[r][gd]) * 0x1p-24f;
-    cc[r] = ldexpf(scale * 1.44269504088896f, 24 - e);
+    cc[r] = ldexpf(p.a.scale * 1.44269504088896f, 24 - e2);
   }
 
-  // One step.  EDGE: some position is out of some row's sight.
-  template <bool EDGE>
-  __device__ __forceinline__ void step(int tile, const int (&id)[2], const Step& t) {
+  // outputs: rows = channels, columns = query rows; sums of the zero points
+  v4f o[RT][kTd], oz[RT][kGd];
+  float l[RT], sh[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+#pragma unroll
+    for (int j = 0; j < kTd; ++j) o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int gd = 0; gd < kGd; ++gd) oz[r][gd] = v4f{0.f, 0.f, 0.f, 0.f};
+    l[r] = 0.f;
+    sh[r] = kUnset;
+  }
+  // A power of two near the values' scales, from what some row sees of the wave's
+  // first step: the weights p s are taken relative to it.
+  float unit[kGd];
+#pragma unroll
+  for (int gd = 0; gd < kGd; ++gd) {
+    float top = 0x1p-126f;
+    if (n_steps > 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = kv4_scale((u32)vp[i][gd][e]);
+          const int j = span.tile(min(u, u1 - 1)) * kStep + 16 * i + 4 * g + e;
+          const bool some = ((u32)id[i] < (u32)p.s.P) & (j <= p1) & (j < capacity) & ((window <= 0) | (j > p0 - window) | (j < sinks));
+          top = some && v < __builtin_inff() ? fmaxf(top, v) : top;
+        }
+    }
+    top = max16(top);
+    const u32 ex = (u32)min(max((int)(__builtin_amdgcn_readfirstlane(__float_as_uint(top)) >> 23), 27), 227);
+    unit[gd] = __uint_as_float((254u - ex) << 23);   // 2^-floor(log2 top)
+  }
+
+#pragma unroll 1
+  for (; u < u1; u += kAttnWaves) {
+    const int tile = span.tile(u), t0 = tile * kStep;
+    const bool ok0 = (u32)id[0] < (u32)p.s.P, ok1 = (u32)id[1] < (u32)p.s.P;
+    const bool full = ok0 && ok1 && t0 + kStep - 1 <= p0 && t0 + kStep <= capacity &&
+                      (window <= 0 || t0 > p1 - window || t0 + kStep <= sinks);
     // scores: rows = positions, columns = query rows
     float y[RT][2][4];
-    float sv[kGd][2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       v8h kf[kKw];
 #pragma unroll
       for (int j = 0; j < kKw; ++j) {
-        const u32 w = (u32)t.k[i][j], hi = w >> 8;
+        const u32 w = (u32)kc[i][j], hi = w >> 8;
         kf[j] = __builtin_bit_cast(v8h, v4i{(int)(w & 0x000F000Fu), (int)(w & 0x00F000F0u),
                                             (int)(hi & 0x000F000Fu), (int)(hi & 0x00F000F0u)});
       }
 #pragma unroll
-      for (int gd = 0; gd < kGd; ++gd)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sv[gd][i][e] = kv4_scale((u32)t.vp[i][gd][e]);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int gd = 0; gd < kGd; ++gd) {
           constexpr int kPer = kKw / kGd;
@@ -205,102 +290,109 @@ struct Kv4Few {
             a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[kPer * gd + j], q[r][kPer * gd + j], a, 0, 0, 0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const u32 w = (u32)t.kp[i][gd][e];
-            const float u = __builtin_fmaf(-(float)(w & 15u), qs[r][gd], a[e]) * kv4_scale(w);
-            y[r][i][e] = gd ? y[r][i][e] + u : u;
+            const u32 w = (u32)kp[i][gd][e];
+            const float v = __builtin_fmaf(-(float)(w & 15u), qs[r][gd], a[e]) * kv4_scale(w);
+            y[r][i][e] = gd ? y[r][i][e] + v : v;
           }
         }
-        if constexpr (EDGE) {
-          const int t0 = tile * kStep + 16 * i + 4 * g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int p = t0 + e;
-            const bool seen = id[i] >= 0 && p <= pos[r] && p < capacity &&
-                              (window <= 0 || p > pos[r] - window || p < sinks);
-            if (!seen) y[r][i][e] = -__builtin_inff();
-          }
-        }
-      }
     }
-    // weights
-    v8h pf[RT][kGd];
+    float sv[kGd][2][4];
+    u32 zf[kGd][2][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float top = kLowest;
+    for (int gd = 0; gd < kGd; ++gd)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[r][i][e] = EDGE && y[r][i][e] == -__builtin_inff() ? -__builtin_inff() : y[r][i][e] * cc[r];
-          top = fmaxf(top, y[r][i][e]);
-        }
-      float alpha = 1.f;
-      if (__any(top > m[r] + 8.f)) {   // the bound rises: all lanes of a column agree
-        const float mn = fmaxf(m[r], max16(top));
-        alpha = __builtin_amdgcn_exp2f(m[r] - mn);
-        m[r] = mn;
-        l[r] *= alpha;
-#pragma unroll
-        for (int gd = 0; gd < kGd; ++gd) lim[r][gd] = -1.f;
-      }
-      float p[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[i][e] = __builtin_amdgcn_exp2f(y[r][i][e] - m[r]);
-          l[r] += p[i][e];
-        }
-#pragma unroll
-      for (int gd = 0; gd < kGd; ++gd) {
-        float w[2][4], most = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[i][e] = p[i][e] * sv[gd][i][e];
-            if (EDGE && y[r][i][e] == -__builtin_inff()) w[i][e] = 0.f;   // whatever scale lies there
-            most = fmaxf(most, w[i][e]);
-          }
-        if (__any(most > lim[r][gd])) {   // another power of two for the row's weights
-          const bool set = rinv[r][gd] > 0.f;
-          const float ref = set ? alpha / rinv[r][gd] : 0.f;
-          const float big = fminf(fmaxf(fmaxf(max16(most), ref), 0x1p-100f), 0x1p100f);
-          const float f = __uint_as_float(0x7F000000u - (__float_as_uint(big) & 0x7F800000u));  // 2^-floor(log2 big)
-          const bool some = fmaxf(max16(most), ref) > 0.f;
-          const float by = set ? f * ref : 1.f;
-          rinv[r][gd] = some ? f : 0.f;
-          lim[r][gd] = some ? 0x1p12f / f : 0.f;
-          float rows[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) rows[e] = __shfl(by, 4 * g + e, kWave);
-#pragma unroll
-          for (int j = 0; j < kTd / kGd; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][gd * (kTd / kGd) + j][e] *= rows[e];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) oz[r][gd][e] *= rows[e];
-        }
-        v8h pk;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pk[4 * i + e] = (_Float16)(w[i][e] * rinv[r][gd]);
-        pf[r][gd] = pk;
-      }
-    }
-    // values: rows = query rows, columns = channels, 8 c + j of the lane's word
-#pragma unroll
-    for (int gd = 0; gd < kGd; ++gd) {
-      v4i zf;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int e = 0; e < 4; ++e) sv[gd][i][e] = kv4_scale((u32)vp[i][gd][e]) * unit[gd];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          zf[2 * i + e] = (int)(((u32)t.vp[i][gd][2 * e] & 15u) | (((u32)t.vp[i][gd][2 * e + 1] & 15u) << 16));
+          zf[gd][i][e] = ((u32)vp[i][gd][2 * e] & 15u) | (((u32)vp[i][gd][2 * e + 1] & 15u) << 16);
+      }
+    load_keys(u + kAttnWaves);
+    // weights
+    v8h pf[RT][kGd], pl[RT][kGd];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        oz[r][gd] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pf[r][gd], __builtin_bit_cast(v8h, zf), oz[r][gd], 0, 0, 0);
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[r][i][e] *= cc[r];
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = t0 + 16 * i + 4 * g + e;
+            const bool seen = (i ? ok1 : ok0) & (j <= pos[r]) & (j < capacity) & ((window <= 0) | (j > pos[r] - window) | (j < sinks));
+            y[r][i][e] = seen ? y[r][i][e] : -__builtin_inff();
+          }
+      }
+      float w[kGd][2][4];
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {   // the second round's weights pass
+        float sum = 0.f, most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __builtin_amdgcn_exp2f(y[r][i][e] + sh[r]);
+            sum += x;
+#pragma unroll
+            for (int gd = 0; gd < kGd; ++gd) {
+              // nothing out of sight, whatever its scale
+              w[gd][i][e] = y[r][i][e] == -__builtin_inff() ? 0.f : x * sv[gd][i][e];
+              most = fmaxf(most, w[gd][i][e]);
+            }
+          }
+        if (round > 0 || !__any(most > 0x1p13f || sum > 0x1p70f)) {   // a NaN stays one
+          l[r] += sum;
+          break;
+        }
+        // The row's sh to where its largest weight is near 1, and no exponential past 2^64.
+        float top = kLowest;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = sv[0][i][e];
+#pragma unroll
+            for (int gd = 1; gd < kGd; ++gd) v = fmaxf(v, sv[gd][i][e]);
+            const float yy = y[r][i][e];
+            top = fmaxf(top, fmaxf(yy == -__builtin_inff() ? yy : yy + __builtin_amdgcn_logf(v), yy - 64.f));
+          }
+        top = max16(top);
+        const float to = -floorf(top) - fabsf(top) * 0x1p-21f;   // by more than rounding takes
+        const float by = to < sh[r] ? __builtin_amdgcn_exp2f(to - sh[r]) : 1.f;   // 0 for a row's first weights
+        sh[r] = fminf(sh[r], to);
+        l[r] *= by;
+#pragma unroll
+        for (int j = 0; j < kTd; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][j][e] *= by;
+#pragma unroll
+        for (int gd = 0; gd < kGd; ++gd) oz[r][gd][0] *= by;
+      }
+#pragma unroll
+      for (int gd = 0; gd < kGd; ++gd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const _Float16 hi = (_Float16)w[gd][i][e];
+            pf[r][gd][4 * i + e] = hi;
+            if constexpr (kTwice) pl[r][gd][4 * i + e] = (_Float16)(w[gd][i][e] - (float)hi);
+          }
+      }
+    }
+    // values: rows = channels, columns = query rows
+#pragma unroll
+    for (int gd = 0; gd < kGd; ++gd) {
+      const v8h z = __builtin_bit_cast(v8h, v4i{(int)zf[gd][0][0], (int)zf[gd][0][1], (int)zf[gd][1][0], (int)zf[gd][1][1]});
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        oz[r][gd] = __builtin_amdgcn_mfma_f32_16x16x32_f16(z, pf[r][gd], oz[r][gd], 0, 0, 0);
+        if constexpr (kTwice) oz[r][gd] = __builtin_amdgcn_mfma_f32_16x16x32_f16(z, pl[r][gd], oz[r][gd], 0, 0, 0);
+      }
       constexpr int kHalves = D == 64 ? 1 : 2;
 #pragma unroll
       for (int half = 0; half < kHalves; ++half) {
@@ -310,7 +402,7 @@ struct Kv4Few {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const u32 sel = D == 64 ? ((c & 1) ? 0x07060302u : 0x05040100u) : half ? 0x07060302u : 0x05040100u;
-            x[2 * i + e] = __builtin_amdgcn_perm((u32)t.v[i][gd][2 * e + 1], (u32)t.v[i][gd][2 * e], sel);
+            x[2 * i + e] = __builtin_amdgcn_perm((u32)vc[i][gd][2 * e + 1], (u32)vc[i][gd][2 * e], sel);
           }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -320,152 +412,57 @@ struct Kv4Few {
           for (int e = 0; e < 4; ++e) vf[e] = (int)((j & 2 ? x[e] >> 8 : x[e]) & mask);
           const int td = 8 * gd + 4 * half + j;
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-            o[r][td] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pf[r][gd], __builtin_bit_cast(v8h, vf), o[r][td], 0, 0, 0);
+          for (int r = 0; r < RT; ++r) {
+            o[r][td] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, vf), pf[r][gd], o[r][td], 0, 0, 0);
+            if constexpr (kTwice)
+              o[r][td] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, vf), pl[r][gd], o[r][td], 0, 0, 0);
+          }
         }
       }
     }
+    load_values(u + kAttnWaves);
+    fetch_ids(u + 2 * kAttnWaves);
   }
 
-  __device__ __forceinline__ void run_step(int tile, const int (&id)[2], const Step& t) {
-    const int a = tile * kStep;
-    const bool full = id[0] >= 0 && id[1] >= 0 && a + kStep - 1 <= p0 && a + kStep <= capacity &&
-                      (window <= 0 || a > p1 - window || a + kStep <= sinks);
-    if (full) step<false>(tile, id, t);
-    else step<true>(tile, id, t);
-  }
-
-  // Steps u, u + stride, ... below end, the next one's loads ahead of each.
-  __device__ __forceinline__ void run(int u, int end, int stride) {
-    if (u >= end) return;
-    Step a, b;
-    int ia[2], ib[2];
-    ids(span.tile(u), ia);
-    load(span.tile(u), ia, a);
-    while (true) {
-      const int ub = min(u + stride, end - 1);
-      ids(span.tile(ub), ib);
-      load(span.tile(ub), ib, b);
-      run_step(span.tile(u), ia, a);
-      u += stride;
-      if (u >= end) break;
-      const int ua = min(u + stride, end - 1);
-      ids(span.tile(ua), ia);
-      load(span.tile(ua), ia, a);
-      run_step(span.tile(u), ib, b);
-      u += stride;
-      if (u >= end) break;
-    }
-  }
-};
-
-struct Kv4FewArgs {
-  Kv4Seqs s;
-  Kv4Attend a;
-  int G, splits;
-  int64_t max_rows;   // sequences of more rows are another kernel's
-  float* part_o;
-  float* part_ml;
-};
-
-// Steps of split `split` of a tile with `tiles` steps.
-__device__ __forceinline__ int kv4_per_split(int tiles, int splits) {
-  return max((tiles + splits - 1) / splits, kAttnWaves);
-}
-
-// What both kernels below derive from a workgroup's tile.
-template <int ROWS>
-__device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile& t, int& p0, int& p1,
-                                              int& len, int& rows) {
-  rows = min(t.n * p.G - t.row0, ROWS);
-  len = min(p.s.lengths[t.b], 0x3FFFFFFF);
-  const int first = max(len, -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
-  len = first;
-  p0 = first + t.row0 / p.G;
-  p1 = first + (t.row0 + rows - 1) / p.G;
-}
-
-template <int DT, int D, int RT>
-__global__ __launch_bounds__(64 * kAttnWaves) void k_kv4_attend_few(Kv4FewArgs p) {
-  typedef Kv4Few<DT, D, RT> W;
-  constexpr int kRows = W::kRows, kTd = W::kTd;
-  // outputs of three waves, 16 rows and up to 128 channels at a time
-  constexpr int kCols = D < 128 ? D : 128;
-  __shared__ float red[kAttnWaves][16][kCols + 4];
-  __shared__ float stat[kAttnWaves][kRows][2];
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int split = blockIdx.x % p.splits;
-  const int th = blockIdx.x / p.splits;
-  const int h = th % p.s.H;
-  const Kv4Tile t = kv4_tile<kRows>(p.s, p.G, 1, p.max_rows, th / p.s.H);
-  if (t.b < 0) return;
-  W w;
-  int first, rows;
-  kv4_positions<kRows>(p, t, w.p0, w.p1, first, rows);
-  w.s = p.s;
-  w.h = h;
-  w.table = p.s.table + (int64_t)t.b * p.s.W;
-  w.page_words = (int)kv4_words(1 << p.s.shift, D);
-  w.window = p.a.window;
-  w.sinks = p.a.sinks;
-  w.capacity = (int)min((int64_t)p.s.W << p.s.shift, (int64_t)0x40000000);
-  w.span = kv4_span<kStep>(w.p0, w.p1, w.window, w.sinks, w.capacity);
-  const int per = kv4_per_split(w.span.tiles, p.splits);
-  const int u0 = split * per, u1 = min(u0 + per, w.span.tiles);
-  if (u0 >= u1 && (p.splits > 1 || split > 0)) return;   // a split without steps: the join leaves it out
-  w.c = lane & 15;
-  w.g = lane >> 4;
-  w.off_k = w.c * (D / 2) + w.g * (D == 64 ? 8 : 16);
-  w.off_v = (w.g * (D / 8) + (D == 64 ? w.c >> 1 : w.c)) * 16;
-  w.off_p = 16 * w.g;
-  w.start();
+  // ---- join the waves: the smallest sh of each row, sums, outputs in its unit -------
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const int row = t.row0 + 16 * r + w.c;
-    const bool there = 16 * r + w.c < rows;
-    w.pos[r] = there ? first + row / p.G : kKv4Past;
-    w.query(r, p.a.q, (int64_t)(t.token0 + row / p.G) * p.a.q_stride + (int64_t)(h * p.G + row % p.G) * D,
-            there, p.a.scale);
-  }
-  w.run(u0 + wave, u1, kAttnWaves);
-
-  // Join the waves: maximum and sum of each row, then the outputs in common units.
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const float l = sum16(w.l[r]);
-    if (w.g == 0) {
-      stat[wave][16 * r + w.c][0] = w.m[r];
-      stat[wave][16 * r + w.c][1] = l;
+    const float sum = sum16(l[r]);
+    if (g == 0) {
+      stat[wave][16 * r + c][0] = sh[r];
+      stat[wave][16 * r + c][1] = sum;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    // the lane's column: its factor to the common maximum and out of the weights' units
-    float m = kLowest, l = 0.f;
+    float low = kUnset, sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kAttnWaves; ++v) m = fmaxf(m, stat[v][16 * r + w.c][0]);
+    for (int v = 0; v < kAttnWaves; ++v) low = fminf(low, stat[v][16 * r + c][0]);
 #pragma unroll
     for (int v = 0; v < kAttnWaves; ++v)
-      l += stat[v][16 * r + w.c][1] * __builtin_amdgcn_exp2f(stat[v][16 * r + w.c][0] - m);
-    const float mine = __builtin_amdgcn_exp2f(w.m[r] - m);
-    const float inv = p.splits > 1 ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
+      sum += stat[v][16 * r + c][1] * __builtin_amdgcn_exp2f(low - stat[v][16 * r + c][0]);
+    const float mine = __builtin_amdgcn_exp2f(low - sh[r]);
+    const float inv = p.splits > 1 ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int gd = 0; gd < W::kGd; ++gd) {
-      const float back = w.rinv[r][gd] > 0.f ? mine / w.rinv[r][gd] * inv : 0.f;
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = __shfl(back, 4 * w.g + e, kWave);
-      constexpr int kPer = kTd / W::kGd;
+    for (int gd = 0; gd < kGd; ++gd) {
+      const float f = mine * inv / unit[gd];   // unit: a power of two
+      constexpr int kPer = kTd / kGd;
       if (r || gd) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
+      for (int e = 0; e < 4; ++e) {
+        // channel row 4 g + e of the tiles: channels 8 (4 g + e) + j, or of 64 channels
+        // 8 ((4 g + e) / 2) + 4 ((4 g + e) % 2) + j
+        float* const to = &red[wave][c][kPer * (4 * g + e)];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = (w.o[r][gd * kPer + j][e] * ((j & 1) ? 0x1p20f : 0x1p24f) - w.oz[r][gd][e] * 0x1p24f) * f[e];
-          const int col = D == 64 ? 8 * (w.c >> 1) + 4 * (w.c & 1) + j : 8 * w.c + j;
-          red[wave][4 * w.g + e][col] = x;
+        for (int j = 0; j < kPer; j += 4) {
+          v4f x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = (o[r][gd * kPer + j + k][e] * ((k & 1) ? 0x1p20f : 0x1p24f) - oz[r][gd][0] * 0x1p24f) * f;
+          *(v4f*)(to + j) = x;
         }
+      }
       __syncthreads();
       for (int i = threadIdx.x; i < 16 * kCols / 8; i += 64 * kAttnWaves) {
         const int row = i / (kCols / 8), col = 8 * (i % (kCols / 8));
@@ -479,58 +476,69 @@ __global__ __launch_bounds__(64 * kAttnWaves) void k_kv4_attend_few(Kv4FewArgs p
         }
         const int d = kCols * gd + col;
         if (p.splits > 1) {
-          float* to = p.part_o + (((int64_t)th * p.splits + split) * kRows + 16 * r + row) * D + d;
+          float* const to = p.part_o + (((int64_t)th * p.splits + split) * kRows + 16 * r + row) * D + d;
           *(v4f*)to = v4f{x[0], x[1], x[2], x[3]};
           *(v4f*)(to + 4) = v4f{x[4], x[5], x[6], x[7]};
         } else {
-          const int qr = t.row0 + 16 * r + row;
-          kv4_store8<DT>(p.a.out, ((int64_t)(t.token0 + qr / p.G) * p.a.Hq + h * p.G + qr % p.G) * D + d, x);
+          const int qr = t.row0 + 16 * r + row, token = p.by.G(qr);
+          kv4_store8<DT>(p.a.out, ((int64_t)(t.token0 + token) * p.a.Hq + h * p.G + qr - token * p.G) * D + d, x);
         }
       }
     }
-    if (p.splits > 1 && wave == 0 && w.g == 0) {
-      float* to = p.part_ml + (((int64_t)th * p.splits + split) * kRows + 16 * r + w.c) * 2;
-      to[0] = m;
-      to[1] = l;
+    if (p.splits > 1 && wave == 0 && g == 0) {
+      float* const to = p.part_ml + (((int64_t)th * p.splits + split) * kRows + 16 * r + c) * 2;
+      to[0] = low;
+      to[1] = sum;
     }
   }
 }
 
-// Join the splits of a tile: weights 2^(m_i - m) of each split's outputs and sums.
+// Join the splits of a tile, each in the unit of its sh.  16 lanes take the
+// splits of 8 channels of a row in turn, so that their loads are under way together.
 template <int DT, int D, int ROWS>
-__global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p) {
-  const int th = blockIdx.x, h = th % p.s.H;
-  const Kv4Tile t = kv4_tile<ROWS>(p.s, p.G, 1, p.max_rows, th / p.s.H);
+__global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_most, Kv4Div parts) {
+  const int th = parts((int)blockIdx.x), part = blockIdx.x - th * parts.d;
+  const int tile_n = p.by.H(th), h = th - tile_n * p.s.H;
+  const Kv4Tile t = kv4_tile<ROWS>(p.s, p.by, 1, p.max_rows, tile_n);
   if (t.b < 0) return;
-  int p0, p1, first, rows;
-  kv4_positions<ROWS>(p, t, p0, p1, first, rows);
-  const int capacity = (int)min((int64_t)p.s.W << p.s.shift, (int64_t)0x40000000);
-  const Kv4Span span = kv4_span<kStep>(p0, p1, p.a.window, p.a.sinks, capacity);
-  const int per = kv4_per_split(span.tiles, p.splits), used = (span.tiles + per - 1) / per;
-  for (int i = threadIdx.x; i < rows * (D / 8); i += 256) {
-    const int row = i / (D / 8), d = 8 * (i % (D / 8));
-    const float* ml = p.part_ml + ((int64_t)th * p.splits * ROWS + row) * 2;
-    const float* po = p.part_o + ((int64_t)th * p.splits * ROWS + row) * D + d;
-    float m = kLowest, l = 0.f, x[8];
-    for (int v = 0; v < used; ++v) m = fmaxf(m, ml[(int64_t)v * ROWS * 2]);
+  const int rows = min(t.n * p.G - t.row0, rows_most);
+  const int item = part * 16 + (int)threadIdx.x / 16, sub = threadIdx.x & 15;
+  if (item >= rows * (D / 8)) return;
+  const int row = item / (D / 8), d = 8 * (item % (D / 8));
+  const float* const ml = p.part_ml + ((int64_t)th * p.splits * ROWS + row) * 2;
+  const float* const po = p.part_o + ((int64_t)th * p.splits * ROWS + row) * D + d;
+  float low = kUnset, l = 0.f, x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    for (int v = 0; v < used; ++v) {
-      const float f = __builtin_amdgcn_exp2f(ml[(int64_t)v * ROWS * 2] - m);
-      l += f * ml[(int64_t)v * ROWS * 2 + 1];
-      const v4f a = *(const v4f*)(po + (int64_t)v * ROWS * D), b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  for (int v = sub; v < p.splits; v += 16) {
+    const v2f two = *(const v2f*)(ml + (int64_t)v * ROWS * 2);
+    const v4f a = *(const v4f*)(po + (int64_t)v * ROWS * D), b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
+    const float sh = two[0], sum = two[1];
+    if (sh == kUnset) continue;   // no steps, or nothing in the row's sight: no outputs there
+    const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
+    low = to;
+    l = l * f + sum * f1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] += f * a[e];
-        x[4 + e] += f * b[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      x[e] = x[e] * f + a[e] * f1;
+      x[4 + e] = x[4 + e] * f + b[e] * f1;
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= inv;
-    const int qr = t.row0 + row;
-    kv4_store8<DT>(p.a.out, ((int64_t)(t.token0 + qr / p.G) * p.a.Hq + h * p.G + qr % p.G) * D + d, x);
   }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const float sh = __shfl_xor(low, o, kWave), sum = __shfl_xor(l, o, kWave);
+    const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
+    low = to;
+    l = l * f + sum * f1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * f + __shfl_xor(x[e], o, kWave) * f1;
+  }
+  if (sub != 0) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  const int qr = t.row0 + row, token = p.by.G(qr);
+  kv4_store8<DT>(p.a.out, ((int64_t)(t.token0 + token) * p.a.Hq + h * p.G + qr - token * p.G) * D + d, x);
 }
 
 // ---- launch -------------------------------------------------------------------
@@ -565,7 +573,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
     a.few_tiles = tiles(a.few_rows, wide ? 0 : kFewRows);
     // splits of the cached positions: enough workgroups for the GPU, at least 256 positions each
-    const int64_t want = up(2048, a.few_tiles * H);
+    const int64_t want = up(512, a.few_tiles * H);
     a.splits = (int)std::max<int64_t>(1, std::min(want, capacity / 256));
   }
   if (many) {
@@ -592,7 +600,12 @@ int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_
 template <int DT, int D, int RT>
 static hipError_t few_t(Kv4FewArgs p, int64_t tiles, hipStream_t st) {
   k_kv4_attend_few<DT, D, RT><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
-  if (p.splits > 1) k_kv4_attend_join<DT, D, 16 * RT><<<(unsigned)tiles, 256, 0, st>>>(p);
+  if (p.splits > 1) {
+    // workgroups of 16 items of 8 channels; without offsets the rows of a tile are known
+    const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(16 * RT, (int64_t)p.by.n * p.G) : 16 * RT;
+    const Kv4Div parts = kv4_div((rows * (D / 8) + 15) / 16);
+    k_kv4_attend_join<DT, D, 16 * RT><<<(unsigned)(tiles * parts.d), 256, 0, st>>>(p, (int)rows, parts);
+  }
   return hipGetLastError();
 }
 
@@ -604,8 +617,10 @@ static hipError_t few_d(const Kv4FewArgs& p, int D, int rows, int64_t tiles, hip
 }
 
 hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st) {
-  const AttendPlan plan =
-      attend_plan(s.T, s.B, a.Hq, s.H, a.D, (int64_t)s.W << s.shift, s.offsets == nullptr);
+  // A window bounds what the rows of a sequence see: fewer splits than the workspace is for.
+  const int64_t capacity = (int64_t)s.W << s.shift;
+  const int64_t seen = a.window > 0 ? std::min<int64_t>(capacity, (int64_t)a.window + a.sinks + kFewRows + 2 * kStep) : capacity;
+  const AttendPlan plan = attend_plan(s.T, s.B, a.Hq, s.H, a.D, seen, s.offsets == nullptr);
   if (plan.many_tiles > 0) {
     const hipError_t e = launch_kv4_many(s, a, dtype, s.offsets == nullptr ? 1 : kFewRows + 1, plan.many_rows,
                                          plan.many_tiles, st);
@@ -617,6 +632,8 @@ hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hi
   p.G = a.Hq / s.H;
   p.max_rows = plan.many_tiles > 0 || s.offsets != nullptr && a.D < 256 ? kFewRows : (int64_t)1 << 40;
   p.splits = plan.splits;
+  p.by = kv4_divs(s, p.G, plan.few_rows);
+  p.by_splits = kv4_div(p.splits);
   const int64_t tiles = plan.few_tiles * s.H;
   p.part_o = (float*)a.workspace;
   p.part_ml = p.part_o + tiles * p.splits * plan.few_rows * a.D;

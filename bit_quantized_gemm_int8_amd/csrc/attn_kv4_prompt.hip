@@ -26,9 +26,6 @@
 #include <algorithm>
 #include <type_traits>
 
-// a lambda that is called more than once is still part of the kernel: its captures stay in registers
-#define QG_INLINE __attribute__((always_inline))
-
 namespace qg {
 
 namespace {
@@ -81,6 +78,7 @@ struct Kv4ManyArgs {
   Kv4Seqs s;
   Kv4Attend a;
   int G, tiles;
+  Kv4Divs by;
   int64_t min_rows;   // sequences of fewer rows are another kernel's
 };
 
@@ -101,9 +99,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = p.s.H;
-  const int h = blockIdx.x % H;
+  const int tile_n = p.by.H((int)blockIdx.x), h = blockIdx.x - tile_n * H;
   // the rows that see most first
-  const Kv4Tile t = kv4_tile<kRows>(p.s, p.G, p.min_rows, (int64_t)1 << 40, p.tiles - 1 - (int)(blockIdx.x / H));
+  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, p.min_rows, (int64_t)1 << 40, p.tiles - 1 - tile_n);
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, kRows);
   const int len = min(max(p.s.lengths[t.b], -0x3FFFFFFF), 0x3FFFFFFF);
@@ -616,7 +614,7 @@ hipError_t many_d(const Kv4ManyArgs& p, hipStream_t st) {
 
 hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int rows,
                            int64_t tiles, hipStream_t st) {
-  const Kv4ManyArgs p{s, a, a.Hq / s.H, (int)tiles, min_rows};
+  const Kv4ManyArgs p{s, a, a.Hq / s.H, (int)tiles, kv4_divs(s, a.Hq / s.H, rows), min_rows};
   if (rows == 256) return dtype == F16 ? many_d<F16, 8>(p, st) : many_d<BF16, 8>(p, st);
   return dtype == F16 ? many_d<F16, 4>(p, st) : many_d<BF16, 4>(p, st);
 }

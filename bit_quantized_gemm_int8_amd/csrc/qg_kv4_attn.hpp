@@ -7,7 +7,37 @@
 
 #include "qg_kv4.hpp"
 
+#include <algorithm>
+
+// a lambda that is called more than once is still part of the kernel: its captures stay in registers
+#define QG_INLINE __attribute__((always_inline))
+
 namespace qg {
+
+// Exact division of 0 <= n < 2^31 by a divisor that the host knows:
+// n / d = (n * mag) >> (31 + sh), mag = ceil(2^(31 + sh) / d), sh = ceil(log2 d).
+// A division proper costs some 40 instructions at the start of every workgroup.
+struct Kv4Div {
+  int d, sh;
+  u32 mag;
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(u32)n * mag) >> (31 + sh)); }
+};
+inline Kv4Div kv4_div(int64_t d) {
+  Kv4Div v{(int)d, 0, 0};
+  while (((int64_t)1 << v.sh) < d) ++v.sh;
+  v.mag = (u32)((((uint64_t)1 << (31 + v.sh)) + (uint64_t)d - 1) / (uint64_t)d);
+  return v;
+}
+// What the attention kernels divide by: kv heads, query heads of one, and without
+// offsets a sequence's tokens and tiles.
+struct Kv4Divs {
+  Kv4Div H, G, tiles;
+  int n;
+};
+inline Kv4Divs kv4_divs(const Kv4Seqs& s, int G, int rows) {
+  const int64_t n = s.offsets == nullptr ? s.T / s.B : 0;
+  return {kv4_div(s.H), kv4_div(G), kv4_div(std::max<int64_t>((n * G + rows - 1) / rows, 1)), (int)n};
+}
 
 struct Kv4Tile {
   int b;          // sequence, -1: no such tile
@@ -18,14 +48,13 @@ struct Kv4Tile {
 // Tile `idx` among the sequences with min_rows <= n G <= max_rows, ROWS rows each.
 // All lanes of a wave call it with the same arguments; the result is uniform.
 template <int ROWS>
-__device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, int G, int64_t min_rows,
+__device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, const Kv4Divs& by, int64_t min_rows,
                                             int64_t max_rows, int idx) {
   if (s.offsets == nullptr) {
-    const int n = s.T / s.B;
-    const int tiles = (n * G + ROWS - 1) / ROWS;
-    const int b = idx / tiles;
-    return {b < s.B ? b : -1, b * n, n, (idx - b * tiles) * ROWS};
+    const int b = by.tiles(idx);
+    return {b < s.B ? b : -1, b * by.n, by.n, (idx - b * by.tiles.d) * ROWS};
   }
+  const int G = by.G.d;
   const int lane = threadIdx.x & 63;
   int64_t base = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
