@@ -78,7 +78,10 @@ __device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile
   p1 = first + p.by.G(t.row0 + rows - 1);
 }
 
-template <int DT, int D, int RT>
+// ONCE: a sequence's rows are one tile, so that its cache is read once: past the
+// caches (64 requests of up to 16384 positions, 8 kv heads: 131 us against 144; where
+// many tiles read the same pages it costs 8%).
+template <int DT, int D, int RT, bool ONCE>
 __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3 : 2) void k_kv4_attend_few(Kv4FewArgs p) {
   constexpr int kRows = 16 * RT, kGd = kv4_groups(D), kKw = D / 32, kTd = D / 16;   // key words, channel tiles
   constexpr bool kTwice = DT == F16;   // weights in two parts
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
           kc[i][0] = a[0];
           kc[i][1] = a[1];
         } else {
-          const v4i a = ld16(kb + (off_k + 64 * gd));
+          const v4i a = ONCE ? ld16_stream(kb + (off_k + 64 * gd)) : ld16(kb + (off_k + 64 * gd));
 #pragma unroll
           for (int j = 0; j < 4; ++j) kc[i][4 * gd + j] = a[j];
         }
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
       const char* const pb = at[i] + (S * D + (kGd * S + slot) * 4);
 #pragma unroll
       for (int gd = 0; gd < kGd; ++gd) {
-        vc[i][gd] = ld16(vb + (off_v + 256 * gd));
+        vc[i][gd] = ONCE ? ld16_stream(vb + (off_v + 256 * gd)) : ld16(vb + (off_v + 256 * gd));
         vp[i][gd] = ld16(pb + gd * 4 * S + off_p);
       }
     }
@@ -572,9 +575,12 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     // 16 rows a tile where a sequence has no more on average, else 32
     a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
     a.few_tiles = tiles(a.few_rows, wide ? 0 : kFewRows);
-    // splits of the cached positions: enough workgroups for the GPU, at least 256 positions each
-    const int64_t want = up(512, a.few_tiles * H);
-    a.splits = (int)std::max<int64_t>(1, std::min(want, capacity / 256));
+    // Splits of the cached positions.  A workgroup on each CU, of 256 positions or more
+    // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 20); four on
+    // each where that leaves 2048 positions or more, for sequences of uneven lengths
+    // (64 of 4096 to 16384: 131 us against 143).  Joining costs some 4 us.
+    const int64_t all = a.few_tiles * H;
+    a.splits = (int)std::max<int64_t>({1, std::min(up(256, all), capacity / 256), std::min(up(2048, all), capacity / 2048)});
   }
   if (many) {
     const auto of = [&](int64_t tile) {
@@ -599,7 +605,10 @@ int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_
 
 template <int DT, int D, int RT>
 static hipError_t few_t(Kv4FewArgs p, int64_t tiles, hipStream_t st) {
-  k_kv4_attend_few<DT, D, RT><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
+  if (p.by.n > 0 && (int64_t)p.by.n * p.G <= 16 * RT)
+    k_kv4_attend_few<DT, D, RT, true><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
+  else
+    k_kv4_attend_few<DT, D, RT, false><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
   if (p.splits > 1) {
     // workgroups of 16 items of 8 channels; without offsets the rows of a tile are known
     const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(16 * RT, (int64_t)p.by.n * p.G) : 16 * RT;
