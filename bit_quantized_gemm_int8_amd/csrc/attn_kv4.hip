@@ -53,7 +53,7 @@ struct Kv4FewArgs {
   int G, splits;
   Kv4Divs by;
   Kv4Div by_splits;
-  int64_t max_rows;   // sequences of more rows are another kernel's
+  int64_t min_rows, max_rows;   // sequences of other numbers of rows are another kernel's
   float* part_o;
   float* part_ml;
 };
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int th = p.by_splits((int)blockIdx.x), split = blockIdx.x - th * p.splits;
   const int tile_n = p.by.H(th), h = th - tile_n * p.s.H;
-  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, 1, p.max_rows, tile_n);
+  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, p.min_rows, p.max_rows, tile_n);
   if (t.b < 0) return;
   int p0, p1, first, rows;
   kv4_positions<kRows>(p, t, p0, p1, first, rows);
@@ -496,16 +496,16 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
   }
 }
 
-// Join the splits of a tile, each in the unit of its sh.  16 lanes take the
-// splits of 8 channels of a row in turn, so that their loads are under way together.
-template <int DT, int D, int ROWS>
+// Join the splits of a tile, each in the unit of its sh.  SUB lanes take the splits
+// of 8 channels of a row in turn, so that their loads are under way together.
+template <int DT, int D, int ROWS, int SUB>
 __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_most, Kv4Div parts) {
   const int th = parts((int)blockIdx.x), part = blockIdx.x - th * parts.d;
   const int tile_n = p.by.H(th), h = th - tile_n * p.s.H;
-  const Kv4Tile t = kv4_tile<ROWS>(p.s, p.by, 1, p.max_rows, tile_n);
+  const Kv4Tile t = kv4_tile<ROWS>(p.s, p.by, p.min_rows, p.max_rows, tile_n);
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, rows_most);
-  const int item = part * 16 + (int)threadIdx.x / 16, sub = threadIdx.x & 15;
+  const int item = part * (256 / SUB) + (int)threadIdx.x / SUB, sub = threadIdx.x & (SUB - 1);
   if (item >= rows * (D / 8)) return;
   const int row = item / (D / 8), d = 8 * (item % (D / 8));
   const float* const ml = p.part_ml + ((int64_t)th * p.splits * ROWS + row) * 2;
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_
   float low = kUnset, l = 0.f, x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  for (int v = sub; v < p.splits; v += 16) {
+  for (int v = sub; v < p.splits; v += SUB) {
     const v2f two = *(const v2f*)(ml + (int64_t)v * ROWS * 2);
     const v4f a = *(const v4f*)(po + (int64_t)v * ROWS * D), b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
     const float sh = two[0], sum = two[1];
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_
     }
   }
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
+  for (int o = 1; o < SUB; o <<= 1) {
     const float sh = __shfl_xor(low, o, kWave), sum = __shfl_xor(l, o, kWave);
     const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
     low = to;
@@ -555,8 +555,9 @@ constexpr int64_t kFewRows = 64;
 
 struct AttendPlan {
   int64_t few_tiles, many_tiles;   // tiles of a kv head, 0: no launch
-  int few_rows, many_rows;         // rows of a tile
-  int splits;
+  int few_rows;                    // rows of a tile of the former
+  int few_splits, many_splits;     // of the cached positions
+  int64_t few_part, many_part;     // floats of their parts
   bool fits;
 };
 
@@ -564,33 +565,34 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
   AttendPlan a = {};
   const int64_t G = Hq / H, rows = T * G;
   const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-  const auto tiles = [&](int64_t tile, int64_t most) {
-    // of sequences with at most `most` rows each, `rows` together
-    if (uniform) return B * up(rows / B, tile);
-    return std::min(std::min(rows, rows / tile + B), most == 0 ? rows : B * up(most, tile));
-  };
   const bool wide = D == 256;   // all rows here
   const bool few = wide || !uniform || rows / B <= kFewRows, many = !wide && (uniform ? !few : rows > kFewRows);
   if (few) {
     // 16 rows a tile where a sequence has no more on average, else 32
     a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
-    a.few_tiles = tiles(a.few_rows, wide ? 0 : kFewRows);
+    if (uniform) a.few_tiles = B * up(rows / B, a.few_rows);
+    else a.few_tiles = std::min(std::min(rows, rows / a.few_rows + B), wide ? rows : B * up(kFewRows, a.few_rows));
     // Splits of the cached positions.  A workgroup on each CU, of 256 positions or more
     // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 20); four on
     // each where that leaves 2048 positions or more, for sequences of uneven lengths
     // (64 of 4096 to 16384: 131 us against 143).  Joining costs some 4 us.
     const int64_t all = a.few_tiles * H;
-    a.splits = (int)std::max<int64_t>({1, std::min(up(256, all), capacity / 256), std::min(up(2048, all), capacity / 2048)});
+    a.few_splits = (int)std::max<int64_t>({1, std::min(up(256, all), capacity / 256), std::min(up(2048, all), capacity / 2048)});
+    a.few_part = a.few_splits > 1 ? all * a.few_splits * a.few_rows * (D + 2) : 0;
   }
   if (many) {
-    const auto of = [&](int64_t tile) {
-      return uniform ? tiles(tile, 0) : rows / tile + std::min(B, rows / (kFewRows + 1));
-    };
-    a.many_rows = D < 256 && of(256) * H >= 512 ? 256 : 128;
-    a.many_tiles = of(a.many_rows);
+    a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + std::min(B, rows / (kFewRows + 1));
+    const int64_t all = a.many_tiles * H;
+    // a workgroup on each CU, of 512 positions or more
+    a.many_splits = (int)std::max<int64_t>(1, std::min(256 / all, capacity / 512));
+    a.many_part = a.many_splits > 1 ? all * a.many_splits * kKv4ManyRows * (D + 2) : 0;
   }
-  // a launch holds fewer than 2^32 threads
-  a.fits = a.few_tiles * H * std::max(a.splits, 1) < (int64_t)1 << 24 && a.many_tiles * H < (int64_t)1 << 23;
+  // a launch holds fewer than 2^32 threads; a join has up to 16 for 8 channels of a row
+  const auto fits = [&](int64_t tiles, int splits, int64_t threads, int64_t joins) {
+    return tiles * H * std::max<int64_t>(splits * threads, splits > 1 ? joins * (D / 8) + 256 : 0) < (int64_t)1 << 32;
+  };
+  a.fits = fits(a.few_tiles, std::max(a.few_splits, 1), 64 * kAttnWaves, 16 * a.few_rows) &&
+           fits(a.many_tiles, std::max(a.many_splits, 1), 2 * kKv4ManyRows, 4 * kKv4ManyRows);
   return a;
 }
 
@@ -599,8 +601,15 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
 int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
                              int64_t capacity, bool uniform) {
   const AttendPlan a = attend_plan(T, B, Hq, H, D, capacity, uniform);
-  if (!a.fits) return -1;
-  return a.splits > 1 ? a.few_tiles * H * a.splits * a.few_rows * (D + 2) * 4 : 0;
+  return a.fits ? std::max(a.few_part, a.many_part) * 4 : -1;   // one after the other
+}
+
+template <int DT, int D, int ROWS, int SUB>
+static void join_t(const Kv4FewArgs& p, int64_t tiles, hipStream_t st) {
+  // workgroups of 256 / SUB items of 8 channels; without offsets the rows of a tile are known
+  const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(ROWS, (int64_t)p.by.n * p.G) : ROWS;
+  const Kv4Div parts = kv4_div((rows * (D / 8) * SUB + 255) / 256);
+  k_kv4_attend_join<DT, D, ROWS, SUB><<<(unsigned)(tiles * parts.d), 256, 0, st>>>(p, (int)rows, parts);
 }
 
 template <int DT, int D, int RT>
@@ -609,12 +618,7 @@ static hipError_t few_t(Kv4FewArgs p, int64_t tiles, hipStream_t st) {
     k_kv4_attend_few<DT, D, RT, true><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
   else
     k_kv4_attend_few<DT, D, RT, false><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
-  if (p.splits > 1) {
-    // workgroups of 16 items of 8 channels; without offsets the rows of a tile are known
-    const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(16 * RT, (int64_t)p.by.n * p.G) : 16 * RT;
-    const Kv4Div parts = kv4_div((rows * (D / 8) + 15) / 16);
-    k_kv4_attend_join<DT, D, 16 * RT><<<(unsigned)(tiles * parts.d), 256, 0, st>>>(p, (int)rows, parts);
-  }
+  if (p.splits > 1) join_t<DT, D, 16 * RT, 16>(p, tiles, st);
   return hipGetLastError();
 }
 
@@ -630,21 +634,32 @@ hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hi
   const int64_t capacity = (int64_t)s.W << s.shift;
   const int64_t seen = a.window > 0 ? std::min<int64_t>(capacity, (int64_t)a.window + a.sinks + kFewRows + 2 * kStep) : capacity;
   const AttendPlan plan = attend_plan(s.T, s.B, a.Hq, s.H, a.D, seen, s.offsets == nullptr);
-  if (plan.many_tiles > 0) {
-    const hipError_t e = launch_kv4_many(s, a, dtype, s.offsets == nullptr ? 1 : kFewRows + 1, plan.many_rows,
-                                         plan.many_tiles, st);
-    if (e != hipSuccess || plan.few_tiles == 0) return e;
-  }
   Kv4FewArgs p;
   p.s = s;
   p.a = a;
   p.G = a.Hq / s.H;
-  p.max_rows = plan.many_tiles > 0 || s.offsets != nullptr && a.D < 256 ? kFewRows : (int64_t)1 << 40;
-  p.splits = plan.splits;
+  p.part_o = (float*)a.workspace;
+  if (plan.many_tiles > 0) {
+    const int64_t tiles = plan.many_tiles * s.H;
+    p.min_rows = s.offsets == nullptr ? 1 : kFewRows + 1;
+    p.max_rows = (int64_t)1 << 40;
+    p.splits = plan.many_splits;
+    p.part_ml = p.part_o + tiles * p.splits * kKv4ManyRows * a.D;
+    hipError_t e = launch_kv4_many(s, a, dtype, p.min_rows, plan.many_tiles, p.splits, p.part_o, p.part_ml, st);
+    if (e == hipSuccess && p.splits > 1) {
+      p.by = kv4_divs(s, p.G, kKv4ManyRows);
+      if (dtype == F16) a.D == 64 ? join_t<F16, 64, kKv4ManyRows, 4>(p, tiles, st) : join_t<F16, 128, kKv4ManyRows, 4>(p, tiles, st);
+      else a.D == 64 ? join_t<BF16, 64, kKv4ManyRows, 4>(p, tiles, st) : join_t<BF16, 128, kKv4ManyRows, 4>(p, tiles, st);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess || plan.few_tiles == 0) return e;
+  }
+  p.min_rows = 1;
+  p.max_rows = s.offsets != nullptr && a.D < 256 ? kFewRows : (int64_t)1 << 40;
+  p.splits = plan.few_splits;
   p.by = kv4_divs(s, p.G, plan.few_rows);
   p.by_splits = kv4_div(p.splits);
   const int64_t tiles = plan.few_tiles * s.H;
-  p.part_o = (float*)a.workspace;
   p.part_ml = p.part_o + tiles * p.splits * plan.few_rows * a.D;
   return dtype == F16 ? few_d<F16>(p, a.D, plan.few_rows, tiles, st) : few_d<BF16>(p, a.D, plan.few_rows, tiles, st);
 }

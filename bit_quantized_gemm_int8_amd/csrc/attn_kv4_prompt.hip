@@ -1,7 +1,7 @@
 // Attention of many query rows over the 4-bit paged KV cache (qg_kv4.hpp):
 // prompts and chunks of them, heads of 64 and 128 channels.  The mathematics is
 // that of attn_kv4.hip; here the codes of 64 positions become binary16 values once
-// for all rows of a workgroup.
+// for all 256 rows of a workgroup.
 //
 // A value (q - z) s has 11 significant bits.  Scaled by a power of two that takes s
 // to [2^-18, 2^-8) it is exact in binary16, and since a nibble masked out of a code
@@ -33,8 +33,10 @@ namespace {
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 64;      // positions of a tile
+constexpr int kManyWaves = kKv4ManyRows / 32;
 constexpr int kVBufs = 3;      // tiles of values at hand (two of keys)
 constexpr float kLow = -3.402823466e38f;
 constexpr float kUnset = 1e30f;
@@ -77,14 +79,16 @@ __device__ __forceinline__ void for_each(F&& f) {
 struct Kv4ManyArgs {
   Kv4Seqs s;
   Kv4Attend a;
-  int G, tiles;
+  int G, tiles, splits;
   Kv4Divs by;
+  Kv4Div by_splits;
   int64_t min_rows;   // sequences of fewer rows are another kernel's
+  float *part_o, *part_ml;
 };
 
-template <int DT, int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv4ManyArgs p) {
-  constexpr int NT = 64 * NW, kRows = 32 * NW, kC = D / 8;   // code words of a position
+template <int DT, int D>
+__global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyArgs p) {
+  constexpr int NW = kManyWaves, NT = 64 * NW, kRows = kKv4ManyRows, kC = D / 8;   // code words of a position
   constexpr int kSt = D / 16;        // steps of the first product
   constexpr int kDt = D / 32;        // channel tiles of the second
   // values: [tile % bufs][position / 32][step][half][channel], keys: [tile % 2][position / 32]
@@ -99,17 +103,25 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int H = p.s.H;
-  const int tile_n = p.by.H((int)blockIdx.x), h = blockIdx.x - tile_n * H;
+  const int from = p.by_splits((int)blockIdx.x), split = blockIdx.x - from * p.splits;
+  const int tile_n = p.by.H(from), h = from - tile_n * H;
   // the rows that see most first
   const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, p.min_rows, (int64_t)1 << 40, p.tiles - 1 - tile_n);
+  const int64_t part = (((int64_t)(p.tiles - 1 - tile_n) * H + h) * p.splits + split) * kRows;
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, kRows);
   const int len = min(max(p.s.lengths[t.b], -0x3FFFFFFF), 0x3FFFFFFF);
   const int first = len - t.n;
-  const int p0 = first + t.row0 / p.G, p1 = first + (t.row0 + rows - 1) / p.G;
+  const int p0 = first + p.by.G(t.row0), p1 = first + p.by.G(t.row0 + rows - 1);
   const int shift = p.s.shift, S = 1 << shift, W = p.s.W, window = p.a.window, sinks = p.a.sinks;
   const int capacity = (int)min((int64_t)W << shift, (int64_t)0x40000000);
   const Kv4Span span = kv4_span<kTile>(p0, p1, window, sinks, capacity);
+  const int per = (span.tiles + p.splits - 1) / p.splits, first_tile = split * per;
+  const int n_tiles = min(per, span.tiles - first_tile);   // of this split
+  if (n_tiles <= 0 && p.splits > 1) {   // the join leaves it out
+    if (tid < kRows) *(v2f*)(p.part_ml + (part + tid) * 2) = v2f{kUnset, 0.f};
+    return;
+  }
   const int32_t* table = p.s.table + (int64_t)t.b * W;
   const int page_words = (int)kv4_words(S, D);
 
@@ -117,15 +129,16 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   const int c = lane & 31, half = lane >> 5;
   const int row = t.row0 + 32 * wave + c;
   const bool there = 32 * wave + c < rows;
-  const int pos = there ? first + row / p.G : kKv4Past;
+  const int row_token = p.by.G(row);
+  const int pos = there ? first + row_token : kKv4Past;
   const bool alive = 32 * wave < rows;                               // the wave has rows
   const int last_row = min(32 * wave + 31, rows - 1);
-  const int wp0 = first + (t.row0 + 32 * wave) / p.G, wp1 = first + (t.row0 + last_row) / p.G;
+  const int wp0 = first + p.by.G(t.row0 + 32 * wave), wp1 = first + p.by.G(t.row0 + last_row);
   v8h q[kSt];
   float cc;
   {
     float x[kSt][8], top = 0.f;
-    const int64_t at = (int64_t)(t.token0 + row / p.G) * p.a.q_stride + (int64_t)(h * p.G + row % p.G) * D;
+    const int64_t at = (int64_t)(t.token0 + row_token) * p.a.q_stride + (int64_t)(h * p.G + row - row_token * p.G) * D;
 #pragma unroll
     for (int j = 0; j < kSt; ++j) {
       const v4i a = there ? ld16((const uint16_t*)p.a.q + at + 16 * j + 8 * half) : v4i{0, 0, 0, 0};
@@ -159,7 +172,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   constexpr int NH = NT / 2, kN = kTile * kC / 4, kL = (kN + NH - 1) / NH;
   const bool keys = wave < NW / 2;
   const int htid = keys ? tid : tid - NH;
-  const int n_tiles = span.tiles;
   const char* const pool = (const char*)(p.s.pages + (int64_t)h * page_words);
   const u32 page_step = (u32)H * (u32)page_words * 4u;   // < 2^32: 1024 heads of 256 positions of 136 bytes
   const int inside = S < kTile ? S - 1 : kTile - 1;      // bits of a position that the thread holds
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
     }
   };
 
-  auto tile_at = [&](int u) QG_INLINE { return span.tile(min(u, n_tiles - 1)); };
+  auto tile_at = [&](int u) QG_INLINE { return span.tile(first_tile + min(u, n_tiles - 1)); };
   if (n_tiles > 0) {
     // the first tile, and from its largest scales the common powers of two
     fetch_ids(tile_at(0));
@@ -563,8 +575,20 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
   // ---- outputs: lane (c, half) has, of row c, eight runs of 8 channels ---------------
   l += __shfl_xor(l, 32, kWave);
   if (!there) return;
-  const int64_t to = ((int64_t)(t.token0 + row / p.G) * p.a.Hq + h * p.G + row % p.G) * D;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const int64_t to = ((int64_t)(t.token0 + row_token) * p.a.Hq + h * p.G + row - row_token * p.G) * D;
+  const bool whole = p.splits == 1;
+  const int64_t to_part = (part + 32 * wave + c) * D;
+  // 8 channels of the output, or of this split's in the unit of its sh
+  auto store = [&](int d, const float (&x)[8]) QG_INLINE {
+    if (whole) {
+      kv4_store8<DT>(p.a.out, to + d, x);
+    } else {
+      *(v4f*)(p.part_o + to_part + d) = v4f{x[0], x[1], x[2], x[3]};
+      *(v4f*)(p.part_o + to_part + d + 4) = v4f{x[4], x[5], x[6], x[7]};
+    }
+  };
+  if (!whole && half == 0) *(v2f*)(p.part_ml + (part + 32 * wave + c) * 2) = v2f{sh, l};
+  const float inv = !whole ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
   const float f = ldexpf(inv, 9 + ev);
   if constexpr (D == 64) {
     // place 32 j + 8 a + 4 half + b holds channel 8 (place % 8) + place / 8
@@ -575,7 +599,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int a = 0; a < 4; ++a) x[4 * j + a] = o[j][4 * a + b] * f;
-      kv4_store8<DT>(p.a.out, to + 32 * half + 8 * b, x);
+      store(32 * half + 8 * b, x);
     }
   } else {
     // place 32 j + 8 a + 4 half + b holds channel 8 (place % 16) + place / 16
@@ -589,7 +613,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void k_kv4_attend_many(Kv
           x[2 * j] = o[j][4 * a + b] * f;
           x[2 * j + 1] = o[j][4 * (a + 2) + b] * f;
         }
-        kv4_store8<DT>(p.a.out, to + 64 * a + 32 * half + 8 * b, x);
+        store(64 * a + 32 * half + 8 * b, x);
       }
   }
 }
@@ -599,24 +623,21 @@ namespace {
 template <int D>
 constexpr int many_lds() { return (kVBufs + 2) * kTile * (D / 8) * 16 + 8 * kTile * 4 + 16 * 4 + 8 * 2 * kTile * 4; }
 
-template <int DT, int D, int NW>
-hipError_t many_t(Kv4ManyArgs p, hipStream_t st) {
-  k_kv4_attend_many<DT, D, NW><<<(unsigned)(p.tiles * p.s.H), 64 * NW, many_lds<D>(), st>>>(p);
+template <int DT>
+hipError_t many_t(const Kv4ManyArgs& p, hipStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)p.tiles * p.s.H * p.splits);
+  if (p.a.D == 64) k_kv4_attend_many<DT, 64><<<grid, 64 * kManyWaves, many_lds<64>(), st>>>(p);
+  else k_kv4_attend_many<DT, 128><<<grid, 64 * kManyWaves, many_lds<128>(), st>>>(p);
   return hipGetLastError();
-}
-
-template <int DT, int NW>
-hipError_t many_d(const Kv4ManyArgs& p, hipStream_t st) {
-  return p.a.D == 64 ? many_t<DT, 64, NW>(p, st) : many_t<DT, 128, NW>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int rows,
-                           int64_t tiles, hipStream_t st) {
-  const Kv4ManyArgs p{s, a, a.Hq / s.H, (int)tiles, kv4_divs(s, a.Hq / s.H, rows), min_rows};
-  if (rows == 256) return dtype == F16 ? many_d<F16, 8>(p, st) : many_d<BF16, 8>(p, st);
-  return dtype == F16 ? many_d<F16, 4>(p, st) : many_d<BF16, 4>(p, st);
+hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int64_t tiles,
+                           int splits, float* part_o, float* part_ml, hipStream_t st) {
+  const Kv4ManyArgs p{s, a, a.Hq / s.H, (int)tiles, splits, kv4_divs(s, a.Hq / s.H, kKv4ManyRows), kv4_div(splits),
+                      min_rows, part_o, part_ml};
+  return dtype == F16 ? many_t<F16>(p, st) : many_t<BF16>(p, st);
 }
 
 }  // namespace qg

@@ -110,4 +110,7 @@ __device__ __forceinline__ Kv4Span kv4_span(int p0, int p1, int window, int sink
 // Position of row `row` of a tile's sequence (kPast: the row does not exist).
 constexpr int kKv4Past = -0x40000000;
 
+// Rows of a workgroup of the prompt kernel.
+constexpr int kKv4ManyRows = 256;
+
 }  // namespace qg

@@ -134,9 +134,10 @@ hipError_t launch_kv4_dequant(const Kv4Seqs& s, int D, void* k, void* v, int out
                               hipStream_t st);
 hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st);
 // The part of launch_kv4_attend for sequences of at least min_rows rows (tokens
-// times query heads of a kv head): `tiles` tiles of `rows` (128 or 256) rows.
-hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int rows,
-                           int64_t tiles, hipStream_t st);
+// times query heads of a kv head), in `tiles` tiles a kv head; with splits > 1
+// outputs [tile][head][split][row][D] and (exponent, sum) for a join.
+hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int64_t tiles,
+                           int splits, float* part_o, float* part_ml, hipStream_t st);
 // Bytes of device workspace launch_kv4_attend needs (uniform: no offsets), -1
 // where a launch would not hold the call.
 int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
