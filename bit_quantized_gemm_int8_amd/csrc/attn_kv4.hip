@@ -5,9 +5,11 @@
 // The codes n go to the matrix cores as they are:
 //   q . k_t = s_t (sum_d q_d n_td - z_t sum_d q_d)
 //   o       = (sum_t (p_t s_t) n_t - sum_t (p_t s_t) z_t) / sum_t p_t
-// A nibble masked out of a code word is a binary16 subnormal, n 2^-24 (or
-// n 2^-20 one nibble up), which gfx950's matrix cores take exactly: unpacking
-// costs one AND for two codes.  Queries are scaled to binary16's upper range by
+// A nibble masked out of a code word is a binary16 subnormal, n 2^-20 at bits 4 to 7
+// of its half, which gfx950's matrix cores take exactly: unpacking costs an AND and at
+// most a shift for two codes.  (At bits 0 to 3 they do not: an operand n 2^-24 counts
+// with the exponent of 2^-14 when the products are aligned, and sums of 32 came out up
+// to 1.6e-5 of their terms too small, against 1.3e-7 for n 2^-20.)  Queries are scaled to binary16's upper range by
 // a power of two of their row, exactly for bfloat16 and binary16 inputs; the
 // weights p s are rounded to binary16 (half a step: 2^-11), the codes' sum and
 // the zero points' sum taking the same rounded weights, both through the matrix
@@ -32,6 +34,7 @@ namespace {
 constexpr int kStep = 32;            // positions of a wave's step
 constexpr int kAttnWaves = 4;
 constexpr float kLowest = -3.402823466e38f, kUnset = 1e30f;
+constexpr u32 kNibbles = 0x00F000F0u;
 
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
@@ -165,8 +168,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
   };
 
   // ---- queries -------------------------------------------------------------------
-  // A lane's words in the order of the unpacked codes (nibbles 0 4 1 5 2 6 3 7, the
-  // second of each byte 16 times as large), and their sum.
+  // A lane's words in the order of the unpacked codes (nibbles 0 4 1 5 2 6 3 7), and
+  // their sum.
   int pos[RT];
   v8h q[RT][kKw];
   float cc[RT], qs[RT][kGd];
@@ -221,14 +224,14 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
       for (int i = 0; i < 8; ++i) {
         const float v = ldexpf(x[j][order[i]], e2);
         sum += v;
-        q[r][j][i] = (_Float16)((i & 2) ? v * 0.0625f : v);
+        q[r][j][i] = (_Float16)v;
       }
       qs[r][j / 4] += sum;
     }
-    // scores in units of 2^(e2 - 24), exponents in base 2
+    // scores in units of 2^(e2 - 20), exponents in base 2
 #pragma unroll
-    for (int gd = 0; gd < kGd; ++gd) qs[r][gd] = sum16(qs[r][gd]) * 0x1p-24f;
-    cc[r] = ldexpf(p.a.scale * 1.44269504088896f, 24 - e2);
+    for (int gd = 0; gd < kGd; ++gd) qs[r][gd] = sum16(qs[r][gd]) * 0x1p-20f;
+    cc[r] = ldexpf(p.a.scale * 1.44269504088896f, 20 - e2);
   }
 
   // outputs: rows = channels, columns = query rows; sums of the zero points
@@ -278,9 +281,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
       v8h kf[kKw];
 #pragma unroll
       for (int j = 0; j < kKw; ++j) {
-        const u32 w = (u32)kc[i][j], hi = w >> 8;
-        kf[j] = __builtin_bit_cast(v8h, v4i{(int)(w & 0x000F000Fu), (int)(w & 0x00F000F0u),
-                                            (int)(hi & 0x000F000Fu), (int)(hi & 0x00F000F0u)});
+        const u32 w = (u32)kc[i][j];
+        kf[j] = __builtin_bit_cast(v8h, v4i{(int)(w << 4 & kNibbles), (int)(w & kNibbles), (int)(w >> 4 & kNibbles),
+                                            (int)(w >> 8 & kNibbles)});
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r)
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
         for (int e = 0; e < 4; ++e) sv[gd][i][e] = kv4_scale((u32)vp[i][gd][e]) * unit[gd];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          zf[gd][i][e] = ((u32)vp[i][gd][2 * e] & 15u) | (((u32)vp[i][gd][2 * e + 1] & 15u) << 16);
+          zf[gd][i][e] = (((u32)vp[i][gd][2 * e] & 15u) | (((u32)vp[i][gd][2 * e + 1] & 15u) << 16)) << 4;
       }
     load_keys(u + kAttnWaves);
     // weights
@@ -409,10 +412,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
           }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const u32 mask = (j & 1) ? 0x00F000F0u : 0x000F000Fu;
           v4i vf;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vf[e] = (int)((j & 2 ? x[e] >> 8 : x[e]) & mask);
+          for (int e = 0; e < 4; ++e) vf[e] = (int)((j == 0 ? x[e] << 4 : x[e] >> (4 * (j - 1))) & kNibbles);
           const int td = 8 * gd + 4 * half + j;
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
@@ -462,7 +464,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
           v4f x;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            x[k] = (o[r][gd * kPer + j + k][e] * ((k & 1) ? 0x1p20f : 0x1p24f) - oz[r][gd][0] * 0x1p24f) * f;
+            x[k] = (o[r][gd * kPer + j + k][e] - oz[r][gd][0]) * (f * 0x1p20f);
           *(v4f*)(to + j) = x;
         }
       }
@@ -550,8 +552,11 @@ namespace {
 
 // Sequences of up to kFewRows rows are this file's, longer ones the prompt
 // kernel's.  Without offsets the call's sequences are alike; with them the GPU
-// tells, so that both kernels are launched where either may have some.
-constexpr int64_t kFewRows = 64;
+// tells, so that both kernels are launched where either may have some.  Rows times
+// kv heads of 128 at which they meet (us, this kernel and the other): 8 requests of 8
+// kv heads and 4096 positions 64 rows 38 and 41, 128 rows 54 and 48; one of 8192
+// positions 256 rows 35 and 39, 512 rows 51 and 47.
+constexpr int64_t kFewRows = 128;
 
 struct AttendPlan {
   int64_t few_tiles, many_tiles;   // tiles of a kv head, 0: no launch

@@ -193,7 +193,7 @@ ATTEND = [
     (128, 64, 1, 4, "bf16", [257], None, 257, 0, 0),
     (64, 16, 1, 1, "f16", [130], None, 130, 1, 0),                        # only itself
     (128, 32, 1, 1, "bf16", [40], None, 1, 1, 64),
-    # many rows of a sequence: the prompt kernel's tiles, 128 rows or 256
+    # many rows of a sequence: the prompt kernel
     (128, 16, 2, 2, "bf16", [333, 200], None, 190, 0, 0),
     (128, 64, 1, 8, "f16", [100, 1000], None, 65, 0, 0),
     (128, 256, 3, 3, "f16", [129], None, 129, 0, 0),
@@ -206,8 +206,10 @@ ATTEND = [
     (128, 64, 1, 1, "f16", [700], None, 300, 100, 600),                   # first positions reach into the window
     (128, 64, 2, 2, "bf16", [60, 500], None, 100, 0, 0),                  # rows ahead of position 0
     (128, 32, 2, 4, "f16", [400, 9, 300, 50, 333], [0, 200, 201, 203, 253, 353], 0, 0, 0),   # rows for both kernels
-    (64, 16, 256, 256, "f16", [257], None, 257, 0, 0),
-    (128, 64, 256, 256, "bf16", [300], None, 257, 90, 3),
+    (64, 16, 20, 20, "f16", [257], None, 257, 0, 0),
+    (128, 64, 2, 4, "f16", [2100, 700], None, 130, 0, 0),                 # its positions in splits
+    (64, 32, 1, 4, "bf16", [2500], [1, 300], 0, 1500, 30),
+    (128, 128, 3, 6, "bf16", [1800, 600, 40], [0, 130, 131, 135], 0, 0, 0),
 ]
 
 
@@ -251,7 +253,7 @@ def test_attend(case):
 @pytest.mark.parametrize("q_scale,kv_scale", [(1e-6, 1.0), (300.0, 1e-3), (1.0, 1e-20), (1e-3, 1e4)])
 def test_attend_scales(q_scale, kv_scale):
     """Queries and values far from 1; the scores stay within a few hundred."""
-    for n in (2, 45):
+    for n in (2, 70):
         case = (128, 32, 2, 4, "bf16", [300, 45], None, n, 0, 0)
         check_attend(*run_attend(case, q_scale=q_scale, kv_scale=kv_scale, scale=0.09 / (q_scale * kv_scale)))
 
@@ -286,7 +288,7 @@ def test_attend_large_values_with_small_weights(D, n):
     assert (worst <= 0).all()
 
 
-@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("n", [3, 40, 70])
 def test_attend_out_of_sight(n):
     """NaN, infinite and huge groups, and table entries of no page, where no row
     may look: behind the last position, outside the window, in other pages."""
@@ -311,7 +313,7 @@ def test_attend_out_of_sight(n):
     check_attend(*run_attend(case, edit=edit))
 
 
-@pytest.mark.parametrize("D,Hq", [(64, 1), (64, 2), (256, 2)])
+@pytest.mark.parametrize("D,Hq", [(64, 1), (64, 2), (64, 4), (128, 5), (256, 2)])
 def test_attend_rows_that_see_nothing_or_nan(D, Hq):
     page, gd = 16, max(1, D // 128)
     c = D // 8
