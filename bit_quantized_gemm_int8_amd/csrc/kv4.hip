@@ -46,165 +46,277 @@ __device__ __forceinline__ u32 kv4_group(float lo, float hi, float& s, float& r)
 // 8 codes as a word.  The quotient x / s is within (-15.5, 15.5); its nearest
 // integer comes from x r unless that lies within 2^-15 of a tie, and from the
 // correctly rounded division there (as in sym_code_t, whose bound on the two's
-// distance holds here too).
+// distance holds here too): one test for the 8.
 __device__ __forceinline__ u32 kv4_codes(const float (&x)[8], float s, float r, u32 word) {
-  if (!(s >= 0x1p-126f)) {   // subnormal scales count as zero: no kernel has to know them
-    s = 0.f;
-    return 0u;
-  }
+  if (!(s >= 0x1p-126f)) return 0u;   // a scale of zero, or the mark of a group without one
   const float z = (float)(word & 15u);
-  u32 out = 0;
+  float t[8], far = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float a = x[e] * r;
-    float t = rintf(a);
-    if (!(fabsf(a - t) <= kCodeTie)) t = rintf(x[e] / s);
-    out |= (u32)__builtin_amdgcn_fmed3f(t + z, 0.f, 15.f) << (4 * e);
+    t[e] = rintf(a);
+    far = fmaxf(far, fabsf(a - t[e]));
   }
+  if (!(far <= kCodeTie)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = rintf(x[e] / s);
+  }
+  u32 out = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out |= (u32)__builtin_amdgcn_fmed3f(t[e] + z, 0.f, 15.f) << (4 * e);
   return out;
 }
 
 }  // namespace
 
-// One row (token) of one head: D / 16 neighbouring threads with two chunks of 8
-// channels each, the two that a rotation by halves pairs up.  A workgroup takes
-// one token and up to 256 / (D / 16) of its heads, queries first, then keys,
-// then values.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void k_kv4_append(Kv4Seqs s, Kv4Append a, int parts) {
+// Rows a workgroup takes where a call has many.
+constexpr int kQuad = 4;
+
+// Whether rows row .. row + 3 are the four positions of one block of value codes.
+__device__ __forceinline__ bool kv4_quad(const Kv4Row& at, int row) {
+  return at.b >= 0 && row + kQuad <= at.end && (at.pos & (kQuad - 1)) == 0;
+}
+
+// What a thread of an append works on: a head's rows, and its chunks in them.
+struct Kv4Head {
+  const void* src;     // the operand's
+  int64_t stride;      // elements from row to row
+  int h, l;            // head of the operand, thread of the head
+  bool is_q, is_k;
+};
+
+// N rows (tokens) of one head: D / 16 neighbouring threads with two chunks of 8
+// channels each, the two that a rotation by halves pairs up.  N = 4 is for the
+// positions of one block of value codes, whose words go out side by side.
+template <int DT, int D, int N>
+__device__ __forceinline__ void kv4_append_rows(const Kv4Seqs& s, const Kv4Append& a, int row,
+                                                const Kv4Row& at, const Kv4Head& w) {
   constexpr int kL = D / 16, kGd = kv4_groups(D);
-  const int row = blockIdx.x / parts, part = blockIdx.x - row * parts;
-  const int heads = a.Hq + 2 * s.H;
-  const int hh = part * (int)(blockDim.x / kL) + (int)threadIdx.x / kL, l = (int)threadIdx.x % kL;
-  if (hh >= heads) return;   // whole groups of kL lanes: the exchanges below stay complete
-  const Kv4Row at = kv4_row(s, row);
-  if (at.b < 0) return;      // rows of no sequence stay as they are
-  const int rc = a.rot >> 4;   // chunks of a half of the rotated channels
+  const int l = w.l, rc = a.rot >> 4;   // chunks of a half of the rotated channels
   const int c0 = l < rc ? l : 2 * rc + (l - rc), c1 = l < rc ? l + rc : c0 + (kL - rc);
   const bool known = a.rot == 0 || (at.pos >= 0 && at.pos < a.table_rows);
-  const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + s.H;
-  const int h = is_q ? hh : is_k ? hh - a.Hq : hh - a.Hq - s.H;
-  const void* src = is_q ? a.q : is_k ? a.k : a.v;
-  const int64_t base = row * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (int64_t)h * D;
+  const bool is_q = w.is_q, is_k = w.is_k;
+  const int h = w.h;
   int slot = 0;
   int32_t* page = nullptr;
   if (!is_q) {
     page = known ? kv4_page(s, at.b, at.pos, h, D, slot) : nullptr;
     if (page == nullptr) return;   // the kL lanes of a head alike
   }
-  float x0[8], x1[8];
-  kv4_load8<DT>(src, base + 8 * c0, x0);
-  kv4_load8<DT>(src, base + 8 * c1, x1);
+  float x0[N][8], x1[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    kv4_load8<DT>(w.src, (row + n) * w.stride + (int64_t)h * D + 8 * c0, x0[n]);
+    kv4_load8<DT>(w.src, (row + n) * w.stride + (int64_t)h * D + 8 * c1, x1[n]);
+  }
   if ((is_q || is_k) && l < rc) {
-    const int64_t tab = known ? at.pos * (a.rot >> 1) : 0;
-    if (a.interleaved) {   // angle i turns channels 2 i and 2 i + 1
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        kv4_turn(x0[2 * e], x0[2 * e + 1], a.cos[tab + 4 * c0 + e], a.sin[tab + 4 * c0 + e]);
-        kv4_turn(x1[2 * e], x1[2 * e + 1], a.cos[tab + 4 * c1 + e], a.sin[tab + 4 * c1 + e]);
+    for (int n = 0; n < N; ++n) {
+      const int64_t tab = known ? (at.pos + n) * (a.rot >> 1) : 0;
+      if (a.interleaved) {   // angle i turns channels 2 i and 2 i + 1
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kv4_turn(x0[n][2 * e], x0[n][2 * e + 1], a.cos[tab + 4 * c0 + e], a.sin[tab + 4 * c0 + e]);
+          kv4_turn(x1[n][2 * e], x1[n][2 * e + 1], a.cos[tab + 4 * c1 + e], a.sin[tab + 4 * c1 + e]);
+        }
+      } else {               // angle i turns channels i and i + rot / 2
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          kv4_turn(x0[n][e], x1[n][e], a.cos[tab + 8 * c0 + e], a.sin[tab + 8 * c0 + e]);
       }
-    } else {               // angle i turns channels i and i + rot / 2
-#pragma unroll
-      for (int e = 0; e < 8; ++e) kv4_turn(x0[e], x1[e], a.cos[tab + 8 * c0 + e], a.sin[tab + 8 * c0 + e]);
     }
   }
   if (is_q) {
-    if (!known) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x0[e] = x1[e] = 0.f;
+    for (int n = 0; n < N; ++n) {
+      if (!known) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x0[n][e] = x1[n][e] = 0.f;
+      }
+      const int64_t o = ((int64_t)(row + n) * a.Hq + h) * D;
+      kv4_store8<DT>(a.q_out, o + 8 * c0, x0[n]);
+      kv4_store8<DT>(a.q_out, o + 8 * c1, x1[n]);
     }
-    const int64_t o = ((int64_t)row * a.Hq + h) * D;
-    kv4_store8<DT>(a.q_out, o + 8 * c0, x0);
-    kv4_store8<DT>(a.q_out, o + 8 * c1, x1);
     return;
   }
-  // range of each group, zero included; a value that is not finite makes it infinite
-  float lo[kGd], hi[kGd];
+  const int g0 = c0 >> 4, g1 = c1 >> 4;
+  u32 q0[N], q1[N], word[N][kGd];
 #pragma unroll
-  for (int g = 0; g < kGd; ++g) lo[g] = hi[g] = 0.f;
+  for (int n = 0; n < N; ++n) {
+    // range of each group, zero included; a value that is not finite makes it infinite
+    float lo[kGd], hi[kGd];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    float mn = 0.f, mx = 0.f, odd = 0.f;
+    for (int g = 0; g < kGd; ++g) lo[g] = hi[g] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = t ? x1[e] : x0[e];
-      mn = fminf(mn, v);
-      mx = fmaxf(mx, v);
-      odd = __builtin_fmaf(v, 0.f, odd);
+    for (int t = 0; t < 2; ++t) {
+      float mn = 0.f, mx = 0.f, odd = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = t ? x1[n][e] : x0[n][e];
+        mn = fminf(mn, v);
+        mx = fmaxf(mx, v);
+        odd = __builtin_fmaf(v, 0.f, odd);
+      }
+      if (odd != 0.f) mx = __builtin_inff();
+      const int g = t ? g1 : g0;
+#pragma unroll
+      for (int i = 0; i < kGd; ++i) {
+        lo[i] = g == i ? fminf(lo[i], mn) : lo[i];
+        hi[i] = g == i ? fmaxf(hi[i], mx) : hi[i];
+      }
     }
-    if (odd != 0.f) mx = __builtin_inff();
-    const int g = (t ? c1 : c0) >> 4;
+    float sc[kGd], re[kGd];
 #pragma unroll
-    for (int i = 0; i < kGd; ++i) {
-      lo[i] = g == i ? fminf(lo[i], mn) : lo[i];
-      hi[i] = g == i ? fmaxf(hi[i], mx) : hi[i];
+    for (int g = 0; g < kGd; ++g) {
+#pragma unroll
+      for (int o = 1; o < kL; o <<= 1) {
+        lo[g] = fminf(lo[g], __shfl_xor(lo[g], o, kWave));
+        hi[g] = fmaxf(hi[g], __shfl_xor(hi[g], o, kWave));
+      }
+      word[n][g] = kv4_group(lo[g], hi[g], sc[g], re[g]);
     }
+    q0[n] = kv4_codes(x0[n], g0 ? sc[kGd - 1] : sc[0], g0 ? re[kGd - 1] : re[0], g0 ? word[n][kGd - 1] : word[n][0]);
+    q1[n] = kv4_codes(x1[n], g1 ? sc[kGd - 1] : sc[0], g1 ? re[kGd - 1] : re[0], g1 ? word[n][kGd - 1] : word[n][0]);
   }
-  float sc[kGd], rc_[kGd];
-  u32 word[kGd];
+  const int S = 1 << s.shift;
+  int32_t* const codes = is_k ? page + slot * (D / 8) : page + S * (D / 8) + (slot >> 2) * (D / 2) + (slot & 3);
+  int32_t* const par = page + S * (D / 4) + (is_k ? 0 : kGd * S) + (l < kGd ? l * S : 0) + slot;
+  if constexpr (N == kQuad) {
+    if (is_k) {
 #pragma unroll
-  for (int g = 0; g < kGd; ++g) {
-#pragma unroll
-    for (int o = 1; o < kL; o <<= 1) {
-      lo[g] = fminf(lo[g], __shfl_xor(lo[g], o, kWave));
-      hi[g] = fmaxf(hi[g], __shfl_xor(hi[g], o, kWave));
+      for (int n = 0; n < N; ++n) {
+        codes[n * (D / 8) + c0] = (int32_t)q0[n];
+        codes[n * (D / 8) + c1] = (int32_t)q1[n];
+      }
+    } else {
+      st16(codes + 4 * c0, v4i{(int)q0[0], (int)q0[1], (int)q0[2], (int)q0[3]});
+      st16(codes + 4 * c1, v4i{(int)q1[0], (int)q1[1], (int)q1[2], (int)q1[3]});
     }
-    word[g] = kv4_group(lo[g], hi[g], sc[g], rc_[g]);
+    if (l < kGd) {
+      v4i w;
+#pragma unroll
+      for (int n = 0; n < N; ++n) w[n] = (int)(l ? word[n][kGd - 1] : word[n][0]);
+      st16(par, w);
+    }
+  } else {
+    const int step = is_k ? 1 : 4;
+    codes[c0 * step] = (int32_t)q0[0];
+    codes[c1 * step] = (int32_t)q1[0];
+    if (l < kGd) *par = (int32_t)(l ? word[0][kGd - 1] : word[0][0]);
   }
-  const int S = 1 << s.shift, g0 = c0 >> 4, g1 = c1 >> 4;
-  const u32 q0 = kv4_codes(x0, g0 ? sc[kGd - 1] : sc[0], g0 ? rc_[kGd - 1] : rc_[0], g0 ? word[kGd - 1] : word[0]);
-  const u32 q1 = kv4_codes(x1, g1 ? sc[kGd - 1] : sc[0], g1 ? rc_[kGd - 1] : rc_[0], g1 ? word[kGd - 1] : word[0]);
-  int32_t* codes = is_k ? page + (int64_t)slot * (D / 8)
-                        : page + S * (D / 8) + (slot >> 2) * (D / 2) + (slot & 3);
-  const int step = is_k ? 1 : 4;
-  codes[c0 * step] = (int32_t)q0;
-  codes[c1 * step] = (int32_t)q1;
-  int32_t* par = page + S * (D / 4) + (is_k ? 0 : kGd * S) + slot;
-  if (l < kGd) par[l * S] = (int32_t)(kGd > 1 && l ? word[kGd - 1] : word[0]);
 }
 
-// Values of the cached positions of the call's rows, [T][H][D] each: one thread
-// for 8 channels of keys or values; (q - z) s is exact in binary32.
-template <int DT, int D>
+// A workgroup takes ROWS tokens and up to 256 / (D / 16) of their heads, queries
+// first, then keys, then values.
+template <int DT, int D, int ROWS>
+__global__ __launch_bounds__(256) void k_kv4_append(Kv4Seqs s, Kv4Append a, int parts) {
+  constexpr int kL = D / 16;
+  const int part = blockIdx.x % parts, row = blockIdx.x / parts * ROWS;
+  const int hh = part * (int)(blockDim.x / kL) + (int)threadIdx.x / kL, l = (int)threadIdx.x % kL;
+  if (hh >= a.Hq + 2 * s.H) return;   // whole groups of kL lanes: the exchanges stay complete
+  const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + s.H;
+  const Kv4Head w{is_q ? a.q : is_k ? a.k : a.v, is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride,
+                  is_q ? hh : is_k ? hh - a.Hq : hh - a.Hq - s.H, l, is_q, is_k};
+  const Kv4Row at = kv4_row(s, row);
+  if constexpr (ROWS == kQuad) {
+    // the last of four positions has its angles if and only if the first has
+    const bool alike = a.rot == 0 || at.pos + kQuad <= a.table_rows || at.pos >= a.table_rows;
+    if (kv4_quad(at, row) && alike) return kv4_append_rows<DT, D, kQuad>(s, a, row, at, w);
+    for (int r = 0; r < kQuad; ++r) {
+      if (row + r >= s.T) return;
+      const Kv4Row one = kv4_row(s, row + r);
+      if (one.b >= 0) kv4_append_rows<DT, D, 1>(s, a, row + r, one, w);
+    }
+  } else {
+    if (at.b >= 0) kv4_append_rows<DT, D, 1>(s, a, row, at, w);   // rows of no sequence stay as they are
+  }
+}
+
+// N rows of one chunk of 8 channels of one head.
+template <int DT, int D, int N>
+__device__ __forceinline__ void kv4_dequant_rows(const Kv4Seqs& s, void* out, int row, const Kv4Row& at,
+                                                 int h, int is_v, int c) {
+  constexpr int kC = D / 8, kGd = kv4_groups(D);
+  const int S = 1 << s.shift;
+  int slot = 0;
+  const int32_t* const page = kv4_page(s, at.b, at.pos, h, D, slot);
+  u32 w[N], p[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) w[n] = p[n] = 0;   // zeros where the position has no page
+  if (page != nullptr) {
+    const int32_t* const par = page + S * (D / 4) + (is_v ? kGd * S : 0) + (c >> 4) * S + slot;
+    const int32_t* const codes = is_v ? page + S * kC + (slot >> 2) * (D / 2) + 4 * c + (slot & 3) : page + slot * kC + c;
+    if constexpr (N == kQuad) {
+      const v4i pw = ld16(par);
+      if (is_v) {
+        const v4i cw = ld16(codes);
+#pragma unroll
+        for (int n = 0; n < N; ++n) w[n] = (u32)cw[n];
+      } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) w[n] = (u32)codes[n * kC];
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) p[n] = (u32)pw[n];
+    } else {
+      w[0] = (u32)*codes;
+      p[0] = (u32)*par;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const float sc = kv4_scale(p[n]);
+    const int z = (int)(p[n] & 15u);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w[n] >> (4 * e)) & 15u) - z) * sc;
+    kv4_store8<DT>(out, ((int64_t)(row + n) * s.H + h) * D + 8 * c, x);
+  }
+}
+
+// Values of the cached positions of the call's rows, [T][H][D] each: ROWS rows and
+// up to 256 chunks of 8 channels of keys or values a workgroup.  (q - z) s is exact
+// in binary32.
+template <int DT, int D, int ROWS>
 __global__ __launch_bounds__(256) void k_kv4_dequant(Kv4Seqs s, void* __restrict__ k,
                                                      void* __restrict__ v, int parts) {
   constexpr int kC = D / 8;
-  const int row = blockIdx.x / parts, part = blockIdx.x - row * parts;
-  const int i = part * (int)blockDim.x + (int)threadIdx.x;
-  if (i >= 2 * s.H * kC) return;
+  const int part = blockIdx.x % parts, row = blockIdx.x / parts * ROWS;
+  const int at_c = part * (int)blockDim.x + (int)threadIdx.x;
+  if (at_c >= 2 * s.H * kC) return;
+  const int c = at_c % kC, hv = at_c / kC, is_v = hv >= s.H, h = is_v ? hv - s.H : hv;
+  void* const out = is_v ? v : k;
   const Kv4Row at = kv4_row(s, row);
-  if (at.b < 0) return;
-  const int c = i % kC, hv = i / kC, is_v = hv >= s.H, h = is_v ? hv - s.H : hv;
-  const int S = 1 << s.shift;
-  int slot = 0;
-  const int32_t* page = kv4_page(s, at.b, at.pos, h, D, slot);
-  float x[8];
-  if (page == nullptr) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  if constexpr (ROWS == kQuad) {
+    if (kv4_quad(at, row)) return kv4_dequant_rows<DT, D, kQuad>(s, out, row, at, h, is_v, c);
+    for (int r = 0; r < kQuad; ++r) {
+      if (row + r >= s.T) return;
+      const Kv4Row one = kv4_row(s, row + r);
+      if (one.b >= 0) kv4_dequant_rows<DT, D, 1>(s, out, row + r, one, h, is_v, c);
+    }
   } else {
-    const u32 w = is_v ? page[S * kC + (slot >> 2) * (D / 2) + 4 * c + (slot & 3)]
-                       : page[slot * kC + c];
-    const u32 p = page[S * (D / 4) + (is_v ? kv4_groups(D) * S : 0) + (c >> 4) * S + slot];
-    const float sc = kv4_scale(p);
-    const int z = (int)(p & 15u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - z) * sc;
+    if (at.b >= 0) kv4_dequant_rows<DT, D, 1>(s, out, row, at, h, is_v, c);   // rows of no sequence stay as they are
   }
-  kv4_store8<DT>(is_v ? v : k, ((int64_t)row * s.H + h) * D + 8 * c, x);
 }
 
-// Threads and workgroups of one row of `items` threads.
+// Threads and workgroups of one row of `items` threads: workgroups as even as whole
+// waves and whole heads (`head` threads, a divisor of 64) allow.
 static void kv4_split(int64_t items, int& threads, int& parts) {
-  threads = (int)std::min<int64_t>(256, (items + 63) / 64 * 64);
-  parts = (int)((items + threads - 1) / threads);
+  parts = (int)((items + 255) / 256);
+  threads = (int)(((items + parts - 1) / parts + 63) / 64 * 64);
 }
+
+// Rows of a workgroup: KV4_RULE
+static bool kv4_quads(int T, int parts) { return (int64_t)T * parts >= 4096; }
 
 template <int DT, int D>
 static hipError_t kv4_append_t(const Kv4Seqs& s, const Kv4Append& a, hipStream_t st) {
   int threads, parts;
   kv4_split((int64_t)(a.Hq + 2 * s.H) * (D / 16), threads, parts);
-  k_kv4_append<DT, D><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, a, parts);
+  if (kv4_quads(s.T, parts))
+    k_kv4_append<DT, D, kQuad><<<(unsigned)(((int64_t)s.T + kQuad - 1) / kQuad * parts), threads, 0, st>>>(s, a, parts);
+  else
+    k_kv4_append<DT, D, 1><<<(unsigned)(s.T * parts), threads, 0, st>>>(s, a, parts);
   return hipGetLastError();
 }
 
@@ -229,7 +341,10 @@ template <int DT, int D>
 static hipError_t kv4_dequant_t(const Kv4Seqs& s, void* k, void* v, hipStream_t st) {
   int threads, parts;
   kv4_split((int64_t)2 * s.H * (D / 8), threads, parts);
-  k_kv4_dequant<DT, D><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, k, v, parts);
+  if (kv4_quads(s.T, parts))
+    k_kv4_dequant<DT, D, kQuad><<<(unsigned)(((int64_t)s.T + kQuad - 1) / kQuad * parts), threads, 0, st>>>(s, k, v, parts);
+  else
+    k_kv4_dequant<DT, D, 1><<<(unsigned)(s.T * parts), threads, 0, st>>>(s, k, v, parts);
   return hipGetLastError();
 }
 

@@ -84,6 +84,7 @@ __device__ __forceinline__ void kv4_store8(void* p, int64_t at, const float (&v)
 struct Kv4Row {
   int b;
   int64_t pos;
+  int64_t end;   // first row behind the sequence's
 };
 
 __device__ __forceinline__ Kv4Row kv4_row(const Kv4Seqs& s, int row) {
@@ -101,10 +102,10 @@ __device__ __forceinline__ Kv4Row kv4_row(const Kv4Seqs& s, int row) {
       else hi = mid;
     }
     b = lo;
-    if (b >= s.B || row < s.offsets[b]) return {-1, -1};
+    if (b >= s.B || row < s.offsets[b]) return {-1, -1, 0};
     end = s.offsets[b + 1];
   }
-  return {b, (int64_t)s.lengths[b] - end + row};
+  return {b, (int64_t)s.lengths[b] - end + row, end};
 }
 
 // First word of position pos of sequence b in head h, and its slot; NULL
