@@ -558,11 +558,19 @@ namespace {
 // positions 256 rows 35 and 39, 512 rows 51 and 47.
 constexpr int64_t kFewRows = 128;
 
+// With offsets, sequences of few rows among longer ones have whole tiles of the
+// prompt kernel where the tiles find room side by side and no row sees more than
+// this: the second kernel and its join cost more (a chunk of 1500 tokens and two
+// tokens of two other requests, 16 heads, a window of 2048 positions: 66 us,
+// with both kernels 79).
+constexpr int64_t kOneSight = 4096;
+
 struct AttendPlan {
   int64_t few_tiles, many_tiles;   // tiles of a kv head, 0: no launch
   int few_rows;                    // rows of a tile of the former
   int few_splits, many_splits;     // of the cached positions
   int64_t few_part, many_part;     // floats of their parts
+  bool one;                        // the latter's sequences may be of any length
   bool fits;
 };
 
@@ -571,7 +579,9 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
   const int64_t G = Hq / H, rows = T * G;
   const auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const bool wide = D == 256;   // all rows here
-  const bool few = wide || !uniform || rows / B <= kFewRows, many = !wide && (uniform ? !few : rows > kFewRows);
+  const bool long_ones = rows / B > kFewRows;   // on average
+  a.one = !uniform && !wide && long_ones && capacity <= kOneSight && (rows / kKv4ManyRows + B) * H <= 256;
+  const bool few = wide || !(uniform ? long_ones : a.one), many = !wide && (uniform ? long_ones : rows > kFewRows);
   if (few) {
     // 16 rows a tile where a sequence has no more on average, else 32
     a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
@@ -586,7 +596,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     a.few_part = a.few_splits > 1 ? all * a.few_splits * a.few_rows * (D + 2) : 0;
   }
   if (many) {
-    a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + std::min(B, rows / (kFewRows + 1));
+    a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + (a.one ? B : std::min(B, rows / (kFewRows + 1)));
     const int64_t all = a.many_tiles * H;
     // a workgroup on each CU, of 512 positions or more
     a.many_splits = (int)std::max<int64_t>(1, std::min(256 / all, capacity / 512));
@@ -605,8 +615,11 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
 
 int64_t kv4_attend_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
                              int64_t capacity, bool uniform) {
+  // A call's window may let its rows see less, which leaves fewer splits and may leave one kernel.
   const AttendPlan a = attend_plan(T, B, Hq, H, D, capacity, uniform);
-  return a.fits ? std::max(a.few_part, a.many_part) * 4 : -1;   // one after the other
+  const AttendPlan b = attend_plan(T, B, Hq, H, D, std::min(capacity, kOneSight), uniform);
+  if (!a.fits || !b.fits) return -1;
+  return std::max({a.few_part, a.many_part, b.few_part, b.many_part}) * 4;   // one kernel after the other
 }
 
 template <int DT, int D, int ROWS, int SUB>
@@ -615,6 +628,14 @@ static void join_t(const Kv4FewArgs& p, int64_t tiles, hipStream_t st) {
   const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(ROWS, (int64_t)p.by.n * p.G) : ROWS;
   const Kv4Div parts = kv4_div((rows * (D / 8) * SUB + 255) / 256);
   k_kv4_attend_join<DT, D, ROWS, SUB><<<(unsigned)(tiles * parts.d), 256, 0, st>>>(p, (int)rows, parts);
+}
+
+// A thread takes up to 4 splits by itself (2 splits of 6000 rows: 7 us, with 4 lanes
+// to each item 14), more are shared out.
+template <int DT, int D>
+static void join_many(const Kv4FewArgs& p, int64_t tiles, hipStream_t st) {
+  if (p.splits <= 4) join_t<DT, D, kKv4ManyRows, 1>(p, tiles, st);
+  else join_t<DT, D, kKv4ManyRows, 4>(p, tiles, st);
 }
 
 template <int DT, int D, int RT>
@@ -646,15 +667,15 @@ hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hi
   p.part_o = (float*)a.workspace;
   if (plan.many_tiles > 0) {
     const int64_t tiles = plan.many_tiles * s.H;
-    p.min_rows = s.offsets == nullptr ? 1 : kFewRows + 1;
+    p.min_rows = s.offsets == nullptr || plan.one ? 1 : kFewRows + 1;
     p.max_rows = (int64_t)1 << 40;
     p.splits = plan.many_splits;
     p.part_ml = p.part_o + tiles * p.splits * kKv4ManyRows * a.D;
     hipError_t e = launch_kv4_many(s, a, dtype, p.min_rows, plan.many_tiles, p.splits, p.part_o, p.part_ml, st);
     if (e == hipSuccess && p.splits > 1) {
       p.by = kv4_divs(s, p.G, kKv4ManyRows);
-      if (dtype == F16) a.D == 64 ? join_t<F16, 64, kKv4ManyRows, 4>(p, tiles, st) : join_t<F16, 128, kKv4ManyRows, 4>(p, tiles, st);
-      else a.D == 64 ? join_t<BF16, 64, kKv4ManyRows, 4>(p, tiles, st) : join_t<BF16, 128, kKv4ManyRows, 4>(p, tiles, st);
+      if (dtype == F16) a.D == 64 ? join_many<F16, 64>(p, tiles, st) : join_many<F16, 128>(p, tiles, st);
+      else a.D == 64 ? join_many<BF16, 64>(p, tiles, st) : join_many<BF16, 128>(p, tiles, st);
       e = hipGetLastError();
     }
     if (e != hipSuccess || plan.few_tiles == 0) return e;
