@@ -718,7 +718,8 @@ int64_t kv_u4_page_bytes(int64_t page, int64_t D);
  * cos, sin: [table_rows][rot / 2] float, read; rot a multiple of 16 up to D,
  * 0 for no rotation (then cos and sin may be NULL and q is copied).
  * q_out: [T][Hq][D] of dtype, written; it may be q where q_stride is Hq * D.
- * Two rows of one call for one position: either's codes.
+ * A position is one row's: where two rows of a call have the same position of the
+ * same page, its codes and group words are some of either's.
  */
 qg_status_t append_kv_u4_pages(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                const void* v, int64_t v_stride, int dtype, const float* cos,
@@ -752,9 +753,13 @@ qg_status_t dequantize_kv_u4_pages(const int32_t* pages, int64_t P, int64_t page
  * workspace: attend_kv_u4_pages_workspace_bytes(...) bytes of device memory, 16-byte
  * aligned (NULL where that is 0), free again when the call's work is done;
  * calls that overlap on the GPU need one each.
- * Scores, weights and sums are binary32; the weights times their value scales
- * are rounded to binary16 (relative to the row's largest, 2^-11) for the matrix
- * cores.  The order of a row's sums goes by the sizes of the call.
+ * Scores, weights and sums are binary32.  For the matrix cores the weights (in calls
+ * of few rows the weights times their value scales) are rounded to binary16: 2^-11
+ * of a weight, no less than 2^-24 of the row's largest; twice as many bits in calls
+ * of few rows with binary16 outputs.  Scores up to 2^22 in magnitude: past that,
+ * where neighbours in binary32 are 1/2 and more apart, outputs are not specified.
+ * Which of two kernels a row goes through, and with it the order of its sums and the
+ * rounding of its weights, goes by the sizes of the call, never by its values.
  */
 int64_t attend_kv_u4_pages_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D,
                                            int64_t page, int64_t W, int ragged /* offsets given */);
