@@ -774,10 +774,18 @@ def kv_u4_pages(P: int, H: int, page: int, D: int, device="cuda") -> torch.Tenso
     return torch.zeros((P, H, words), dtype=torch.int32, device=device)
 
 
+def _there(t, dtype, index) -> bool:
+    """Whether t is a contiguous tensor of dtype on GPU `index`: what _dev checks, in
+    a third of its time (a token's calls are bound by the host)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
+
+
 def _kv4_where(pages, page_table, lengths, offsets, D):
     """Checked operands that the calls on a paged cache share: device, pointers
     and sizes (pages, P, page, H, page_table, W, lengths, offsets, B)."""
-    pp = _dev(pages, "pages", (torch.int32,))
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or not _there(pages, torch.int32, pages.get_device()):
+        _dev(pages, "pages", (torch.int32,))
     if pages.dim() != 3:
         raise ValueError("pages must be [P, H, words]")
     P, H, words = pages.shape
@@ -788,11 +796,18 @@ def _kv4_where(pages, page_table, lengths, offsets, D):
     if page * per != words or page not in (16, 32, 64, 128, 256):
         raise ValueError(f"pages of {words} words do not hold 16, 32, 64, 128 or 256 positions of {D} channels")
     dev = pages.device
+    index = dev.index
     B, W = _2d(page_table, "page_table")
-    pt = _dev(page_table, "page_table", (torch.int32,), None, dev)
-    pl = _dev(lengths, "lengths", (torch.int32,), (B,), dev)
-    po = _opt(offsets, "offsets", (torch.int32,), (B + 1,), dev)
-    return dev, pp, P, page, H, pt, W, pl, po, B
+    if not _there(page_table, torch.int32, index):
+        _dev(page_table, "page_table", (torch.int32,), None, dev)
+    if not (_there(lengths, torch.int32, index) and lengths.shape == (B,)):
+        _dev(lengths, "lengths", (torch.int32,), (B,), dev)
+    po = None
+    if offsets is not None:
+        if not (_there(offsets, torch.int32, index) and offsets.shape == (B + 1,)):
+            _dev(offsets, "offsets", (torch.int32,), (B + 1,), dev)
+        po = offsets.data_ptr()
+    return dev, pages.data_ptr(), P, page, H, page_table.data_ptr(), W, lengths.data_ptr(), po, B
 
 
 def _heads(t, name, dtypes, device, T=None, D=None):
@@ -800,20 +815,21 @@ def _heads(t, name, dtypes, device, T=None, D=None):
     contiguous; tokens may be further apart (a view of a fused projection)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (D is not None and t.shape[2] != D):
+    shape = t.shape
+    if len(shape) != 3 or (T is not None and shape[0] != T) or (D is not None and shape[2] != D):
         raise ValueError(f"{name} must be [{'T' if T is None else T}, heads, {'D' if D is None else D}], "
-                         f"got {tuple(t.shape)}")
-    rows, heads, d = t.shape
+                         f"got {tuple(shape)}")
+    rows, heads, d = shape
     step, by_head, by_one = t.stride()
     if (d > 1 and by_one != 1) or (heads > 1 and by_head != d):
         raise ValueError(f"{name} must have contiguous heads")
     if rows <= 1:
         step = heads * d
-    if step < heads * d:
+    elif step < heads * d:
         raise ValueError(f"{name} has tokens that overlap")
     return t.data_ptr(), step
 
@@ -845,13 +861,16 @@ def append_kv_u4_pages(k, v, pages, page_table, lengths, offsets=None, q=None, c
         rot = 2 * half
         if rot % 16 or not 0 < rot <= D:
             raise ValueError(f"cos must have a multiple of 8 columns up to {D // 2}, got {half}")
-        pc = _dev(cos, "cos", (torch.float32,), None, dev)
-        ps = _dev(sin, "sin", (torch.float32,), (rows, half), dev)
+        if not _there(cos, torch.float32, dev.index):
+            _dev(cos, "cos", (torch.float32,), None, dev)
+        if not (_there(sin, torch.float32, dev.index) and sin.shape == cos.shape):
+            _dev(sin, "sin", (torch.float32,), (rows, half), dev)
+        pc, ps = cos.data_ptr(), sin.data_ptr()
     pq, qs, Hq, y = None, 0, 0, None
     if q is not None:
         pq, qs = _heads(q, "q", (k.dtype,), dev, T, D)
         Hq = q.shape[1]
-        y = _out(out, (T, Hq, D), q.dtype, dev)
+        y = q.new_empty((T, Hq, D)) if out is None else _out(out, (T, Hq, D), q.dtype, dev)
     elif out is not None:
         raise ValueError("out is for the rotated q, and there is no q")
     _call_on(dev, "append_kv_u4_pages", pq, qs, pk, ks, pv, vs, _DTYPE_CODE[k.dtype], pc, ps, rows,
@@ -902,7 +921,7 @@ def attend_kv_u4_pages(q, pages, page_table, lengths, offsets=None, window=0, si
         raise ValueError(f"q has {Hq} heads, which the {H} heads of pages do not divide")
     if offsets is None and (T % B if B else T):
         raise ValueError(f"{T} rows are no whole number for each of {B} sequences")
-    y = _out(out, (T, Hq, D), q.dtype, dev)
+    y = q.new_empty((T, Hq, D)) if out is None else _out(out, (T, Hq, D), q.dtype, dev)
     need = (_lib or load()).attend_kv_u4_pages_workspace_bytes(T, B, Hq, H, D, page, W,
                                                                0 if offsets is None else 1)
     pw, size = None, 0
