@@ -226,7 +226,10 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     return __builtin_bit_cast(int, __builtin_elementwise_fma(__builtin_bit_cast(v2h, n), __builtin_bit_cast(v2h, s),
                                                              __builtin_bit_cast(v2h, z)));
   };
-  // In pieces, for the places between the products: piece k of kPieces.
+  // In pieces, piece k of kPieces: some for the places between the products, the rest
+  // for the turn behind them, ahead of the weights (all of them between the products:
+  // 160 us for a prompt of 4096 tokens of 32 heads, so 157; the products' turn is the
+  // longer one).  Words 0 and 1 of the keys are read ahead of that turn's barrier.
   constexpr int kPieces = 4 * kDt + 2 * kSt;
   u32 s24[kL][2], s20[kL][2], zz[kL][2];   // constants: of the keys' position, or of the values' two pairs
   float sv[kL][4];
@@ -283,15 +286,19 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
         v2i{fma2((j & 2 ? x >> 8 : x) & mask, j & 1 ? s20[i][0] : s24[i][0], zz[i][0]),
             fma2((j & 2 ? y >> 8 : y) & mask, j & 1 ? s20[i][1] : s24[i][1], zz[i][1])};
   };
-  auto piece = [&](auto role, auto at, int vb_at, int u) QG_INLINE {
+  constexpr int kWhole = 0, kBetween = 1, kBehind = 2;   // which pieces: all, those between the products, the others
+  constexpr int kKeysBetween = 3, kValuesBetween = 4;    // of 5 and 12
+  auto piece = [&](auto role, auto which, auto at, int vb_at, int u) QG_INLINE {
     constexpr bool KEYS = decltype(role)::value;
-    constexpr int k = decltype(at)::value;
+    constexpr int k = decltype(at)::value, WHICH = decltype(which)::value;
+    constexpr auto now = [](int w) { return WHICH == kWhole || (w < (KEYS ? kKeysBetween : kValuesBetween)) == (WHICH == kBetween); };
     if constexpr (KEYS) {
       // a fit, then its four words, two places apart
       constexpr int kEvery = kPieces / (5 * kL);
       if constexpr (k % kEvery == 0 && k / kEvery < 5 * kL) {
         constexpr int i = k / kEvery / 5, w = k / kEvery % 5;
-        if constexpr (w == 0) fit_key(i, u);
+        if constexpr (!now(w)) return;
+        else if constexpr (w == 0) fit_key(i, u);
         else word_of_key(i, w - 1, u);
       }
     } else {
@@ -299,7 +306,9 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       constexpr int kEvery = kPieces / (12 * kL);
       if constexpr (k % kEvery == 0 && k / kEvery < 12 * kL) {
         constexpr int i = k / kEvery / 12, w = k / kEvery % 12;
-        if constexpr (w < 4) {
+        if constexpr (!now(w)) {
+          return;
+        } else if constexpr (w < 4) {
           fit_value(i, w);
           if constexpr (w == 3) *(v4i*)&vraw[u & 3][off[i]] = word[i];
         } else {
@@ -311,7 +320,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   auto unpack = [&](auto role, int tile, int vb_at, int u) QG_INLINE {
     mark(role, tile);
     odd = false;
-    for_each<kPieces>([&](auto k) QG_INLINE { piece(role, k, vb_at, u); });
+    for_each<kPieces>([&](auto k) QG_INLINE { piece(role, std::integral_constant<int, kWhole>(), k, vb_at, u); });
   };
 
   // ---- the products of a tile ------------------------------------------------------
@@ -352,7 +361,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     kb = kbuf + (u & 1) * kTile * kC + half * 32 + c;
     for_each<kAhead - 1>([&](auto k) QG_INLINE { read(k); });
   };
-  auto fused = [&](auto role, int third, int fourth, int vb_at, int u) QG_INLINE {
+  auto fused = [&](auto role, int vb_at, int u) QG_INLINE {
     odd = false;
     __builtin_amdgcn_sched_barrier(0);
     for_each<kPieces>([&](auto at) QG_INLINE {
@@ -367,11 +376,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
         const v16f zero = {};
         s[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[j], j ? s[i] : zero, 0, 0, 0);
       }
-      piece(role, at, vb_at, u + 1);
-      if constexpr (k == kPieces - 2) {   // the codes are used: the next ones
-        fetch(third);
-        fetch_ids(fourth);
-      }
+      piece(role, std::integral_constant<int, kBetween>(), at, vb_at, u + 1);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -522,9 +527,10 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   }
   // In turn 2 u the first half has the products of tile u, in turn 2 u + 1 its
   // weights; the second half runs one turn behind.  Keys of tile u + 1 are written by
-  // the first half between its products of tile u, into the buffer that the second
-  // half read last in the turn before; values of tile u + 1 by the second half
-  // between its products of tile u, into that of tile u - 2.
+  // the first half in turns 2 u and 2 u + 1, into the buffer that the second half read
+  // last in turn 2 u - 1; values of tile u + 1 by the second half in turn 2 u + 2 (their
+  // group words in turn 2 u + 1), into that of tile u - 2, which was read last in turn
+  // 2 u - 1.  The first half needs the values in turn 2 u + 4.
   // Every turn has both products, so that the outputs stay in one place: where the
   // wave sees nothing of a tile its weights are zeros (and the values are finite).
   int vnow = 0;   // buffer of the tile's values
@@ -545,12 +551,16 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       mark(role, next);
       __builtin_amdgcn_s_setprio(1);
       const int flag = flags[u & 7];   // complete since the last turn
-      fused(role, third, fourth, vnext, u);
+      fused(role, vnext, u);
       __builtin_amdgcn_s_setprio(0);
       if (__any(odd)) flags[(u + 1) & 7] = 1;
       if (KEYS && wave == 0) flags[(u + 4) & 7] = 0;
       const bool is_odd = __builtin_amdgcn_readfirstlane(flag) != 0;
       lds_barrier();
+      for_each<kPieces>([&](auto k) QG_INLINE { piece(role, std::integral_constant<int, kBehind>(), k, vnext, u + 1); });
+      fetch(third);   // the codes are used: the next ones
+      fetch_ids(fourth);
+      __builtin_amdgcn_sched_barrier(0);
       const bool all = t0 >= all0 && t0 <= all1;
       if (t0 <= act1 && (t0 >= act0 || t0 < sinks0)) {
         // first positions that stay visible take the general form
@@ -562,9 +572,10 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       now = next;
       next = third;
       third = fourth;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the pieces are written, long since
       read_ahead(vnow, u + 1);
       vnow = vnext;
-      asm volatile("s_barrier" ::: "memory");   // nothing was written since the last one
+      asm volatile("s_barrier" ::: "memory");
     }
     if constexpr (KEYS) lds_barrier();
   };
