@@ -583,14 +583,17 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
   a.one = !uniform && !wide && long_ones && capacity <= kOneSight && (rows / kKv4ManyRows + B) * H <= 256;
   const bool few = wide || !(uniform ? long_ones : a.one), many = !wide && (uniform ? long_ones : rows > kFewRows);
   if (few) {
-    // 16 rows a tile where a sequence has no more on average, else 32
-    a.few_rows = D < 256 && rows > 16 * B ? 32 : 16;
+    // 32 rows a tile where that makes one tile of two, on average: 64 requests of 4 tokens
+    // of 8 query heads a kv head and 8192 positions 187 us, with 16 rows 201; 8 tokens each
+    // of 8 requests 41 and 40, 5 tokens of one of 16384 positions 14.2 and 13.2.
+    a.few_rows = D < 256 && rows > 16 * B && rows <= 32 * B ? 32 : 16;
     if (uniform) a.few_tiles = B * up(rows / B, a.few_rows);
     else a.few_tiles = std::min(std::min(rows, rows / a.few_rows + B), wide ? rows : B * up(kFewRows, a.few_rows));
     // Splits of the cached positions.  A workgroup on each CU, of 256 positions or more
-    // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 20); four on
-    // each where that leaves 2048 positions or more, for sequences of uneven lengths
-    // (64 of 4096 to 16384: 131 us against 143).  Joining costs some 4 us.
+    // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 35; 8 requests of
+    // 2047 and 2 heads in parts of 256 12 us, of 512 14); four on each where that leaves
+    // 2048 positions or more, for sequences of uneven lengths (64 of up to 16384: 131 us,
+    // without 152).  Joining costs some 4 us of it.
     const int64_t all = a.few_tiles * H;
     a.few_splits = (int)std::max<int64_t>({1, std::min(up(256, all), capacity / 256), std::min(up(2048, all), capacity / 2048)});
     a.few_part = a.few_splits > 1 ? all * a.few_splits * a.few_rows * (D + 2) : 0;
@@ -598,7 +601,8 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
   if (many) {
     a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + (a.one ? B : std::min(B, rows / (kFewRows + 1)));
     const int64_t all = a.many_tiles * H;
-    // a workgroup on each CU, of 512 positions or more
+    // a workgroup on each CU, of 512 positions or more (a chunk of 1500 tokens of 16 heads,
+    // a window of 2048 positions: 64 us in two parts, 81 whole)
     a.many_splits = (int)std::max<int64_t>(1, std::min(256 / all, capacity / 512));
     a.many_part = a.many_splits > 1 ? all * a.many_splits * kKv4ManyRows * (D + 2) : 0;
   }

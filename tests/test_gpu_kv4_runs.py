@@ -92,6 +92,11 @@ MORE = [
     (128, 32, 1, 8, "bf16", [3, 1000], [1, 5, 100], 0, 64, 0),
     # and in two: the sight is long
     (128, 256, 1, 2, "bf16", [4500, 700, 33], [0, 300, 301, 304], 0, 0, 0),
+    # tiles of 32 rows of the other kernel
+    (128, 64, 2, 8, "f16", [300, 1000], None, 8, 0, 0),
+    (64, 32, 1, 4, "bf16", [700, 50], None, 5, 60, 3),
+    (128, 32, 1, 4, "bf16", [400, 90, 300], [0, 9, 10, 18], 0, 0, 0),
+    (64, 16, 2, 4, "f16", [500, 40], [0, 20, 24], 0, 0, 0),
     # many splits of few tiles
     (128, 64, 1, 1, "f16", [4000], None, 130, 0, 0),
     (64, 128, 1, 2, "bf16", [5000], None, 70, 0, 0),
