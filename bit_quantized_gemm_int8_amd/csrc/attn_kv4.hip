@@ -9,11 +9,11 @@
 // of its half, which gfx950's matrix cores take exactly: unpacking costs an AND and at
 // most a shift for two codes.  (At bits 0 to 3 they do not: an operand n 2^-24 counts
 // with the exponent of 2^-14 when the products are aligned, and sums of 32 came out up
-// to 1.6e-5 of their terms too small, against 1.3e-7 for n 2^-20.)  Queries are scaled to binary16's upper range by
-// a power of two of their row, exactly for bfloat16 and binary16 inputs; the
-// weights p s are rounded to binary16 (half a step: 2^-11), the codes' sum and
-// the zero points' sum taking the same rounded weights, both through the matrix
-// cores.  Binary16 outputs, whose own rounding is no larger, get what the rounding
+// to 1.6e-5 of their terms too small, against 1.3e-7 for n 2^-20.)  Queries are
+// scaled to binary16's upper range by a power of two of their row, exactly for
+// bfloat16 and binary16 inputs; the weights p s are rounded to binary16 (half a step:
+// 2^-11), the codes' sum and the zero points' sum taking the same rounded weights,
+// both through the matrix cores.  Binary16 outputs, whose own rounding is no larger, get what the rounding
 // left over in a second product (2^-22).  Softmax and sums: binary32.
 //
 // Layout.  A wave takes 32 positions a step.  Both products have the query rows
@@ -23,6 +23,13 @@
 // word are neighbours in the cache for the same reason.  No lane exchange per
 // step: the weights are exp2(x + sh) for an sh of the row that falls only where a
 // weight passes 2^13, outputs and sum with it.
+//
+// What bounds it.  Many sequences: memory (64 requests of up to 16384 positions, 8 kv
+// heads of 128, 680 MB: 131 us, 5.2 TB/s).  One: latency, offsets, page table, codes and
+// the join in turn (4096 positions of 32 heads 12.8 us, a call of one page's positions
+// 9).  Heads of 256 with many rows: the vector unit, since the codes are unpacked again
+// for each 16 rows (149 us for 60 GFLOP; tiles of 32 rows need all registers of a wave
+// and more, and one wave a SIMD: 220).
 #include "qg_kv4_attn.hpp"
 
 #include <algorithm>
