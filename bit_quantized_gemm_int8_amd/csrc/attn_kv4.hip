@@ -82,8 +82,7 @@ template <int ROWS>
 __device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile& t, int& p0, int& p1,
                                               int& first, int& rows) {
   rows = min(t.n * p.G - t.row0, ROWS);
-  const int len = min(p.s.lengths[t.b], 0x3FFFFFFF);
-  first = max(len, -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
+  first = max(p.s.lengths[t.b], -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
   p0 = first + p.by.G(t.row0);
   p1 = first + p.by.G(t.row0 + rows - 1);
 }

@@ -117,8 +117,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   const int64_t part = (((int64_t)(p.tiles - 1 - tile_n) * H + h) * p.splits + split) * kRows;
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, kRows);
-  const int len = min(max(p.s.lengths[t.b], -0x3FFFFFFF), 0x3FFFFFFF);
-  const int first = len - t.n;
+  const int first = max(p.s.lengths[t.b], -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
   const int p0 = first + p.by.G(t.row0), p1 = first + p.by.G(t.row0 + rows - 1);
   const int shift = p.s.shift, S = 1 << shift, W = p.s.W, window = p.a.window, sinks = p.a.sinks;
   const int capacity = (int)min((int64_t)W << shift, (int64_t)0x40000000);

@@ -122,6 +122,59 @@ def test_attend_short_sequences_under_a_wide_page_table(D, n):
     check_attend(out_f64(got), want, bound, torch.finfo(torch.float16), own)
 
 
+@pytest.mark.parametrize("n", [1, 150])
+def test_attend_lengths_far_past_the_page_table(n):
+    """Positions near 2^31 - 1 under windows up to 2^30: the table's positions are behind
+    the window, all but the first ones that stay visible."""
+    D, H, page = 128, 1, 32
+    rng = np.random.default_rng(n)
+    pages, table = make_pool(rng, [200], page, H, D)
+    q = torch.from_numpy(rng.standard_normal((n, 1, D)).astype(np.float32)).half()
+    for length in (2 ** 31 - 1, 2 ** 30 + 2 ** 29):
+        for window in (1, 2 ** 29, 2 ** 30):
+            for sinks in (0, 3):
+                got = out_f64(qg.attend_kv_u4_pages(q.to(DEV), dev(pages), dev(table), i32([length]), window=window, sinks=sinks))
+                k, v, _ = kv4.values(pages, page, table[0], np.arange(3), D)
+                want, _ = kv4.attend(q.double().numpy(), k, v, np.tile(np.arange(3) < sinks, (n, 1)), D ** -0.5)
+                assert np.linalg.norm(got - want) <= (2.0 ** -11 + 2.0 ** -10) * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("D,H,Hq,n", [(64, 1, 1024, 1), (128, 1, 300, 1), (128, 512, 512, 1), (256, 1, 130, 2)])
+def test_attend_many_heads(D, H, Hq, n):
+    """Rows that are nearly all heads of one token, and many kv heads."""
+    check_attend(*run_attend((D, 16, H, Hq, "bf16", [45, 20], None, n, 0, 0)))
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 5), (256, 2)])
+def test_many_ragged_sequences(D, G):
+    """150 sequences, of no rows, one, a few, and some of many."""
+    rng = np.random.default_rng(D + G)
+    B, H, page = 150, 1, 16
+    counts = rng.integers(0, 3, B)
+    counts[[0, 63, 64, 100, 149]] = [0, 40, 150, 33, 0]
+    offsets = np.concatenate([[2], 2 + np.cumsum(counts)])
+    lengths = counts + rng.integers(0, 60, B)
+    T = int(offsets[-1]) + 3
+    pages, table = make_pool(rng, lengths, page, H, D, fill=False)
+    x = torch.from_numpy(rng.standard_normal((T, (G + 2) * H, D)).astype(np.float32)).half()
+    pd, td, ld, od = dev(pages), dev(table), i32(lengths), i32(offsets)
+    old = torch.from_numpy(rng.standard_normal((int(lengths.sum()), 2 * H, D)).astype(np.float32)).half()
+    ends = np.concatenate([[0], np.cumsum(lengths)])
+    qg.append_kv_u4_pages(*old.to(DEV).split(H, 1), pd, td, ld, offsets=i32(ends))          # all positions
+    q = x[:, :G * H]
+    qg.append_kv_u4_pages(*x[:, G * H:].to(DEV).split(H, 1), pd, td, ld, offsets=od)        # and the last ones again
+    for kv, w, o in ((old, kv4.rows(len(old), B, lengths, ends), 0), (x, kv4.rows(T, B, lengths, offsets), G * H)):
+        a = kv.float().numpy()
+        kv4.append(pages, page, w, table, a[:, o:o + H], a[:, o + H:])
+    np.testing.assert_array_equal(host_pages(pd), pages)
+    print(f"ragged {D} {G}", flush=True)
+    out = torch.full((T, G * H, D), 3.0, dtype=torch.float16, device=DEV)
+    qg.attend_kv_u4_pages(q.to(DEV), pd, td, ld, offsets=od, out=out)
+    want, bound, own = attend_case(pages, table, lengths, page, D, q.double().numpy(), T, offsets)
+    want[~own] = 3.0
+    check_attend(out_f64(out), want, bound, torch.finfo(torch.float16), own)
+
+
 def geometric(D, page, L, first, ratio, rising):
     """A cache whose position t scores first * ratio^t (rising) or the same from the
     other end, for queries of ones, up to the scales' rounding: keys of one value each
