@@ -784,28 +784,29 @@ def _there(t, dtype, index) -> bool:
 def _kv4_where(pages, page_table, lengths, offsets, D):
     """Checked operands that the calls on a paged cache share: device, pointers
     and sizes (pages, P, page, H, page_table, W, lengths, offsets, B)."""
-    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or not _there(pages, torch.int32, pages.get_device()):
-        _dev(pages, "pages", (torch.int32,))
+    i32 = torch.int32
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype is not i32 or not pages.is_contiguous():
+        _dev(pages, "pages", (i32,))
     if pages.dim() != 3:
         raise ValueError("pages must be [P, H, words]")
     P, H, words = pages.shape
-    per = D // 4 + max(2, D // 64)      # words of a position
     if D not in (64, 128, 256):
         raise ValueError(f"the head width must be 64, 128 or 256, got {D}")
+    per = D // 4 + max(2, D // 64)      # words of a position
     page = words // per
     if page * per != words or page not in (16, 32, 64, 128, 256):
         raise ValueError(f"pages of {words} words do not hold 16, 32, 64, 128 or 256 positions of {D} channels")
     dev = pages.device
     index = dev.index
     B, W = _2d(page_table, "page_table")
-    if not _there(page_table, torch.int32, index):
-        _dev(page_table, "page_table", (torch.int32,), None, dev)
-    if not (_there(lengths, torch.int32, index) and lengths.shape == (B,)):
-        _dev(lengths, "lengths", (torch.int32,), (B,), dev)
+    if not _there(page_table, i32, index):
+        _dev(page_table, "page_table", (i32,), None, dev)
+    if not _there(lengths, i32, index) or lengths.shape != (B,):
+        _dev(lengths, "lengths", (i32,), (B,), dev)
     po = None
     if offsets is not None:
-        if not (_there(offsets, torch.int32, index) and offsets.shape == (B + 1,)):
-            _dev(offsets, "offsets", (torch.int32,), (B + 1,), dev)
+        if not _there(offsets, i32, index) or offsets.shape != (B + 1,):
+            _dev(offsets, "offsets", (i32,), (B + 1,), dev)
         po = offsets.data_ptr()
     return dev, pages.data_ptr(), P, page, H, page_table.data_ptr(), W, lengths.data_ptr(), po, B
 
@@ -888,9 +889,13 @@ def dequantize_kv_u4_pages(pages, page_table, lengths, T, D, offsets=None, out_d
     if offsets is None and (T % B if B else T):
         raise ValueError(f"{T} rows are no whole number for each of {B} sequences")
     code = _float_code(out_dtype)
-    k, v = out if out is not None else (None, None)
-    k = _out(k, (T, H, D), out_dtype, dev, "k out")
-    v = _out(v, (T, H, D), out_dtype, dev, "v out")
+    if out is None:
+        k = pages.new_empty((T, H, D), dtype=out_dtype)
+        v = pages.new_empty((T, H, D), dtype=out_dtype)
+    else:
+        k, v = out
+        k = _out(k, (T, H, D), out_dtype, dev, "k out")
+        v = _out(v, (T, H, D), out_dtype, dev, "v out")
     _call_on(dev, "dequantize_kv_u4_pages", pp, P, page, pt, W, pl, po, B, T, H, D, k.data_ptr(),
              v.data_ptr(), code)
     return k, v
