@@ -28,8 +28,9 @@
 // heads of 128, 680 MB: 131 us, 5.2 TB/s).  One: latency, offsets, page table, codes and
 // the join in turn (4096 positions of 32 heads 12.8 us, a call of one page's positions
 // 9).  Heads of 256 with many rows: the vector unit, since the codes are unpacked again
-// for each 16 rows (149 us for 60 GFLOP; tiles of 32 rows need all registers of a wave
-// and more, and one wave a SIMD: 220).
+// for each 16 rows (141 us for 60 GFLOP; tiles of 32 rows need all registers of a wave
+// and more, and one wave a SIMD: 220; waves that share 32 rows, with weights and
+// queries in LDS, keep in step and take 151).
 #include "qg_kv4_attn.hpp"
 
 #include <algorithm>

@@ -45,8 +45,15 @@ struct Kv4Tile {
   int row0;       // the tile's first row
 };
 
+// Up to this many sequences with offsets are taken longest first.
+constexpr int kKv4Sorted = 32;
+
 // Tile `idx` among the sequences with min_rows <= n G <= max_rows, ROWS rows each.
 // All lanes of a wave call it with the same arguments; the result is uniform.
+// With offsets, workgroups differ in length and the longest should not start last: up
+// to kKv4Sorted sequences come in the order of their lengths, the last tile of each
+// first (9 of 1148 to 4001 positions, 8 heads of 256: 141 us, in the order of the call
+// 149).  More would cost a decode step's start more than it gives.
 template <int ROWS>
 __device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, const Kv4Divs& by, int64_t min_rows,
                                             int64_t max_rows, int idx) {
@@ -56,6 +63,26 @@ __device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, const Kv4Divs& by,
   }
   const int G = by.G.d;
   const int lane = threadIdx.x & 63;
+  if (s.B <= kKv4Sorted) {
+    int first = 0, n = 0, len = 0;
+    if (lane < s.B) {
+      first = min(max(s.offsets[lane], 0), s.T);
+      n = min(max(s.offsets[lane + 1], first), s.T) - first;
+      len = s.lengths[lane];
+    }
+    const int64_t rows = (int64_t)n * G;
+    const int tiles = rows >= min_rows && rows <= max_rows ? (int)((rows + ROWS - 1) / ROWS) : 0;
+    int before = 0;   // tiles of the sequences ahead of the lane's
+    for (int j = 0; j < s.B; ++j) {
+      const int l = __builtin_amdgcn_readlane(len, j), t = __builtin_amdgcn_readlane(tiles, j);
+      before += l > len || (l == len && j < lane) ? t : 0;
+    }
+    const uint64_t here = __ballot(idx >= before && idx - before < tiles);
+    if (here == 0) return {-1, 0, 0, 0};
+    const int l = __ffsll((unsigned long long)here) - 1;
+    const int tile = __builtin_amdgcn_readlane(before + tiles, l) - 1 - idx;
+    return {l, __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(n, l), tile * ROWS};
+  }
   int64_t base = 0;
   for (int b0 = 0; b0 < s.B; b0 += 64) {
     int first = 0, n = 0;
