@@ -112,10 +112,8 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   const int H = p.s.H;
   const int from = p.by_splits((int)blockIdx.x), split = blockIdx.x - from * p.splits;
   const int tile_n = p.by.H(from), h = from - tile_n * H;
-  // the rows that see most first
-  const int tile_id = p.s.offsets == nullptr ? p.tiles - 1 - tile_n : tile_n;
-  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, p.min_rows, (int64_t)1 << 40, tile_id);
-  const int64_t part = (((int64_t)tile_id * H + h) * p.splits + split) * kRows;
+  const Kv4Tile t = kv4_tile<kRows>(p.s, p.by, p.min_rows, (int64_t)1 << 40, tile_n);
+  const int64_t part = (int64_t)blockIdx.x * kRows;
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, kRows);
   const int first = max(p.s.lengths[t.b], -0x3FFFFFFF) - t.n;   // n <= 2^30: no overflow
