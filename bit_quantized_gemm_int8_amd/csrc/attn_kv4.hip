@@ -40,7 +40,7 @@ namespace qg {
 namespace {
 
 constexpr int kStep = 32;            // positions of a wave's step
-constexpr int kAttnWaves = 4;
+constexpr int kAttnWaves = 4, kAttnWavesLong = 8;   // of a workgroup
 constexpr float kLowest = -3.402823466e38f, kUnset = 1e30f;
 constexpr u32 kNibbles = 0x00F000F0u;
 
@@ -91,14 +91,14 @@ __device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile
 // ONCE: a sequence's rows are one tile, so that its cache is read once: past the
 // caches (64 requests of up to 16384 positions, 8 kv heads: 131 us against 144; where
 // many tiles read the same pages it costs 8%).
-template <int DT, int D, int RT, bool ONCE>
-__global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3 : 2) void k_kv4_attend_few(Kv4FewArgs p) {
+template <int DT, int D, int RT, bool ONCE, int NW = kAttnWaves>
+__global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3 : 2) void k_kv4_attend_few(Kv4FewArgs p) {
   constexpr int kRows = 16 * RT, kGd = kv4_groups(D), kKw = D / 32, kTd = D / 16;   // key words, channel tiles
   constexpr bool kTwice = DT == F16;   // weights in two parts
   // outputs of the waves, 16 rows and up to 128 channels at a time
   constexpr int kCols = D < 128 ? D : 128;
-  __shared__ float red[kAttnWaves][16][kCols + 4];
-  __shared__ float stat[kAttnWaves][kRows][2];
+  __shared__ float red[NW][16][kCols + 4];
+  __shared__ float stat[NW][kRows][2];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int th = p.by_splits((int)blockIdx.x), split = blockIdx.x - th * p.splits;
   const int tile_n = p.by.H(th), h = th - tile_n * p.s.H;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
     fetch_ids(u);
     load_keys(u);
     load_values(u);
-    fetch_ids(u + kAttnWaves);
+    fetch_ids(u + NW);
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
   }
 
 #pragma unroll 1
-  for (; u < u1; u += kAttnWaves) {
+  for (; u < u1; u += NW) {
     const int tile = span.tile(u), t0 = tile * kStep;
     const bool ok0 = (u32)id[0] < (u32)p.s.P, ok1 = (u32)id[1] < (u32)p.s.P;
     const bool full = ok0 && ok1 && t0 + kStep - 1 <= p0 && t0 + kStep <= capacity &&
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
         for (int e = 0; e < 2; ++e)
           zf[gd][i][e] = (((u32)vp[i][gd][2 * e] & 15u) | (((u32)vp[i][gd][2 * e + 1] & 15u) << 16)) << 4;
       }
-    load_keys(u + kAttnWaves);
+    load_keys(u + NW);
     // weights
     v8h pf[RT][kGd], pl[RT][kGd];
 #pragma unroll
@@ -432,8 +432,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
         }
       }
     }
-    load_values(u + kAttnWaves);
-    fetch_ids(u + 2 * kAttnWaves);
+    load_values(u + NW);
+    fetch_ids(u + 2 * NW);
   }
 
   // ---- join the waves: the smallest sh of each row, sums, outputs in its unit -------
@@ -450,9 +450,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
   for (int r = 0; r < RT; ++r) {
     float low = kUnset, sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kAttnWaves; ++v) low = fminf(low, stat[v][16 * r + c][0]);
+    for (int v = 0; v < NW; ++v) low = fminf(low, stat[v][16 * r + c][0]);
 #pragma unroll
-    for (int v = 0; v < kAttnWaves; ++v)
+    for (int v = 0; v < NW; ++v)
       sum += stat[v][16 * r + c][1] * __builtin_amdgcn_exp2f(low - stat[v][16 * r + c][0]);
     const float mine = __builtin_amdgcn_exp2f(low - sh[r]);
     const float inv = p.splits > 1 ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 16 * kCols / 8; i += 64 * kAttnWaves) {
+      for (int i = threadIdx.x; i < 16 * kCols / 8; i += 64 * NW) {
         const int row = i / (kCols / 8), col = 8 * (i % (kCols / 8));
         if (16 * r + row >= rows) continue;
         float x[8];
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D * RT == 64 ? 4 : D == 128 && RT 
         for (int e = 0; e < 8; ++e) {
           x[e] = red[0][row][col + e];
 #pragma unroll
-          for (int v = 1; v < kAttnWaves; ++v) x[e] += red[v][row][col + e];
+          for (int v = 1; v < NW; ++v) x[e] += red[v][row][col + e];
         }
         const int d = kCols * gd + col;
         if (p.splits > 1) {
@@ -650,20 +650,33 @@ static void join_many(const Kv4FewArgs& p, int64_t tiles, hipStream_t st) {
 }
 
 template <int DT, int D, int RT>
-static hipError_t few_t(Kv4FewArgs p, int64_t tiles, hipStream_t st) {
-  if (p.by.n > 0 && (int64_t)p.by.n * p.G <= 16 * RT)
-    k_kv4_attend_few<DT, D, RT, true><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
-  else
-    k_kv4_attend_few<DT, D, RT, false><<<(unsigned)(tiles * p.splits), 64 * kAttnWaves, 0, st>>>(p);
+static hipError_t few_t(Kv4FewArgs p, int64_t tiles, int64_t sight, hipStream_t st) {
+  const unsigned grid = (unsigned)(tiles * p.splits);
+  const bool once = p.by.n > 0 && (int64_t)p.by.n * p.G <= 16 * RT;
+  if constexpr (RT == 1 && D < 256) {
+    // With a workgroup or less on each CU and a long way to go, two waves on each SIMD
+    // (32 requests of 8 kv heads, a window of 1024 positions 13.1 us, with four waves 15.2;
+    // 16 of 4096 positions 21.0 and 24.0).  Short ways and joins lose by it (5 drafted
+    // tokens of 8 requests of 2047 positions 12.9 and 11.6), and with more workgroups two
+    // waves are there already (64 requests of up to 16384 positions 153 and 131).
+    if (grid <= 256 && sight / p.splits >= 1024) {
+      if (once) k_kv4_attend_few<DT, D, RT, true, kAttnWavesLong><<<grid, 64 * kAttnWavesLong, 0, st>>>(p);
+      else k_kv4_attend_few<DT, D, RT, false, kAttnWavesLong><<<grid, 64 * kAttnWavesLong, 0, st>>>(p);
+      if (p.splits > 1) join_t<DT, D, 16 * RT, 16>(p, tiles, st);
+      return hipGetLastError();
+    }
+  }
+  if (once) k_kv4_attend_few<DT, D, RT, true><<<grid, 64 * kAttnWaves, 0, st>>>(p);
+  else k_kv4_attend_few<DT, D, RT, false><<<grid, 64 * kAttnWaves, 0, st>>>(p);
   if (p.splits > 1) join_t<DT, D, 16 * RT, 16>(p, tiles, st);
   return hipGetLastError();
 }
 
 template <int DT>
-static hipError_t few_d(const Kv4FewArgs& p, int D, int rows, int64_t tiles, hipStream_t st) {
-  if (D == 256) return few_t<DT, 256, 1>(p, tiles, st);
-  if (rows == 16) return D == 64 ? few_t<DT, 64, 1>(p, tiles, st) : few_t<DT, 128, 1>(p, tiles, st);
-  return D == 64 ? few_t<DT, 64, 2>(p, tiles, st) : few_t<DT, 128, 2>(p, tiles, st);
+static hipError_t few_d(const Kv4FewArgs& p, int D, int rows, int64_t tiles, int64_t sight, hipStream_t st) {
+  if (D == 256) return few_t<DT, 256, 1>(p, tiles, sight, st);
+  if (rows == 16) return D == 64 ? few_t<DT, 64, 1>(p, tiles, sight, st) : few_t<DT, 128, 1>(p, tiles, sight, st);
+  return D == 64 ? few_t<DT, 64, 2>(p, tiles, sight, st) : few_t<DT, 128, 2>(p, tiles, sight, st);
 }
 
 hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st) {
@@ -698,7 +711,8 @@ hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hi
   p.by_splits = kv4_div(p.splits);
   const int64_t tiles = plan.few_tiles * s.H;
   p.part_ml = p.part_o + tiles * p.splits * plan.few_rows * a.D;
-  return dtype == F16 ? few_d<F16>(p, a.D, plan.few_rows, tiles, st) : few_d<BF16>(p, a.D, plan.few_rows, tiles, st);
+  return dtype == F16 ? few_d<F16>(p, a.D, plan.few_rows, tiles, seen, st)
+                      : few_d<BF16>(p, a.D, plan.few_rows, tiles, seen, st);
 }
 
 }  // namespace qg

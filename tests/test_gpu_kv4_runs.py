@@ -97,6 +97,11 @@ MORE = [
     (64, 32, 1, 4, "bf16", [700, 50], None, 5, 60, 3),
     (128, 32, 1, 4, "bf16", [400, 90, 300], [0, 9, 10, 18], 0, 0, 0),
     (64, 16, 2, 4, "f16", [500, 40], [0, 20, 24], 0, 0, 0),
+    # a workgroup of eight waves for each kv head
+    (128, 64, 64, 64, "f16", [2200, 1500], None, 1, 0, 0),
+    (64, 64, 256, 256, "bf16", [1100], None, 1, 0, 0),
+    (64, 128, 128, 256, "f16", [1200, 300], [0, 1, 2], 0, 0, 0),
+    (128, 32, 128, 128, "bf16", [2100, 2], None, 1, 1500, 3),
     # many splits of few tiles
     (128, 64, 1, 1, "f16", [4000], None, 130, 0, 0),
     (64, 128, 1, 2, "bf16", [5000], None, 70, 0, 0),
