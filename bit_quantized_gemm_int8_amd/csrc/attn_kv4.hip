@@ -69,9 +69,10 @@ struct Kv4FewArgs {
   float* part_ml;
 };
 
-// Workspace of a call with several splits: outputs [tile][split][row][D] and
-// (sh, sum) [tile][split][row], binary32, where tile counts row tiles times kv
-// heads; outputs and sums are in the unit of their sh.
+// Workspace of a call with several splits: outputs [tile][split][row][D] (of the prompt
+// kernel [tile][split][row / 32][D / 8][row % 32][8]) and (sh, sum) [tile][split][row],
+// binary32, where tile counts row tiles times kv heads; outputs and sums are in the
+// unit of their sh.
 
 // Steps of split `split` of a tile with `tiles` steps.
 __device__ __forceinline__ int kv4_per_split(int tiles, const Kv4Div& splits) {
@@ -515,10 +516,14 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_
   if (t.b < 0) return;
   const int rows = min(t.n * p.G - t.row0, rows_most);
   const int item = part * (256 / SUB) + (int)threadIdx.x / SUB, sub = threadIdx.x & (SUB - 1);
-  if (item >= rows * (D / 8)) return;
-  const int row = item / (D / 8), d = 8 * (item % (D / 8));
+  // neighbouring threads have neighbours of the parts
+  constexpr bool kMany = ROWS == kKv4ManyRows;
+  const int row = kMany ? item / (4 * D) * 32 + (item & 31) : item / (D / 8);
+  const int chunk = kMany ? (item >> 5) % (D / 8) : item % (D / 8), d = 8 * chunk;
+  if (row >= rows) return;   // the lanes of an item alike
   const float* const ml = p.part_ml + ((int64_t)th * p.splits * ROWS + row) * 2;
-  const float* const po = p.part_o + ((int64_t)th * p.splits * ROWS + row) * D + d;
+  const float* const po = p.part_o + (int64_t)th * p.splits * ROWS * D +
+                          (kMany ? (row >> 5) * 32 * D + 32 * d + 8 * (row & 31) : row * D + d);
   float low = kUnset, l = 0.f, x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
@@ -609,7 +614,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + (a.one ? B : std::min(B, rows / (kFewRows + 1)));
     const int64_t all = a.many_tiles * H;
     // a workgroup on each CU, of 512 positions or more (a chunk of 1500 tokens of 16 heads,
-    // a window of 2048 positions: 64 us in two parts, 81 whole)
+    // a window of 2048 positions: 59 us in two parts, 81 whole)
     a.many_splits = (int)std::max<int64_t>(1, std::min(256 / all, capacity / 512));
     a.many_part = a.many_splits > 1 ? all * a.many_splits * kKv4ManyRows * (D + 2) : 0;
   }
@@ -637,7 +642,7 @@ template <int DT, int D, int ROWS, int SUB>
 static void join_t(const Kv4FewArgs& p, int64_t tiles, hipStream_t st) {
   // workgroups of 256 / SUB items of 8 channels; without offsets the rows of a tile are known
   const int64_t rows = p.s.offsets == nullptr ? std::min<int64_t>(ROWS, (int64_t)p.by.n * p.G) : ROWS;
-  const Kv4Div parts = kv4_div((rows * (D / 8) * SUB + 255) / 256);
+  const Kv4Div parts = kv4_div(((ROWS == kKv4ManyRows ? (rows + 31) / 32 * 32 : rows) * (D / 8) * SUB + 255) / 256);
   k_kv4_attend_join<DT, D, ROWS, SUB><<<(unsigned)(tiles * parts.d), 256, 0, st>>>(p, (int)rows, parts);
 }
 

@@ -139,38 +139,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   const bool alive = 32 * wave < rows;                               // the wave has rows
   const int last_row = min(32 * wave + 31, rows - 1);
   const int wp0 = first + p.by.G(t.row0 + 32 * wave), wp1 = first + p.by.G(t.row0 + last_row);
-  v8h q[kSt];
-  float cc;
-  {
-    float x[kSt][8], top = 0.f;
-    const int64_t at = (int64_t)(t.token0 + row_token) * p.a.q_stride + (int64_t)(h * p.G + row - row_token * p.G) * D;
-#pragma unroll
-    for (int j = 0; j < kSt; ++j) {
-      const v4i a = there ? ld16((const uint16_t*)p.a.q + at + 16 * j + 8 * half) : v4i{0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const u32 u = ((u32)a[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-        x[j][e] = DT == BF16 ? bf16_bits_to_f32(u) : f16_bits_to_f32((uint16_t)u);
-        top = fmaxf(top, fabsf(x[j][e]));
-      }
-    }
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    const int e = top > 0.f && top < __builtin_inff() ? 14 - ilogbf(top) : 0;
-    constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};   // of the unpacked codes
-#pragma unroll
-    for (int j = 0; j < kSt; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[j][i] = (_Float16)ldexpf(x[j][order[i]], e);
-    cc = ldexpf(p.a.scale * 1.44269504088896f, 9 - e);
-  }
-  v16f o[kDt];
-#pragma unroll
-  for (int j = 0; j < kDt; ++j)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
-  float l = 0.f, sh = there ? kUnset : -kUnset;   // sum of the weights, exponent added to the scores
-
-  // ---- loads of later tiles ----------------------------------------------------
+  // ---- loads of tiles ------------------------------------------------------------
   // The first half of the workgroup brings the keys, the other half the values.
   // Load n of a tile: key codes of position n % 64, words 4 (n / 64) ..; value codes
   // of positions 4 (n / kC) .., word n % kC.
@@ -219,6 +188,49 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       else word[i] = ld16(word_at[i] + page + slot0 * 4);
     }
   };
+  auto tile_at = [&](int u) QG_INLINE { return span.tile(first_tile + min(u, n_tiles - 1)); };
+  // The first tile's codes come in behind the queries, while those are scaled.
+  if (n_tiles > 0) fetch_ids(tile_at(0));
+  v4i qw[kSt];
+  {
+    const int r = there ? row : t.row0, token = p.by.G(r);
+    const int64_t at = (int64_t)(t.token0 + token) * p.a.q_stride + (int64_t)(h * p.G + r - token * p.G) * D;
+#pragma unroll
+    for (int j = 0; j < kSt; ++j) qw[j] = ld16((const uint16_t*)p.a.q + at + 16 * j + 8 * half);
+  }
+  if (n_tiles > 0) {
+    fetch(tile_at(0));
+    fetch_ids(tile_at(1));
+  }
+  v8h q[kSt];
+  float cc;
+  {
+    float x[kSt][8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kSt; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const u32 u = there ? ((u32)qw[j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu : 0u;
+        x[j][e] = DT == BF16 ? bf16_bits_to_f32(u) : f16_bits_to_f32((uint16_t)u);
+        top = fmaxf(top, fabsf(x[j][e]));
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    const int e = top > 0.f && top < __builtin_inff() ? 14 - ilogbf(top) : 0;
+    constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};   // of the unpacked codes
+#pragma unroll
+    for (int j = 0; j < kSt; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[j][i] = (_Float16)ldexpf(x[j][order[i]], e);
+    cc = ldexpf(p.a.scale * 1.44269504088896f, 9 - e);
+  }
+  v16f o[kDt];
+#pragma unroll
+  for (int j = 0; j < kDt; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
+  float l = 0.f, sh = there ? kUnset : -kUnset;   // sum of the weights, exponent added to the scores
+
   // positions of a tile that some row sees, or that lie between such
   auto seen_from = [&](int tile) QG_INLINE {
     const int t0 = tile * kTile;
@@ -488,12 +500,8 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     }
   };
 
-  auto tile_at = [&](int u) QG_INLINE { return span.tile(first_tile + min(u, n_tiles - 1)); };
   if (n_tiles > 0) {
     // the first tile, and from its largest scales the common powers of two
-    fetch_ids(tile_at(0));
-    fetch(tile_at(0));
-    fetch_ids(tile_at(1));
     if (tid < 8) flags[tid] = 0;
     // the values ahead of the first tile's, which zero weights meet
     for (int i = tid; i < kTile * kC; i += NT) vbuf[(kVBufs - 1) * kTile * kC + i] = v4i{0, 0, 0, 0};
@@ -593,14 +601,15 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   if (!there) return;
   const int64_t to = ((int64_t)(t.token0 + row_token) * p.a.Hq + h * p.G + row - row_token * p.G) * D;
   const bool whole = p.splits == 1;
-  const int64_t to_part = (part + 32 * wave + c) * D;
+  // parts: [32 rows][D / 8][row][8], so that the lanes of a store are neighbours
+  const int64_t to_part = (part + 32 * wave) * D + 8 * c;
   // 8 channels of the output, or of this split's in the unit of its sh
   auto store = [&](int d, const float (&x)[8]) QG_INLINE {
     if (whole) {
       kv4_store8<DT>(p.a.out, to + d, x);
     } else {
-      *(v4f*)(p.part_o + to_part + d) = v4f{x[0], x[1], x[2], x[3]};
-      *(v4f*)(p.part_o + to_part + d + 4) = v4f{x[4], x[5], x[6], x[7]};
+      *(v4f*)(p.part_o + to_part + 32 * d) = v4f{x[0], x[1], x[2], x[3]};
+      *(v4f*)(p.part_o + to_part + 32 * d + 4) = v4f{x[4], x[5], x[6], x[7]};
     }
   };
   if (!whole && half == 0) *(v2f*)(p.part_ml + (part + 32 * wave + c) * 2) = v2f{sh, l};
