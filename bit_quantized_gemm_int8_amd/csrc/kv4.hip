@@ -313,18 +313,21 @@ static void kv4_split(int64_t items, int& threads, int& parts) {
 // Four rows a workgroup where there are enough workgroups to fill the GPU several
 // times over: their value codes and group words are then 16 bytes side by side.  One
 // row against four: 65536 rows read back 107 us and 68, 4096 rows of 96 heads appended
-// and read back 66 and 62; 500 rows read back 3.1 and 3.5, 16 rows appended and read
-// back 6 and 15, where four rows are of four sequences and come after one another.
-static bool kv4_quads(int T, int parts) { return (int64_t)T * parts >= 4096; }
+// and read back 66 and 62; 500 rows read back 3.1 and 3.5.  Not where sequences are
+// known to have fewer rows than four, which would come after one another (one token of
+// 4096 sequences, 48 heads, appended: 23.4 us and 29.2).
+static bool kv4_quads(const Kv4Seqs& s, int parts) {
+  return (int64_t)s.T * parts >= 4096 && (s.offsets != nullptr || s.T / s.B >= kQuad);
+}
 
 template <int DT, int D>
 static hipError_t kv4_append_t(const Kv4Seqs& s, const Kv4Append& a, hipStream_t st) {
   int threads, parts;
   kv4_split((int64_t)(a.Hq + 2 * s.H) * (D / 16), threads, parts);
-  if (kv4_quads(s.T, parts))
+  if (kv4_quads(s, parts))
     k_kv4_append<DT, D, kQuad><<<(unsigned)(((int64_t)s.T + kQuad - 1) / kQuad * parts), threads, 0, st>>>(s, a, parts);
   else
-    k_kv4_append<DT, D, 1><<<(unsigned)(s.T * parts), threads, 0, st>>>(s, a, parts);
+    k_kv4_append<DT, D, 1><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, a, parts);
   return hipGetLastError();
 }
 
@@ -349,10 +352,10 @@ template <int DT, int D>
 static hipError_t kv4_dequant_t(const Kv4Seqs& s, void* k, void* v, hipStream_t st) {
   int threads, parts;
   kv4_split((int64_t)2 * s.H * (D / 8), threads, parts);
-  if (kv4_quads(s.T, parts))
+  if (kv4_quads(s, parts))
     k_kv4_dequant<DT, D, kQuad><<<(unsigned)(((int64_t)s.T + kQuad - 1) / kQuad * parts), threads, 0, st>>>(s, k, v, parts);
   else
-    k_kv4_dequant<DT, D, 1><<<(unsigned)(s.T * parts), threads, 0, st>>>(s, k, v, parts);
+    k_kv4_dequant<DT, D, 1><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, k, v, parts);
   return hipGetLastError();
 }
 
