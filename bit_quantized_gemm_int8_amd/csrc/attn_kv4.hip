@@ -531,7 +531,9 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_
     const v2f two = *(const v2f*)(ml + (int64_t)v * ROWS * 2);
     const v4f a = *(const v4f*)(po + (int64_t)v * ROWS * D), b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
     const float sh = two[0], sum = two[1];
-    if (sh == kUnset) continue;   // no steps, or nothing in the row's sight: no outputs there
+    // no steps, or nothing in the row's sight: no outputs there.  Scores that are all NaN
+    // leave sh unset too, and their sum NaN.
+    if (sh == kUnset && sum == 0.f) continue;
     const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
     low = to;
     l = l * f + sum * f1;

@@ -746,7 +746,8 @@ qg_status_t dequantize_kv_u4_pages(const int32_t* pages, int64_t P, int64_t page
  *   page; with window > 0 only those with j > p - window or j < sinks.
  *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j), over the visible
  *   j, for query head h with kv head h / (Hq / H); a row that sees nothing is
- *   zeros.  What lies in positions out of sight has no influence, NaN included.
+ *   zeros, and one that sees something with a NaN in its query is NaN.  What lies in
+ *   positions out of sight has no influence, NaN included.
  * q: [T][Hq][D] of dtype QG_F16 or QG_BF16, tokens q_stride elements apart (as
  * in append_kv_u4_pages), read; H divides Hq; T * Hq <= 2^30; scale is finite.
  * out: [T][Hq][D] of dtype, 16-byte aligned, written.

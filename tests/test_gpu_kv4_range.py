@@ -1,0 +1,101 @@
+"""Attention over the 4-bit paged cache where positions are of very different kinds: groups
+that are not finite in splits of their own, values and keys of far magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_gemm_int8_amd as qg
+import oracle.kv4 as kv4
+from tests.gpu_util import DEV, out_f64
+from tests.kv4_util import attend_case
+from tests.test_gpu_kv4 import DT, dev
+from tests.test_gpu_kv4_runs import i32
+
+pytestmark = pytest.mark.gpu
+
+
+def cache(k, v, page, W=None):
+    """Pages and page table of one sequence with keys and values f32 [L, H, D]."""
+    L, H, D = k.shape
+    P = -(-L // page)
+    pages = np.zeros((P, H, kv4.page_words(page, D)), np.uint32)
+    table = np.full((1, W or P), -1, np.int32)
+    table[0, :P] = np.random.default_rng(P).permutation(P)
+    kv4.append(pages, page, [(0, i) for i in range(L)], table, k, v)
+    return pages, table
+
+
+def attend(q, pages, table, length, fmt, page, window=0, sinks=0):
+    """(outputs in binary64, the oracle's, the bound on the error ahead of the output's rounding)."""
+    n, Hq, D = q.shape
+    q = torch.from_numpy(q).to(DT[fmt])
+    print(f"attend {D} {n} {Hq} {fmt} {length}", flush=True)
+    got = qg.attend_kv_u4_pages(q.to(DEV), dev(pages), dev(table), i32([length]), window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    want, bound, _ = attend_case(pages, table, [length], page, D, q.double().numpy(), n, window=window, sinks=sinks)
+    return out_f64(got), want, bound
+
+
+def close(got, want, bound, fmt):
+    """The output's rounding on top of the bound; whatever is finite in 64 bits is finite."""
+    fin = torch.finfo(DT[fmt])
+    off = np.abs(got - want) - (fin.eps / 2 * (np.abs(want) + bound) + bound + fin.smallest_normal * fin.eps)
+    assert (off <= 0).all(), (off.max(), np.unravel_index(np.nanargmax(off), off.shape))
+
+
+# ---- groups that are not finite, by themselves in a split of the positions -----------
+# splits of 8 steps of 32 positions for few rows, of 5 to 8 tiles of 64 for many
+
+NAN_AT = [
+    # D, tokens, positions, page table in positions, not finite from .. to
+    (64, 1, 1793, 2048, 1792, 1793),      # the newest position, the only one of its split
+    (128, 1, 1793, 2048, 1792, 1793),
+    (256, 1, 1793, 2048, 1792, 1793),
+    (128, 1, 257, 768, 256, 257),
+    (128, 1, 1793, 2048, 1536, 1792),     # a whole split
+    (64, 2, 1800, 2048, 0, 256),          # the first one
+    (256, 3, 1793, 2048, 256, 512),
+    (128, 200, 1540, 2048, 1344, 1345),   # the first position of a split, which some rows see alone there
+    (64, 200, 1540, 2048, 1344, 1345),
+    (128, 150, 2000, 2048, 1536, 2000),
+    (64, 150, 2000, 2048, 0, 512),
+]
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("case", NAN_AT, ids=range(len(NAN_AT)))
+def test_not_finite_in_a_split(case, fmt):
+    D, n, L, capacity, lo, hi = case
+    page = 64
+    rng = np.random.default_rng(L + lo)
+    x = rng.standard_normal((2, L, 1, D)).astype(np.float32)
+    x[0, lo:hi, 0, 5] = np.inf                       # keys; the whole group is NaN with it
+    if D == 256:
+        x[0, lo:hi, 0, 200] = np.nan
+    pages, table = cache(x[0], x[1], page, capacity // page)
+    q = rng.standard_normal((n, 1, D)).astype(np.float32)
+    assert qg.attend_kv_u4_pages_workspace_bytes(n, 1, 1, 1, D, page, table.shape[1]) > 0      # there are splits
+    got, want, bound = attend(q, pages, table, L, fmt, page)
+    sees = L - n + np.arange(n) >= lo
+    assert np.isnan(got[sees]).all()
+    if not sees.all():
+        pages, table = cache(np.where(np.isfinite(x[0]), x[0], 0), x[1], page, capacity // page)
+        want, bound, _ = attend_case(pages, table, [L], page, D, torch.from_numpy(q).to(DT[fmt]).double().numpy(), n)
+        close(got[~sees], want[~sees], bound[~sees], fmt)
+
+
+@pytest.mark.parametrize("D,n,L", [(64, 2, 1793), (128, 2, 1793), (256, 2, 1793), (64, 150, 2000), (128, 150, 2000), (128, 3, 200), (128, 150, 200)])
+def test_query_that_is_nan(D, n, L):
+    """Its row is NaN, split or not; the other rows are as without it."""
+    page = 64
+    rng = np.random.default_rng(D + n)
+    x = rng.standard_normal((2, L, 1, D)).astype(np.float32)
+    pages, table = cache(x[0], x[1], page, -(-L // page) + 1)
+    q = rng.standard_normal((n, 2, D)).astype(np.float32)
+    q[n - 2, 1, 7] = np.nan
+    q[0, 0] = np.nan
+    got, _, _ = attend(q, pages, table, L, "f16", page)
+    bad = np.isnan(q).any(-1)
+    assert np.isnan(got[bad]).all()
+    want, bound, _ = attend_case(pages, table, [L], page, D, torch.from_numpy(np.where(np.isnan(q), 0, q)).half().double().numpy(), n)
+    close(got[~bad], want[~bad], bound[~bad], "f16")
