@@ -21,8 +21,10 @@
 // neighbouring positions in each half of the step, are the operand that the second
 // product needs, with the positions in that order.  Value codes of 4 positions of a
 // word are neighbours in the cache for the same reason.  No lane exchange per
-// step: the weights are exp2(x + sh) for an sh of the row that falls only where a
-// weight passes 2^13, outputs and sum with it.
+// step: the softmax's weights are exp2(x + sh) for an sh of the row that falls only where
+// they pass 2^9, outputs and sum with it.  The outputs' weights p s are in a power of two
+// of their own for each row and value group, so that neither the sum nor the other group
+// loses bits to scales far from those before them.
 //
 // What bounds it.  Many sequences: memory (64 requests of up to 16384 positions, 8 kv
 // heads of 128, 680 MB: 131 us, 5.2 TB/s).  One: latency, offsets, page table, codes and
@@ -244,36 +246,19 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
 
   // outputs: rows = channels, columns = query rows; sums of the zero points
   v4f o[RT][kTd], oz[RT][kGd];
-  float l[RT], sh[RT];
+  // l: sum of exp2(x + sh); outputs: sums of exp2(x + sh) s unit
+  float l[RT], sh[RT], unit[RT][kGd];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
 #pragma unroll
     for (int j = 0; j < kTd; ++j) o[r][j] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int gd = 0; gd < kGd; ++gd) oz[r][gd] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int gd = 0; gd < kGd; ++gd) {
+      oz[r][gd] = v4f{0.f, 0.f, 0.f, 0.f};
+      unit[r][gd] = 1.f;
+    }
     l[r] = 0.f;
     sh[r] = kUnset;
-  }
-  // A power of two near the values' scales, from what some row sees of the wave's
-  // first step: the weights p s are taken relative to it.
-  float unit[kGd];
-#pragma unroll
-  for (int gd = 0; gd < kGd; ++gd) {
-    float top = 0x1p-126f;
-    if (n_steps > 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = kv4_scale((u32)vp[i][gd][e]);
-          const int j = span.tile(min(u, u1 - 1)) * kStep + 16 * i + 4 * g + e;
-          const bool some = ((u32)id[i] < (u32)p.s.P) & (j <= p1) & (j < capacity) & ((window <= 0) | (j > p0 - window) | (j < sinks));
-          top = some && v < __builtin_inff() ? fmaxf(top, v) : top;
-        }
-    }
-    top = max16(top);
-    const u32 ex = (u32)min(max((int)(__builtin_amdgcn_readfirstlane(__float_as_uint(top)) >> 23), 27), 227);
-    unit[gd] = __uint_as_float((254u - ex) << 23);   // 2^-floor(log2 top)
   }
 
 #pragma unroll 1
@@ -310,14 +295,14 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
           }
         }
     }
-    float sv[kGd][2][4];
+    float vs[kGd][2][4];
     u32 zf[kGd][2][2];
 #pragma unroll
     for (int gd = 0; gd < kGd; ++gd)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sv[gd][i][e] = kv4_scale((u32)vp[i][gd][e]) * unit[gd];
+        for (int e = 0; e < 4; ++e) vs[gd][i][e] = kv4_scale((u32)vp[i][gd][e]);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           zf[gd][i][e] = (((u32)vp[i][gd][2 * e] & 15u) | (((u32)vp[i][gd][2 * e + 1] & 15u) << 16)) << 4;
@@ -331,6 +316,13 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[r][i][e] *= cc[r];
+      float sv[kGd][2][4], most = 0.f;   // the scales in the row's units
+#pragma unroll
+      for (int gd = 0; gd < kGd; ++gd)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[gd][i][e] = vs[gd][i][e] * unit[r][gd];
       if (!full) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -339,12 +331,20 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
             const int j = t0 + 16 * i + 4 * g + e;
             const bool seen = (i ? ok1 : ok0) & (j <= pos[r]) & (j < capacity) & ((window <= 0) | (j > pos[r] - window) | (j < sinks));
             y[r][i][e] = seen ? y[r][i][e] : -__builtin_inff();
+#pragma unroll
+            for (int gd = 0; gd < kGd; ++gd) sv[gd][i][e] = seen ? sv[gd][i][e] : 0.f;   // whatever lies out of sight
           }
       }
+#pragma unroll
+      for (int gd = 0; gd < kGd; ++gd)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) most = fmaxf(most, sv[gd][i][e]);
       float w[kGd][2][4];
 #pragma unroll 1
       for (int round = 0; round < 2; ++round) {   // the second round's weights pass
-        float sum = 0.f, most = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -352,39 +352,57 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
             const float x = __builtin_amdgcn_exp2f(y[r][i][e] + sh[r]);
             sum += x;
 #pragma unroll
-            for (int gd = 0; gd < kGd; ++gd) {
-              // nothing out of sight, whatever its scale
-              w[gd][i][e] = y[r][i][e] == -__builtin_inff() ? 0.f : x * sv[gd][i][e];
-              most = fmaxf(most, w[gd][i][e]);
-            }
+            for (int gd = 0; gd < kGd; ++gd) w[gd][i][e] = x * sv[gd][i][e];
           }
-        if (round > 0 || !__any(most > 0x1p13f || sum > 0x1p70f)) {   // a NaN stays one
+        // binary16 holds 2^9 2^6; a NaN stays one
+        if (round > 0 || !__any(most > 0x1p6f || sum > 0x1p9f)) {
           l[r] += sum;
           break;
         }
-        // The row's sh to where its largest weight is near 1, and no exponential past 2^64.
+        // The row's sh to where its largest exponential is near 1, by more than rounding
+        // takes from a score, and each unit to where the group's largest weight is.  Neither
+        // the sum nor the outputs ever grow by it.
         float top = kLowest;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = sv[0][i][e];
-#pragma unroll
-            for (int gd = 1; gd < kGd; ++gd) v = fmaxf(v, sv[gd][i][e]);
-            const float yy = y[r][i][e];
-            top = fmaxf(top, fmaxf(yy == -__builtin_inff() ? yy : yy + __builtin_amdgcn_logf(v), yy - 64.f));
-          }
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, y[r][i][e]);
         top = max16(top);
-        const float to = -floorf(top) - fabsf(top) * 0x1p-21f;   // by more than rounding takes
-        const float by = to < sh[r] ? __builtin_amdgcn_exp2f(to - sh[r]) : 1.f;   // 0 for a row's first weights
-        sh[r] = fminf(sh[r], to);
-        l[r] *= by;
+        const float was = sh[r];
+        sh[r] = fminf(was, -floorf(top) - fabsf(top) * 0x1p-21f);
+        l[r] *= __builtin_amdgcn_exp2f(sh[r] - was);   // 0 for a row's first weights
 #pragma unroll
-        for (int j = 0; j < kTd; ++j)
+        for (int gd = 0; gd < kGd; ++gd) {
+          float most_w = kLowest;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[r][j][e] *= by;
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int gd = 0; gd < kGd; ++gd) oz[r][gd][0] *= by;
+            for (int e = 0; e < 4; ++e) {
+              const float yy = y[r][i][e];
+              if (yy > -__builtin_inff()) most_w = fmaxf(most_w, yy + __builtin_amdgcn_logf(vs[gd][i][e]));
+            }
+          most_w = max16(most_w);
+          const float had = (float)((int)(__float_as_uint(unit[r][gd]) >> 23) - 127);
+          const float to = floorf(fminf(-floorf(most_w) - fabsf(most_w) * 0x1p-21f - sh[r], had + (was - sh[r])));
+          // of scales up to 2^124.1, and exponentials up to 2^9, at least 2^-126 will do
+          const float now = fminf(fmaxf(to, -126.f), 126.f);
+          const float by = __builtin_amdgcn_exp2f((sh[r] - was) + (now - had));
+          unit[r][gd] = ldexpf(1.f, (int)now);
+          constexpr int kPer = kTd / kGd;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][gd * kPer + j][e] *= by;
+          oz[r][gd][0] *= by;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // no infinity, which an exponential of zero would make a NaN
+              const float v = vs[gd][i][e] * unit[r][gd];
+              sv[gd][i][e] = y[r][i][e] == -__builtin_inff() ? 0.f : v > 0x1p100f ? 0x1p100f : v;
+            }
+        }
       }
 #pragma unroll
       for (int gd = 0; gd < kGd; ++gd) {
@@ -459,7 +477,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
     const float inv = p.splits > 1 ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
     for (int gd = 0; gd < kGd; ++gd) {
-      const float f = mine * inv / unit[gd];   // unit: a power of two
+      const float f = mine * inv, back = 1.f / unit[r][gd];   // unit: a power of two
       constexpr int kPer = kTd / kGd;
       if (r || gd) __syncthreads();
 #pragma unroll
@@ -472,7 +490,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
           v4f x;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            x[k] = (o[r][gd * kPer + j + k][e] - oz[r][gd][0]) * (f * 0x1p20f);
+            x[k] = (o[r][gd * kPer + j + k][e] - oz[r][gd][0]) * 0x1p20f * f * back;
           *(v4f*)(to + j) = x;
         }
       }

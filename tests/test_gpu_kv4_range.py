@@ -99,3 +99,73 @@ def test_query_that_is_nan(D, n, L):
     assert np.isnan(got[bad]).all()
     want, bound, _ = attend_case(pages, table, [L], page, D, torch.from_numpy(np.where(np.isnan(q), 0, q)).half().double().numpy(), n)
     close(got[~bad], want[~bad], bound[~bad], "f16")
+
+
+# ---- values of which the first positions say nothing ----------------------------------
+
+def history(D, L, H, rng, first, factors_first, factors_then):
+    """Values f32 [L, H, D], each group of channels by its own factor up to position `first` and from there on."""
+    v = rng.standard_normal((L, H, D))
+    w = kv4.group_width(D)
+    for t, f in ((slice(None, first), factors_first), (slice(first, None), factors_then)):
+        for g in range(D // w):
+            v[t, :, g * w:(g + 1) * w] *= f[g % len(f)]
+    return v.astype(np.float32)
+
+
+def lifted(L, D, H, rng, first, lift):
+    """Keys, those from `first` on larger by `lift` in the first channel."""
+    k = rng.standard_normal((L, H, D)).astype(np.float32)
+    k[first:, :, 0] += lift
+    return k
+
+
+@pytest.mark.parametrize("first", [40, 256, 330])
+@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (128, 40), (256, 40)])
+@pytest.mark.parametrize("e0,e1", [(None, 0), (None, 28), (None, 40), (None, 110), (-100, 100), (-60, 30), (-110, 0), (100, -100), (0, -40)])
+def test_values_that_grow(D, n, first, e0, e1):
+    """Zeros, or far smaller (or larger) values, and then others, the later ones with as much weight or far more."""
+    L, page, H = 700, 32, 1
+    rng = np.random.default_rng(D + n + first)
+    v = history(D, L, H, rng, first, [0.0 if e0 is None else 2.0 ** e0], [2.0 ** e1])
+    for lift in (0.0, 30.0):
+        pages, table = cache(lifted(L, D, H, rng, first, lift), v, page)
+        q = rng.standard_normal((n, 2, D)).astype(np.float32)
+        q[:, :, 0] = 10.0
+        close(*attend(q, pages, table, L, "bf16", page), "bf16")
+
+
+def test_values_that_grow_eight_waves():
+    D, L, page, H = 64, 1100, 64, 256
+    rng = np.random.default_rng(1)
+    for first, f0, f1 in ((256, 0.0, 2.0 ** 40), (300, 2.0 ** -90, 2.0 ** 60)):
+        pages, table = cache(rng.standard_normal((L, H, D)).astype(np.float32), history(D, L, H, rng, first, [f0], [f1]), page)
+        close(*attend(rng.standard_normal((1, H, D)).astype(np.float32), pages, table, L, "bf16", page), "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("first", [40, 128, 330])
+@pytest.mark.parametrize("f0,f1", [((1, 0), (1, 1)), ((0, 1), (1, 1)), ((1, 2.0 ** -20), (1, 1)), ((1, 1), (1, 2.0 ** 14)), ((2.0 ** -14, 1), (1, 1)),
+                                   ((1, 1), (2.0 ** -20, 1)), ((1, 1), (1, 2.0 ** -14)), ((1, 0), (0, 1))])
+def test_halves_of_wide_heads(fmt, first, f0, f1):
+    """Heads of 256: what one half of the channels holds leaves the other half's outputs alone."""
+    D, L, page, H = 256, 600, 32, 1
+    rng = np.random.default_rng(first)
+    v = history(D, L, H, rng, first, f0, f1)
+    for lift in (0.0, 30.0, -30.0):
+        pages, table = cache(lifted(L, D, H, rng, first, lift), v, page)
+        for n in (1, 30):
+            q = rng.standard_normal((n, 2, D)).astype(np.float32)
+            q[:, :, 0] = 10.0
+            close(*attend(q, pages, table, L, fmt, page), fmt)
+
+
+def test_halves_of_wide_heads_far_apart():
+    D, L, page, H = 256, 600, 32, 1
+    rng = np.random.default_rng(7)
+    for f0, f1 in (((1, 2.0 ** -30), (1, 2.0 ** 30)), ((2.0 ** 100, 2.0 ** -100), (2.0 ** -100, 2.0 ** 100))):
+        v = history(D, L, H, rng, 140, f0, f1)
+        pages, table = cache(lifted(L, D, H, rng, 140, 8.0), v, page)
+        q = rng.standard_normal((5, 2, D)).astype(np.float32)
+        q[:, :, 0] = 10.0
+        close(*attend(q, pages, table, L, "bf16", page), "bf16")
