@@ -47,6 +47,9 @@ constexpr int kManyWaves = kKv4ManyRows / 32;
 constexpr int kVBufs = 3;      // tiles of values at hand (two of keys)
 constexpr float kLow = -3.402823466e38f;
 constexpr float kUnset = 1e30f;
+// A sum outside of these in the exponent of the outputs keeps its own; within, an
+// exponential is zero below 2^-86 of the largest.
+constexpr float kApartLow = 0x1p-40f, kApartHigh = 0x1p60f;
 constexpr u32 kHidden = 0xFFFFFFFFu;   // group word of a position that no row sees
 
 __device__ __forceinline__ int float_exp(u32 bits) { return (int)((bits >> 23) & 255u) - 127; }
@@ -229,7 +232,10 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   for (int j = 0; j < kDt; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
-  float l = 0.f, sh = there ? kUnset : -kUnset;   // sum of the weights, exponent added to the scores
+  // Exponents added to the scores, for the outputs' weights and for their sum l.  They are
+  // one but where value scales have moved the outputs' so far that l leaves kApartLow .. kApartHigh in it.
+  float l = 0.f, sh = there ? kUnset : -kUnset, shl = sh;
+  bool apart = false;   // some row's differ: the wave's tiles take the general form
 
   // positions of a tile that some row sees, or that lie between such
   auto seen_from = [&](int tile) QG_INLINE {
@@ -401,14 +407,14 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   // ---- scores of a tile to weights -------------------------------------------------
   // With x the scores in base 2 and e the exponents of the values' powers of two, the
   // weights are exp2(x + e - ev + sh) for one sh of a row, which falls where their sum
-  // would pass 2^14, outputs and sum with it:  out = 2^(9 + ev) o / l.
+  // would pass 2^14, outputs with it, and l the sum of exp2(x + shl):
+  // out = 2^(9 + ev + shl - sh) o / l.
   int ek = 0, ev = 0;   // exponents of the common powers of two
   float ct = 0.f;
-  // The row's sh down to `to`, where that is below it.
+  // The row's sh down to `to`, where that is below it, and the outputs with it.
   auto lower = [&](float to) QG_INLINE {
     const float by = to < sh ? __builtin_amdgcn_exp2f(to - sh) : 1.f;   // 0 for a row's first tile
     sh = fminf(sh, to);
-    l *= by;
 #pragma unroll
     for (int j = 0; j < kDt; ++j)
 #pragma unroll
@@ -446,7 +452,12 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       float top = kLow;
 #pragma unroll
       for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15]);
-      if (__any(top + sh > 60.f)) lower(60.f - both(top));
+      if (__any(top + shl > 60.f)) {
+        const float was = shl;
+        top = both(top);
+        shl = fminf(was, -floorf(top) - fabsf(top) * 0x1p-21f);
+        l *= __builtin_amdgcn_exp2f(shl - was);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -455,7 +466,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int e = 4 * a + b;
-            l += __builtin_amdgcn_exp2f(s[i][e] + sh);
+            l += __builtin_amdgcn_exp2f(s[i][e] + shl);
             s[i][e] = s[i][e] == -__builtin_inff() ? s[i][e] : s[i][e] + f[b];   // whatever lies out of sight
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -496,7 +507,20 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
 #pragma unroll
       for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e >> 4][e & 15] * by);
       top = both(top);
+      const float was = sh;
       lower(-floorf(top) - fabsf(top) * 0x1p-21f);
+      if (!odd) {
+        l *= __builtin_amdgcn_exp2f(sh - was);
+        shl = sh;
+      }
+    }
+    if (odd && __any(shl != sh)) {
+      const float other = l * __builtin_amdgcn_exp2f(sh - shl), most = both(other);
+      apart = __any(((most < kApartLow) | (most > kApartHigh)) & (both(l) > 0.f));
+      if (!apart) {
+        l = other;
+        shl = sh;
+      }
     }
   };
 
@@ -577,7 +601,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       const bool all = t0 >= all0 && t0 <= all1;
       if (t0 <= act1 && (t0 >= act0 || t0 < sinks0)) {
         // first positions that stay visible take the general form
-        weights(now, u, all, is_odd || (!all && t0 < sinks0));
+        weights(now, u, all, is_odd || apart || (!all && t0 < sinks0));
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) pf[i >> 1][i & 1] = v8h{};
@@ -612,9 +636,12 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
       *(v4f*)(p.part_o + to_part + 32 * d + 4) = v4f{x[4], x[5], x[6], x[7]};
     }
   };
-  if (!whole && half == 0) *(v2f*)(p.part_ml + (part + 32 * wave + c) * 2) = v2f{sh, l};
+  if (!whole && half == 0) *(v2f*)(p.part_ml + (part + 32 * wave + c) * 2) = v2f{shl, l};
   const float inv = !whole ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
-  const float f = ldexpf(inv, 9 + ev);
+  // 2^(9 + ev) in the unit of l; the whole powers behind the rest, which may not hold them
+  const float gap = shl - sh, more = fmaxf(floorf(gap), -1000.f);
+  const float f = inv * __builtin_amdgcn_exp2f(gap - more);
+  const int up = 9 + ev + (int)more;
   if constexpr (D == 64) {
     // place 32 j + 8 a + 4 half + b holds channel 8 (place % 8) + place / 8
 #pragma unroll
@@ -623,7 +650,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int a = 0; a < 4; ++a) x[4 * j + a] = o[j][4 * a + b] * f;
+        for (int a = 0; a < 4; ++a) x[4 * j + a] = ldexpf(o[j][4 * a + b] * f, up);
       store(32 * half + 8 * b, x);
     }
   } else {
@@ -635,8 +662,8 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
         float x[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[2 * j] = o[j][4 * a + b] * f;
-          x[2 * j + 1] = o[j][4 * (a + 2) + b] * f;
+          x[2 * j] = ldexpf(o[j][4 * a + b] * f, up);
+          x[2 * j + 1] = ldexpf(o[j][4 * (a + 2) + b] * f, up);
         }
         store(64 * a + 32 * half + 8 * b, x);
       }

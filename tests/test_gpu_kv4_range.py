@@ -121,7 +121,7 @@ def lifted(L, D, H, rng, first, lift):
 
 
 @pytest.mark.parametrize("first", [40, 256, 330])
-@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (128, 40), (256, 40)])
+@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (128, 40), (256, 40), (64, 150), (128, 150)])
 @pytest.mark.parametrize("e0,e1", [(None, 0), (None, 28), (None, 40), (None, 110), (-100, 100), (-60, 30), (-110, 0), (100, -100), (0, -40)])
 def test_values_that_grow(D, n, first, e0, e1):
     """Zeros, or far smaller (or larger) values, and then others, the later ones with as much weight or far more."""
@@ -130,6 +130,19 @@ def test_values_that_grow(D, n, first, e0, e1):
     v = history(D, L, H, rng, first, [0.0 if e0 is None else 2.0 ** e0], [2.0 ** e1])
     for lift in (0.0, 30.0):
         pages, table = cache(lifted(L, D, H, rng, first, lift), v, page)
+        q = rng.standard_normal((n, 2, D)).astype(np.float32)
+        q[:, :, 0] = 10.0
+        close(*attend(q, pages, table, L, "bf16", page), "bf16")
+
+
+@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (64, 150), (128, 150)])
+@pytest.mark.parametrize("e0,e1", [(60, -60), (100, 0), (20, -100)])
+def test_values_that_shrink_under_higher_scores(D, n, e0, e1):
+    """The later positions have the weight, by some 70 to 110 bits, and the first ones the values."""
+    L, page = 700, 32
+    rng = np.random.default_rng(D + n)
+    for first in (40, 330):
+        pages, table = cache(lifted(L, D, 1, rng, first, 50.0 if D == 64 else 60.0), history(D, L, 1, rng, first, [2.0 ** e0], [2.0 ** e1]), page)
         q = rng.standard_normal((n, 2, D)).astype(np.float32)
         q[:, :, 0] = 10.0
         close(*attend(q, pages, table, L, "bf16", page), "bf16")
