@@ -73,8 +73,8 @@ struct Kv4FewArgs {
 
 // Workspace of a call with several splits: outputs [tile][split][row][D] (of the prompt
 // kernel [tile][split][row / 32][D / 8][row % 32][8]) and (sh, sum) [tile][split][row],
-// binary32, where tile counts row tiles times kv heads; outputs and sums are in the
-// unit of their sh.
+// binary32, where tile counts row tiles times kv heads; a split's outputs are over its
+// own sum, so that they are in range wherever its values are.
 
 // Steps of split `split` of a tile with `tiles` steps.
 __device__ __forceinline__ int kv4_per_split(int tiles, const Kv4Div& splits) {
@@ -474,7 +474,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
     for (int v = 0; v < NW; ++v)
       sum += stat[v][16 * r + c][1] * __builtin_amdgcn_exp2f(low - stat[v][16 * r + c][0]);
     const float mine = __builtin_amdgcn_exp2f(low - sh[r]);
-    const float inv = p.splits > 1 ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
     for (int gd = 0; gd < kGd; ++gd) {
       const float f = mine * inv, back = 1.f / unit[r][gd];   // unit: a power of two
@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
   }
 }
 
-// Join the splits of a tile, each in the unit of its sh.  SUB lanes take the splits
+// Join the splits of a tile, by their shares in the sum.  SUB lanes take the splits
 // of 8 channels of a row in turn, so that their loads are under way together.
 template <int DT, int D, int ROWS, int SUB>
 __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_most, Kv4Div parts) {
@@ -542,38 +542,46 @@ __global__ __launch_bounds__(256) void k_kv4_attend_join(Kv4FewArgs p, int rows_
   const float* const ml = p.part_ml + ((int64_t)th * p.splits * ROWS + row) * 2;
   const float* const po = p.part_o + (int64_t)th * p.splits * ROWS * D +
                           (kMany ? (row >> 5) * 32 * D + 32 * d + 8 * (row & 31) : row * D + d);
+  const auto outputs = [&](int v, v4f& a, v4f& b) QG_INLINE {
+    a = *(const v4f*)(po + (int64_t)v * ROWS * D);
+    b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
+  };
+  v4f a, b;   // of the lane's first split, under way while the sums are joined
+  outputs(min(sub, p.splits - 1), a, b);
   float low = kUnset, l = 0.f, x[8];
+  for (int v = sub; v < p.splits; v += SUB) {
+    const v2f two = *(const v2f*)(ml + (int64_t)v * ROWS * 2);
+    const float to = fminf(low, two[0]);
+    l = l * __builtin_amdgcn_exp2f(to - low) + two[1] * __builtin_amdgcn_exp2f(to - two[0]);
+    low = to;
+  }
+#pragma unroll
+  for (int o = 1; o < SUB; o <<= 1) {
+    const float sh = __shfl_xor(low, o, kWave), sum = __shfl_xor(l, o, kWave), to = fminf(low, sh);
+    l = l * __builtin_amdgcn_exp2f(to - low) + sum * __builtin_amdgcn_exp2f(to - sh);
+    low = to;
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
   for (int v = sub; v < p.splits; v += SUB) {
     const v2f two = *(const v2f*)(ml + (int64_t)v * ROWS * 2);
-    const v4f a = *(const v4f*)(po + (int64_t)v * ROWS * D), b = *(const v4f*)(po + (int64_t)v * ROWS * D + 4);
-    const float sh = two[0], sum = two[1];
+    if (v != sub) outputs(v, a, b);
     // no steps, or nothing in the row's sight: no outputs there.  Scores that are all NaN
     // leave sh unset too, and their sum NaN.
-    if (sh == kUnset && sum == 0.f) continue;
-    const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
-    low = to;
-    l = l * f + sum * f1;
+    if (two[0] == kUnset && two[1] == 0.f) continue;
+    const float f = two[1] * __builtin_amdgcn_exp2f(low - two[0]) * inv;   // 1 at most
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = x[e] * f + a[e] * f1;
-      x[4 + e] = x[4 + e] * f + b[e] * f1;
+      x[e] += a[e] * f;
+      x[4 + e] += b[e] * f;
     }
   }
 #pragma unroll
-  for (int o = 1; o < SUB; o <<= 1) {
-    const float sh = __shfl_xor(low, o, kWave), sum = __shfl_xor(l, o, kWave);
-    const float to = fminf(low, sh), f = __builtin_amdgcn_exp2f(to - low), f1 = __builtin_amdgcn_exp2f(to - sh);
-    low = to;
-    l = l * f + sum * f1;
+  for (int o = 1; o < SUB; o <<= 1)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * f + __shfl_xor(x[e], o, kWave) * f1;
-  }
+    for (int e = 0; e < 8; ++e) x[e] += __shfl_xor(x[e], o, kWave);
   if (sub != 0) return;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= inv;
   const int qr = t.row0 + row, token = p.by.G(qr);
   kv4_store8<DT>(p.a.out, ((int64_t)(t.token0 + token) * p.a.Hq + h * p.G + qr - token * p.G) * D + d, x);
 }

@@ -627,7 +627,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
   const bool whole = p.splits == 1;
   // parts: [32 rows][D / 8][row][8], so that the lanes of a store are neighbours
   const int64_t to_part = (part + 32 * wave) * D + 8 * c;
-  // 8 channels of the output, or of this split's in the unit of its sh
+  // 8 channels of the output, or of this split's
   auto store = [&](int d, const float (&x)[8]) QG_INLINE {
     if (whole) {
       kv4_store8<DT>(p.a.out, to + d, x);
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     }
   };
   if (!whole && half == 0) *(v2f*)(p.part_ml + (part + 32 * wave + c) * 2) = v2f{shl, l};
-  const float inv = !whole ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   // 2^(9 + ev) in the unit of l; the whole powers behind the rest, which may not hold them
   const float gap = shl - sh, more = fmaxf(floorf(gap), -1000.f);
   const float f = inv * __builtin_amdgcn_exp2f(gap - more);

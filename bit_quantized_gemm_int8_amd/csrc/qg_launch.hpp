@@ -135,7 +135,8 @@ hipError_t launch_kv4_dequant(const Kv4Seqs& s, int D, void* k, void* v, int out
 hipError_t launch_kv4_attend(const Kv4Seqs& s, const Kv4Attend& a, int dtype, hipStream_t st);
 // The part of launch_kv4_attend for sequences of at least min_rows rows (tokens
 // times query heads of a kv head), in `tiles` tiles a kv head; with splits > 1
-// outputs [tile][head][split][row][D] and (exponent, sum) for a join.
+// outputs [tile][head][split][row][D], each over its split's sum, and (exponent, sum)
+// for a join.
 hipError_t launch_kv4_many(const Kv4Seqs& s, const Kv4Attend& a, int dtype, int64_t min_rows, int64_t tiles,
                            int splits, float* part_o, float* part_ml, hipStream_t st);
 // Bytes of device workspace launch_kv4_attend needs (uniform: no offsets), -1

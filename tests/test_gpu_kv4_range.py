@@ -182,3 +182,21 @@ def test_halves_of_wide_heads_far_apart():
         q = rng.standard_normal((5, 2, D)).astype(np.float32)
         q[:, :, 0] = 10.0
         close(*attend(q, pages, table, L, "bf16", page), "bf16")
+
+
+# ---- values up to the end of the range -----------------------------------------------
+
+@pytest.mark.parametrize("D,n,L", [(64, 1, 1), (128, 1, 1), (256, 1, 1), (128, 2, 700), (64, 2, 700), (256, 2, 700), (256, 9, 200),
+                                   (64, 150, 160), (128, 150, 160), (128, 150, 2000), (64, 150, 2000)])
+@pytest.mark.parametrize("top", [1e33, 5e33, 1e36, 1.6e38])
+def test_largest_values(D, n, L, top):
+    page = 32
+    rng = np.random.default_rng(D + n + L)
+    k = rng.standard_normal((L, 1, D)).astype(np.float32)
+    v = (rng.uniform(-1, 1, (L, 1, D)) * top).astype(np.float32)
+    v[:, :, ::5] = np.abs(v[:, :, ::5])               # channels whose sum over the positions is far larger
+    v[::3] /= 64
+    pages, table = cache(k, v, page)
+    for sharp in (1.0, 40.0):
+        got, want, bound = attend((rng.standard_normal((n, 2, D)) * sharp).astype(np.float32), pages, table, L, "bf16", page)
+        close(got, want, bound, "bf16")
