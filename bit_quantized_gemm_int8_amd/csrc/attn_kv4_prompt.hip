@@ -53,8 +53,6 @@ constexpr float kApartLow = 0x1p-40f, kApartHigh = 0x1p60f;
 constexpr u32 kHidden = 0xFFFFFFFFu;   // group word of a position that no row sees
 
 __device__ __forceinline__ int float_exp(u32 bits) { return (int)((bits >> 23) & 255u) - 127; }
-// 2^e for -252 <= e <= 254, in two factors where one would not be normal
-__device__ __forceinline__ float scale_by(float x, int e) { return ldexpf(x, e); }
 
 // A group's scale as the unpacked values have it, times 2^24: s 2^(15 - e), or with
 // its own exponent in the place of e where that leaves [2^6, 2^16).  A group of zeros
@@ -206,7 +204,8 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     fetch_ids(tile_at(1));
   }
   v8h q[kSt];
-  float cc;
+  const float to_log2 = p.a.scale * 1.44269504088896f;
+  int unit;   // scores in base 2 are to_log2 2^unit times those of the scaled queries and keys
   {
     float x[kSt][8], top = 0.f;
 #pragma unroll
@@ -225,7 +224,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     for (int j = 0; j < kSt; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[j][i] = (_Float16)ldexpf(x[j][order[i]], e);
-    cc = ldexpf(p.a.scale * 1.44269504088896f, 9 - e);
+    unit = 9 - e;
   }
   v16f o[kDt];
 #pragma unroll
@@ -427,12 +426,12 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     float by = ct;
     if (odd) {
       // any position may be out of sight, of no page, or of another power of two:
-      // a lane finds its position's factors, for all lanes to read
+      // a lane finds its position's exponents, for all lanes to read
       {
         const u32 wk = kraw[u & 3][lane], wv = vraw[u & 3][lane];
         const float ke = (float)float_exp(wk), ve = (float)float_exp(wv);   // 128: not finite
         const float nan = __builtin_nanf("");
-        own[0][lane] = wk == kHidden ? -1.f : ke == 128.f ? nan : kv4_fit(wk, kf).odd ? __builtin_amdgcn_exp2f(ke - (float)ek) : 1.f;
+        own[0][lane] = wk == kHidden ? kUnset : ke == 128.f ? nan : kv4_fit(wk, kf).odd ? ke : (float)ek;
         own[1][lane] = ve == 128.f ? nan : kv4_fit(wv, vf_).odd ? ve - (float)ev : 0.f;
       }
 #pragma unroll
@@ -443,10 +442,11 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int at = t0 + 32 * i + 8 * a + b, e = 4 * a + b;
-            const bool seen = !(f[b] < 0.f) & (((u32)(pos - at) < reach) | ((at < sinks) & (at <= pos)));
-            s[i][e] = seen ? s[i][e] * ct * f[b] : -__builtin_inff();
+            const bool seen = !(f[b] == kUnset) & (((u32)(pos - at) < reach) | ((at < sinks) & (at <= pos)));
+            // (a NaN's integer is 0)
+            s[i][e] = seen ? ldexpf(__builtin_fmaf(s[i][e], to_log2, f[b] * 0.f), unit + (int)f[b]) : -__builtin_inff();
           }
-          __builtin_amdgcn_sched_barrier(0);   // few factors at a time: registers
+          __builtin_amdgcn_sched_barrier(0);   // few exponents at a time: registers
         }
       // the sum of the exponentials here, since the values' powers of two differ
       float top = kLow;
@@ -552,9 +552,9 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv4_attend_many(Kv4ManyA
     // room for scales 16 times as large and 64 times as small
     ek = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_k))), -100), 100) + 4;
     ev = min(max(__builtin_amdgcn_readfirstlane(float_exp(__float_as_uint(top_v))), -100), 100) + 4;
-    kf = scale_by(1.f, 15 - ek);
-    vf_ = scale_by(1.f, 15 - ev);
-    ct = scale_by(cc, ek);
+    kf = ldexpf(1.f, 15 - ek);
+    vf_ = ldexpf(1.f, 15 - ev);
+    ct = ldexpf(to_log2, unit + ek);
     if (keys) unpack(std::true_type(), tile_at(0), 0, 0);
     else unpack(std::false_type(), tile_at(0), 0, 0);
     if (__any(odd)) flags[0] = 1;

@@ -200,3 +200,18 @@ def test_largest_values(D, n, L, top):
     for sharp in (1.0, 40.0):
         got, want, bound = attend((rng.standard_normal((n, 2, D)) * sharp).astype(np.float32), pages, table, L, "bf16", page)
         close(got, want, bound, "bf16")
+
+
+# ---- keys of far magnitudes ------------------------------------------------------------
+
+@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (64, 150), (128, 150)])
+@pytest.mark.parametrize("e,first", [(60, 0), (110, 0), (120, 0), (124, 0), (-60, 0), (-110, 0), (60, 70), (30, 330), (100, 70), (124, 70), (-100, 70)])
+def test_keys_far_from_one(D, n, e, first):
+    """Keys by 2^e, the first ones zeros, under queries by 2^-e."""
+    L, page = 700, 32
+    rng = np.random.default_rng(D + n)
+    k = np.ldexp(rng.standard_normal((L, 1, D)), e).astype(np.float32)
+    k[:first] = 0
+    pages, table = cache(k, rng.standard_normal((L, 1, D)).astype(np.float32), page)
+    q = np.ldexp(rng.standard_normal((n, 2, D)), -e).astype(np.float32)
+    close(*attend(q, pages, table, L, "bf16", page), "bf16")
