@@ -10,8 +10,9 @@
 // most a shift for two codes.  (At bits 0 to 3 they do not: an operand n 2^-24 counts
 // with the exponent of 2^-14 when the products are aligned, and sums of 32 came out up
 // to 1.6e-5 of their terms too small, against 1.3e-7 for n 2^-20.)  Queries are
-// scaled to binary16's upper range by a power of two of their row, exactly for
-// bfloat16 and binary16 inputs; the weights p s are rounded to binary16 (half a step:
+// scaled to binary16's upper range by a power of two of their row: exact down to 2^-28 of
+// the row's largest element, and off by up to 2^-39 of that below, where binary16 is
+// subnormal.  The weights p s are rounded to binary16 (half a step:
 // 2^-11), the codes' sum and the zero points' sum taking the same rounded weights,
 // both through the matrix cores.  Binary16 outputs, whose own rounding is no larger, get what the rounding
 // left over in a second product (2^-22).  Softmax and sums: binary32.
@@ -232,9 +233,8 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = ldexpf(x[j][order[i]], e2);
-        sum += v;
-        q[r][j][i] = (_Float16)v;
+        q[r][j][i] = (_Float16)ldexpf(x[j][order[i]], e2);
+        sum += (float)q[r][j][i];   // the zero points meet the queries that the codes meet
       }
       qs[r][j / 4] += sum;
     }

@@ -758,7 +758,9 @@ qg_status_t dequantize_kv_u4_pages(const int32_t* pages, int64_t P, int64_t page
  * counts as zero.  For the matrix cores the weights (in calls of few rows the weights
  * times their value scales, each group of channels for itself) are rounded to binary16:
  * 2^-11 of a weight, no less than 2^-24 of the row's largest; twice as many bits in
- * calls of few rows with binary16 outputs.  Scores up to 2^22 in magnitude: past that,
+ * calls of few rows with binary16 outputs.  Queries go there in binary16 too, each row by
+ * a power of two: elements below 2^-28 of the row's largest are off by up to 2^-39 of
+ * that.  Scores up to 2^22 in magnitude: past that,
  * where neighbours in binary32 are 1/2 and more apart, outputs are not specified.
  * Which of two kernels a row goes through, and with it the order of its sums and the
  * rounding of its weights, goes by the sizes of the call, never by its values.

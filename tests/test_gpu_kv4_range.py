@@ -215,3 +215,28 @@ def test_keys_far_from_one(D, n, e, first):
     pages, table = cache(k, rng.standard_normal((L, 1, D)).astype(np.float32), page)
     q = np.ldexp(rng.standard_normal((n, 2, D)), -e).astype(np.float32)
     close(*attend(q, pages, table, L, "bf16", page), "bf16")
+
+
+@pytest.mark.parametrize("n", [1, 9])
+def test_queries_of_far_elements(n):
+    """Elements of a query below 2^-39 of its largest count as one number in the codes' and in
+    the zero points' sums: positions whose keys are zeros there, with a zero point of 15,
+    score as the others do.  A score may be off by scale 2^-39 max |q| sum |k|, here 2^-5.1."""
+    D, L, page, s = 256, 300, 32, 2.0 ** 34
+    rng = np.random.default_rng(n)
+    k = np.zeros((L, 1, D), np.float32)
+    k[::2, 0, 255] = -15 * s
+    v = rng.standard_normal((L, 1, D)).astype(np.float32)
+    pages, table = cache(k, v, page)
+    q = np.zeros((n, 1, D), np.float32)
+    q[:, :, 0] = 1.0
+    q[:, :, 128:255] = 2.0 ** -41
+    got, want, bound = attend(q, pages, table, L, "bf16", page)
+    _, vv, _ = kv4.values(pages, page, table[0], np.arange(L), D)
+    off = D ** -0.5 * 2.0 ** -39 * 15 * s                 # of a score; of the weights relatively, both ways
+    fin = torch.finfo(torch.bfloat16)
+    for r in range(n):
+        seen = np.abs(vv[:L - n + r + 1]).mean(0)
+        limit = np.expm1(2 * off) * (seen + np.abs(want[r]))
+        # the terms of the scores are far below the sums that the bound's own first term counts
+        assert (np.abs(got[r] - want[r]) <= limit * (1 + fin.eps) + fin.eps / 2 * np.abs(want[r]) + 2.0 ** -9 * seen).all()
