@@ -69,170 +69,111 @@ __device__ __forceinline__ u32 kv4_codes(const float (&x)[8], float s, float r, 
 
 }  // namespace
 
-// Rows a workgroup takes where a call has many.
-constexpr int kQuad = 4;
-
-// Whether rows row .. row + 3 are the four positions of one block of value codes.
-// (offsets may be wrong: rows past the call's do not count, whatever they say)
-__device__ __forceinline__ bool kv4_quad(const Kv4Seqs& s, const Kv4Row& at, int row) {
-  return at.b >= 0 && row + kQuad <= s.T && row + kQuad <= at.end && (at.pos & (kQuad - 1)) == 0;
-}
-
-// What a thread of an append works on: a head's rows, and its chunks in them.
-struct Kv4Head {
-  const void* src;     // the operand's
-  int64_t stride;      // elements from row to row
-  int h, l;            // head of the operand, thread of the head
-  bool is_q, is_k;
-};
-
-// N rows (tokens) of one head: D / 16 neighbouring threads with two chunks of 8
-// channels each, the two that a rotation by halves pairs up.  N = 4 is for the
-// positions of one block of value codes, whose words go out side by side.
-template <int DT, int D, int N>
-__device__ __forceinline__ void kv4_append_rows(const Kv4Seqs& s, const Kv4Append& a, int row,
-                                                const Kv4Row& at, const Kv4Head& w) {
+// A workgroup takes one token and up to 256 / (D / 16) of its heads, queries first, then
+// keys, then values: D / 16 neighbouring threads a head, each with two chunks of 8
+// channels, the two that a rotation by halves pairs up.  Bound by memory: what it reads
+// and writes once.  4096 tokens of 32 heads of 128 channels and as many kv heads,
+// binary16, 151 MB: 38 us, 4.0 TB/s; one token of 16 sequences 4.5 us, a launch's
+// latency.  (Four positions of a block of value codes a workgroup, which stores them
+// side by side: 39, and 133 against 142 for 16384 tokens; but where sequences begin inside
+// a block, or have fewer tokens, 190 against 143, and 43 against 24 for 4096 single ones.)
+template <int DT, int D>
+__global__ __launch_bounds__(256) void k_kv4_append(Kv4Seqs s, Kv4Append a, int parts) {
   constexpr int kL = D / 16, kGd = kv4_groups(D);
-  const int l = w.l, rc = a.rot >> 4;   // chunks of a half of the rotated channels
-  const int c0 = l < rc ? l : 2 * rc + (l - rc), c1 = l < rc ? l + rc : c0 + (kL - rc);
+  const int part = blockIdx.x % parts, row = blockIdx.x / parts;
+  const int hh = part * (int)(blockDim.x / kL) + (int)threadIdx.x / kL, l = (int)threadIdx.x % kL;
+  if (hh >= a.Hq + 2 * s.H) return;   // whole groups of kL lanes: the exchanges stay complete
+  const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + s.H;
+  const int h = is_q ? hh : is_k ? hh - a.Hq : hh - a.Hq - s.H;
+  const Kv4Row at = kv4_row(s, row);
+  if (at.b < 0) return;   // rows of no sequence stay as they are
   const bool known = a.rot == 0 || (at.pos >= 0 && at.pos < a.table_rows);
-  const bool is_q = w.is_q, is_k = w.is_k;
-  const int h = w.h;
   int slot = 0;
   int32_t* page = nullptr;
   if (!is_q) {
     page = known ? kv4_page(s, at.b, at.pos, h, D, slot) : nullptr;
     if (page == nullptr) return;   // the kL lanes of a head alike
   }
-  float x0[N][8], x1[N][8];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    kv4_load8<DT>(w.src, (row + n) * w.stride + (int64_t)h * D + 8 * c0, x0[n]);
-    kv4_load8<DT>(w.src, (row + n) * w.stride + (int64_t)h * D + 8 * c1, x1[n]);
-  }
+  const int rc = a.rot >> 4;   // chunks of a half of the rotated channels
+  const int c0 = l < rc ? l : 2 * rc + (l - rc), c1 = l < rc ? l + rc : c0 + (kL - rc);
+  const void* const src = is_q ? a.q : is_k ? a.k : a.v;
+  const int64_t from = row * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (int64_t)h * D;
+  float x0[8], x1[8];
+  kv4_load8<DT>(src, from + 8 * c0, x0);
+  kv4_load8<DT>(src, from + 8 * c1, x1);
   if ((is_q || is_k) && l < rc) {
+    const int64_t tab = known ? at.pos * (a.rot >> 1) : 0;
+    if (a.interleaved) {   // angle i turns channels 2 i and 2 i + 1
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int64_t tab = known ? (at.pos + n) * (a.rot >> 1) : 0;
-      if (a.interleaved) {   // angle i turns channels 2 i and 2 i + 1
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kv4_turn(x0[n][2 * e], x0[n][2 * e + 1], a.cos[tab + 4 * c0 + e], a.sin[tab + 4 * c0 + e]);
-          kv4_turn(x1[n][2 * e], x1[n][2 * e + 1], a.cos[tab + 4 * c1 + e], a.sin[tab + 4 * c1 + e]);
-        }
-      } else {               // angle i turns channels i and i + rot / 2
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          kv4_turn(x0[n][e], x1[n][e], a.cos[tab + 8 * c0 + e], a.sin[tab + 8 * c0 + e]);
+      for (int e = 0; e < 4; ++e) {
+        kv4_turn(x0[2 * e], x0[2 * e + 1], a.cos[tab + 4 * c0 + e], a.sin[tab + 4 * c0 + e]);
+        kv4_turn(x1[2 * e], x1[2 * e + 1], a.cos[tab + 4 * c1 + e], a.sin[tab + 4 * c1 + e]);
       }
+    } else {               // angle i turns channels i and i + rot / 2
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kv4_turn(x0[e], x1[e], a.cos[tab + 8 * c0 + e], a.sin[tab + 8 * c0 + e]);
     }
   }
   if (is_q) {
+    if (!known) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (!known) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x0[n][e] = x1[n][e] = 0.f;
-      }
-      const int64_t o = ((int64_t)(row + n) * a.Hq + h) * D;
-      kv4_store8<DT>(a.q_out, o + 8 * c0, x0[n]);
-      kv4_store8<DT>(a.q_out, o + 8 * c1, x1[n]);
+      for (int e = 0; e < 8; ++e) x0[e] = x1[e] = 0.f;
     }
+    const int64_t o = ((int64_t)row * a.Hq + h) * D;
+    kv4_store8<DT>(a.q_out, o + 8 * c0, x0);
+    kv4_store8<DT>(a.q_out, o + 8 * c1, x1);
     return;
   }
+  // range of each group, zero included; a value that is not finite makes it infinite
   const int g0 = c0 >> 4, g1 = c1 >> 4;
-  u32 q0[N], q1[N], word[N][kGd];
+  float lo[kGd], hi[kGd];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    // range of each group, zero included; a value that is not finite makes it infinite
-    float lo[kGd], hi[kGd];
+  for (int g = 0; g < kGd; ++g) lo[g] = hi[g] = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGd; ++g) lo[g] = hi[g] = 0.f;
+  for (int t = 0; t < 2; ++t) {
+    float mn = 0.f, mx = 0.f, odd = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float mn = 0.f, mx = 0.f, odd = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = t ? x1[n][e] : x0[n][e];
-        mn = fminf(mn, v);
-        mx = fmaxf(mx, v);
-        odd = __builtin_fmaf(v, 0.f, odd);
-      }
-      if (odd != 0.f) mx = __builtin_inff();
-      const int g = t ? g1 : g0;
-#pragma unroll
-      for (int i = 0; i < kGd; ++i) {
-        lo[i] = g == i ? fminf(lo[i], mn) : lo[i];
-        hi[i] = g == i ? fmaxf(hi[i], mx) : hi[i];
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float v = t ? x1[e] : x0[e];
+      mn = fminf(mn, v);
+      mx = fmaxf(mx, v);
+      odd = __builtin_fmaf(v, 0.f, odd);
     }
-    float sc[kGd], re[kGd];
+    if (odd != 0.f) mx = __builtin_inff();
+    const int g = t ? g1 : g0;
 #pragma unroll
-    for (int g = 0; g < kGd; ++g) {
-#pragma unroll
-      for (int o = 1; o < kL; o <<= 1) {
-        lo[g] = fminf(lo[g], __shfl_xor(lo[g], o, kWave));
-        hi[g] = fmaxf(hi[g], __shfl_xor(hi[g], o, kWave));
-      }
-      word[n][g] = kv4_group(lo[g], hi[g], sc[g], re[g]);
+    for (int i = 0; i < kGd; ++i) {
+      lo[i] = g == i ? fminf(lo[i], mn) : lo[i];
+      hi[i] = g == i ? fmaxf(hi[i], mx) : hi[i];
     }
-    q0[n] = kv4_codes(x0[n], g0 ? sc[kGd - 1] : sc[0], g0 ? re[kGd - 1] : re[0], g0 ? word[n][kGd - 1] : word[n][0]);
-    q1[n] = kv4_codes(x1[n], g1 ? sc[kGd - 1] : sc[0], g1 ? re[kGd - 1] : re[0], g1 ? word[n][kGd - 1] : word[n][0]);
   }
-  const int S = 1 << s.shift;
+  float sc[kGd], re[kGd];
+  u32 word[kGd];
+#pragma unroll
+  for (int g = 0; g < kGd; ++g) {
+#pragma unroll
+    for (int o = 1; o < kL; o <<= 1) {
+      lo[g] = fminf(lo[g], __shfl_xor(lo[g], o, kWave));
+      hi[g] = fmaxf(hi[g], __shfl_xor(hi[g], o, kWave));
+    }
+    word[g] = kv4_group(lo[g], hi[g], sc[g], re[g]);
+  }
+  const u32 q0 = kv4_codes(x0, g0 ? sc[kGd - 1] : sc[0], g0 ? re[kGd - 1] : re[0], g0 ? word[kGd - 1] : word[0]);
+  const u32 q1 = kv4_codes(x1, g1 ? sc[kGd - 1] : sc[0], g1 ? re[kGd - 1] : re[0], g1 ? word[kGd - 1] : word[0]);
+  const int S = 1 << s.shift, step = is_k ? 1 : 4;
   int32_t* const codes = is_k ? page + slot * (D / 8) : page + S * (D / 8) + (slot >> 2) * (D / 2) + (slot & 3);
-  int32_t* const par = page + S * (D / 4) + (is_k ? 0 : kGd * S) + (l < kGd ? l * S : 0) + slot;
-  if constexpr (N == kQuad) {
-    if (is_k) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        codes[n * (D / 8) + c0] = (int32_t)q0[n];
-        codes[n * (D / 8) + c1] = (int32_t)q1[n];
-      }
-    } else {
-      st16(codes + 4 * c0, v4i{(int)q0[0], (int)q0[1], (int)q0[2], (int)q0[3]});
-      st16(codes + 4 * c1, v4i{(int)q1[0], (int)q1[1], (int)q1[2], (int)q1[3]});
-    }
-    if (l < kGd) {
-      v4i w;
-#pragma unroll
-      for (int n = 0; n < N; ++n) w[n] = (int)(l ? word[n][kGd - 1] : word[n][0]);
-      st16(par, w);
-    }
-  } else {
-    const int step = is_k ? 1 : 4;
-    codes[c0 * step] = (int32_t)q0[0];
-    codes[c1 * step] = (int32_t)q1[0];
-    if (l < kGd) *par = (int32_t)(l ? word[0][kGd - 1] : word[0][0]);
-  }
+  codes[c0 * step] = (int32_t)q0;
+  codes[c1 * step] = (int32_t)q1;
+  if (l < kGd) page[S * (D / 4) + (is_k ? 0 : kGd * S) + l * S + slot] = (int32_t)(l ? word[kGd - 1] : word[0]);
 }
 
-// A workgroup takes ROWS tokens and up to 256 / (D / 16) of their heads, queries
-// first, then keys, then values.  Bound by memory: what it reads and writes once.
-// 4096 tokens of 32 heads of 128 channels and as many kv heads, binary16, 151 MB:
-// 38 us, 4.0 TB/s; one token of 16 sequences 4.5 us, a launch's latency.
-template <int DT, int D, int ROWS>
-__global__ __launch_bounds__(256) void k_kv4_append(Kv4Seqs s, Kv4Append a, int parts) {
-  constexpr int kL = D / 16;
-  const int part = blockIdx.x % parts, row = blockIdx.x / parts * ROWS;
-  const int hh = part * (int)(blockDim.x / kL) + (int)threadIdx.x / kL, l = (int)threadIdx.x % kL;
-  if (hh >= a.Hq + 2 * s.H) return;   // whole groups of kL lanes: the exchanges stay complete
-  const bool is_q = hh < a.Hq, is_k = !is_q && hh < a.Hq + s.H;
-  const Kv4Head w{is_q ? a.q : is_k ? a.k : a.v, is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride,
-                  is_q ? hh : is_k ? hh - a.Hq : hh - a.Hq - s.H, l, is_q, is_k};
-  const Kv4Row at = kv4_row(s, row);
-  if constexpr (ROWS == kQuad) {
-    // the last of four positions has its angles if and only if the first has
-    const bool alike = a.rot == 0 || at.pos + kQuad <= a.table_rows || at.pos >= a.table_rows;
-    if (kv4_quad(s, at, row) && alike) return kv4_append_rows<DT, D, kQuad>(s, a, row, at, w);
-    for (int r = 0; r < kQuad; ++r) {
-      if (row + r >= s.T) return;
-      const Kv4Row one = kv4_row(s, row + r);
-      if (one.b >= 0) kv4_append_rows<DT, D, 1>(s, a, row + r, one, w);
-    }
-  } else {
-    if (at.b >= 0) kv4_append_rows<DT, D, 1>(s, a, row, at, w);   // rows of no sequence stay as they are
-  }
+// Rows that a workgroup reads back where a call has many.
+constexpr int kQuad = 4;
+
+// Whether rows row .. row + 3 are the four positions of one block of value codes.
+// (offsets may be wrong: rows past the call's do not count, whatever they say)
+__device__ __forceinline__ bool kv4_quad(const Kv4Seqs& s, const Kv4Row& at, int row) {
+  return at.b >= 0 && row + kQuad <= s.T && row + kQuad <= at.end && (at.pos & (kQuad - 1)) == 0;
 }
 
 // N rows of one chunk of 8 channels of one head.
@@ -310,24 +251,20 @@ static void kv4_split(int64_t items, int& threads, int& parts) {
   threads = (int)(((items + parts - 1) / parts + 63) / 64 * 64);
 }
 
-// Four rows a workgroup where there are enough workgroups to fill the GPU several
-// times over: their value codes and group words are then 16 bytes side by side.  One
-// row against four: 65536 rows read back 107 us and 68, 4096 rows of 96 heads appended
-// and read back 66 and 62; 500 rows read back 3.1 and 3.5.  Not where sequences are
-// known to have fewer rows than four, which would come after one another (one token of
-// 4096 sequences, 48 heads, appended: 23.4 us and 29.2).
+// Reading back: four rows a workgroup where there are enough workgroups to fill the GPU
+// several times over, since their value codes and group words are then 16 bytes side by side.
+// One row against four: 65536 rows of 8 heads 84 us and 66, alike from an odd position on; 500
+// rows 3.1 and 3.5.  Not where sequences have fewer rows than four on average, which
+// would come after one another (4096 single ones by offsets 12.0 and 14.5).
 static bool kv4_quads(const Kv4Seqs& s, int parts) {
-  return (int64_t)s.T * parts >= 4096 && (s.offsets != nullptr || s.T / s.B >= kQuad);
+  return (int64_t)s.T * parts >= 4096 && s.T / s.B >= kQuad;
 }
 
 template <int DT, int D>
 static hipError_t kv4_append_t(const Kv4Seqs& s, const Kv4Append& a, hipStream_t st) {
   int threads, parts;
   kv4_split((int64_t)(a.Hq + 2 * s.H) * (D / 16), threads, parts);
-  if (kv4_quads(s, parts))
-    k_kv4_append<DT, D, kQuad><<<(unsigned)(((int64_t)s.T + kQuad - 1) / kQuad * parts), threads, 0, st>>>(s, a, parts);
-  else
-    k_kv4_append<DT, D, 1><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, a, parts);
+  k_kv4_append<DT, D><<<(unsigned)((int64_t)s.T * parts), threads, 0, st>>>(s, a, parts);
   return hipGetLastError();
 }
 
