@@ -361,7 +361,8 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
         }
         // The row's sh to where its largest exponential is near 1, by more than rounding
         // takes from a score, and each unit to where the group's largest weight is.  Neither
-        // the sum nor the outputs ever grow by it.
+        // the sum nor the outputs ever grow by it.  Whole numbers, so that the outputs'
+        // exponent keeps its place as long as their weights do.
         float top = kLowest;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
           for (int e = 0; e < 4; ++e) top = fmaxf(top, y[r][i][e]);
         top = max16(top);
         const float was = sh[r];
-        sh[r] = fminf(was, -floorf(top) - fabsf(top) * 0x1p-21f);
+        sh[r] = fminf(was, -floorf(top) - ceilf(fabsf(top) * 0x1p-21f));
         l[r] *= __builtin_amdgcn_exp2f(sh[r] - was);   // 0 for a row's first weights
 #pragma unroll
         for (int gd = 0; gd < kGd; ++gd) {

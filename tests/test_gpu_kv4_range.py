@@ -148,6 +148,35 @@ def test_values_that_shrink_under_higher_scores(D, n, e0, e1):
         close(*attend(q, pages, table, L, "bf16", page), "bf16")
 
 
+# D, tokens, query heads, positions, dtype, window, first positions
+GROW = [
+    (64, 10, 2, 700, "bf16", 0, 0),          # tiles of 32 rows
+    (128, 12, 2, 700, "f16", 0, 0),
+    (128, 5, 4, 600, "bf16", 200, 40),
+    (64, 2, 1, 700, "f16", 0, 0),
+    (128, 3, 1, 3000, "f16", 0, 0),          # positions in splits
+    (256, 3, 1, 3000, "f16", 600, 64),
+    (128, 150, 1, 2100, "bf16", 0, 0),
+    (64, 150, 2, 2100, "f16", 0, 0),
+    (128, 70, 4, 900, "f16", 300, 50),
+]
+
+
+@pytest.mark.parametrize("case", GROW, ids=range(len(GROW)))
+@pytest.mark.parametrize("e0,e1", [(None, 0), (-40, 0), (6, -14), (-24, 10)])
+def test_values_that_grow_more(case, e0, e1):
+    D, n, Hq, L, fmt, window, sinks = case
+    page = 32
+    rng = np.random.default_rng(D + n + L)
+    for first in (64, L - 300):
+        for lift in (0.0, 20.0):
+            v = history(D, L, 1, rng, first, [0.0 if e0 is None else 2.0 ** e0], [2.0 ** e1])
+            pages, table = cache(lifted(L, D, 1, rng, first, lift), v, page)
+            q = rng.standard_normal((n, Hq, D)).astype(np.float32)
+            q[:, :, 0] = 10.0
+            close(*attend(q, pages, table, L, fmt, page, window, sinks), fmt)
+
+
 def test_values_that_grow_eight_waves():
     D, L, page, H = 64, 1100, 64, 256
     rng = np.random.default_rng(1)
