@@ -14,8 +14,8 @@
 // the row's largest element, and off by up to 2^-39 of that below, where binary16 is
 // subnormal.  The weights p s are rounded to binary16 (half a step:
 // 2^-11), the codes' sum and the zero points' sum taking the same rounded weights,
-// both through the matrix cores.  Binary16 outputs, whose own rounding is no larger, get what the rounding
-// left over in a second product (2^-22).  Softmax and sums: binary32.
+// both through the matrix cores.  Binary16 outputs, whose own rounding is no larger, get
+// what the rounding left over in a second product (2^-22).  Softmax and sums: binary32.
 //
 // Layout.  A wave takes 32 positions a step.  Both products have the query rows
 // as columns, so that a lane has one query row throughout: a lane's scores, 4
@@ -29,11 +29,11 @@
 //
 // What bounds it.  Many sequences: memory (64 requests of up to 16384 positions, 8 kv
 // heads of 128, 680 MB: 131 us, 5.2 TB/s).  One: latency, offsets, page table, codes and
-// the join in turn (4096 positions of 32 heads 12.8 us, a call of one page's positions
-// 9).  Heads of 256 with many rows: the vector unit, since the codes are unpacked again
-// for each 16 rows (141 us for 60 GFLOP; tiles of 32 rows need all registers of a wave
-// and more, and one wave a SIMD: 220; waves that share 32 rows, with weights and
-// queries in LDS, keep in step and take 151).
+// the join in turn (4096 positions of 32 heads 12.7 us, a call of one page's positions
+// 6).  Heads of 256 with many rows: the vector unit, since the codes are unpacked again
+// for each 16 rows (137 us for 60 GFLOP.  With a kernel that took 141, tiles of 32 rows
+// took 220, all registers of a wave and more, and one wave a SIMD; waves that share 32
+// rows, with weights and queries in LDS, keep in step and took 151).
 #include "qg_kv4_attn.hpp"
 
 #include <algorithm>
@@ -93,7 +93,7 @@ __device__ __forceinline__ void kv4_positions(const Kv4FewArgs& p, const Kv4Tile
 }
 
 // ONCE: a sequence's rows are one tile, so that its cache is read once: past the
-// caches (64 requests of up to 16384 positions, 8 kv heads: 131 us against 144; where
+// caches (64 requests of up to 16384 positions, 8 kv heads: 131 us against 146; where
 // many tiles read the same pages it costs 8%).
 template <int DT, int D, int RT, bool ONCE, int NW = kAttnWaves>
 __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3 : 2) void k_kv4_attend_few(Kv4FewArgs p) {
@@ -621,17 +621,23 @@ namespace {
 
 // Sequences of up to kFewRows rows are this file's, longer ones the prompt
 // kernel's.  Without offsets the call's sequences are alike; with them the GPU
-// tells, so that both kernels are launched where either may have some.  Rows times
-// kv heads of 128 at which they meet (us, this kernel and the other): 8 requests of 8
-// kv heads and 4096 positions 64 rows 38 and 41, 128 rows 54 and 48; one of 8192
-// positions 256 rows 35 and 39, 512 rows 51 and 47.
+// tells, so that both kernels are launched where either may have some.  With 64 rows
+// this kernel is never the slower one (heads of 128, us, this kernel and the other: one
+// request of 8192 positions and 8 kv heads 16 and 26, 32 of 4096 positions 107 and 107),
+// with 192 it is from 32 requests times kv heads on (4 of 4096 and 8 kv heads 47 and 39, 32
+// kv heads 149 and 79).  With 128 it goes by the call: one of 2048 positions 14 and 25, 4
+// of 4096 with 8 kv heads 36 and 34, with 32 104 and 68.
 constexpr int64_t kFewRows = 128;
 
 // With offsets, sequences of few rows among longer ones have whole tiles of the
 // prompt kernel where the tiles find room side by side and no row sees more than
-// this: the second kernel and its join cost more (a chunk of 1500 tokens and two
-// tokens of two other requests, 16 heads, a window of 2048 positions: 66 us,
-// with both kernels 79).
+// this: the second kernel and its join cost more.  A chunk of 1500 tokens and two
+// tokens of two other requests, 16 heads, a window of 2048 positions: 53 us, with both
+// kernels 70.  A prompt beside 1 to 19 single tokens that see 512 to 4096 positions, 32
+// heads on 8: up to 29% less (650 tokens at the end of 4096 positions and 19 single ones
+// 130 and 184), but where the prompt is short and the single ones many and long, which
+// the host cannot tell (300 tokens by themselves and 8 single ones of 4096 positions 63 and
+// 54, the worst of those measured 104 and 84).
 constexpr int64_t kOneSight = 4096;
 
 struct AttendPlan {
@@ -653,16 +659,16 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
   const bool few = wide || !(uniform ? long_ones : a.one), many = !wide && (uniform ? long_ones : rows > kFewRows);
   if (few) {
     // 32 rows a tile where that makes one tile of two, on average: 64 requests of 4 tokens
-    // of 8 query heads a kv head and 8192 positions 187 us, with 16 rows 201; 8 tokens each
-    // of 8 requests 41 and 40, 5 tokens of one of 16384 positions 14.2 and 13.2.
+    // of 8 query heads a kv head and 8192 positions 180 us, with 16 rows 192; 8 tokens each
+    // of 8 requests 37 and 36, 5 tokens of one of 16384 positions 13.7 and 12.5.
     a.few_rows = D < 256 && rows > 16 * B && rows <= 32 * B ? 32 : 16;
     if (uniform) a.few_tiles = B * up(rows / B, a.few_rows);
     else a.few_tiles = std::min(std::min(rows, rows / a.few_rows + B), wide ? rows : B * up(kFewRows, a.few_rows));
     // Splits of the cached positions.  A workgroup on each CU, of 256 positions or more
-    // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 35; 8 requests of
+    // (one request's 4096 positions of 32 heads in 8 parts: 13 us, whole 28; 8 requests of
     // 2047 and 2 heads in parts of 256 12 us, of 512 14); four on each where that leaves
     // 2048 positions or more, for sequences of uneven lengths (64 of up to 16384: 131 us,
-    // without 152).  Joining costs some 4 us of it.
+    // without 154).  Joining costs some 4 us of it.
     const int64_t all = a.few_tiles * H;
     a.few_splits = (int)std::max<int64_t>({1, std::min(up(256, all), capacity / 256), std::min(up(2048, all), capacity / 2048)});
     a.few_part = a.few_splits > 1 ? all * a.few_splits * a.few_rows * (D + 2) : 0;
@@ -671,7 +677,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, i
     a.many_tiles = uniform ? B * up(rows / B, kKv4ManyRows) : rows / kKv4ManyRows + (a.one ? B : std::min(B, rows / (kFewRows + 1)));
     const int64_t all = a.many_tiles * H;
     // a workgroup on each CU, of 512 positions or more (a chunk of 1500 tokens of 16 heads,
-    // a window of 2048 positions: 59 us in two parts, 81 whole)
+    // a window of 2048 positions: 60 us in two parts, 83 whole)
     a.many_splits = (int)std::max<int64_t>(1, std::min(256 / all, capacity / 512));
     a.many_part = a.many_splits > 1 ? all * a.many_splits * kKv4ManyRows * (D + 2) : 0;
   }
@@ -717,8 +723,8 @@ static hipError_t few_t(Kv4FewArgs p, int64_t tiles, int64_t sight, hipStream_t 
   const bool once = p.by.n > 0 && (int64_t)p.by.n * p.G <= 16 * RT;
   if constexpr (RT == 1 && D < 256) {
     // With a workgroup or less on each CU and a long way to go, two waves on each SIMD
-    // (32 requests of 8 kv heads, a window of 1024 positions 13.1 us, with four waves 15.2;
-    // 16 of 4096 positions 21.0 and 24.0).  Short ways and joins lose by it (5 drafted
+    // (32 requests of 8 kv heads, a window of 1024 positions 13.4 us, with four waves 16.2;
+    // 16 of 4096 positions 20.4 and 23.8).  Short ways and joins lose by it (5 drafted
     // tokens of 8 requests of 2047 positions 12.9 and 11.6), and with more workgroups two
     // waves are there already (64 requests of up to 16384 positions 153 and 131).
     if (grid <= 256 && sight / p.splits >= 1024) {

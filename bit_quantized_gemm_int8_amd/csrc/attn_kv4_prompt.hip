@@ -22,11 +22,11 @@
 // the products part of the unpacking of a later tile) the other unpacks the rest and
 // makes weights.
 //
-// 4096 tokens of 32 heads of 128 channels, 137 GFLOP: 153 us, 0.90 PFLOP/s (a large
-// matrix product reaches 1.24).  A turn takes some 2400 cycles; its 32 products take
+// 4096 tokens of 32 heads of 128 channels, 137 GFLOP: 148 to 157 us on different GPUs,
+// 0.9 PFLOP/s (a large matrix product reaches 1.24).  A turn takes some 2400 cycles; its 32 products take
 // 1150, issued 45 to 50 cycles apart beside the other wave's vector instructions.  None
-// of the parts bounds it alone: without the exponentials it takes 138 us, with half the
-// products 135.
+// of the parts bounds it alone: of 153 us, without the exponentials 138 are left, with half
+// the products 135.
 #include "qg_decode.hpp"
 #include "qg_kv4_attn.hpp"
 

@@ -53,8 +53,8 @@ constexpr int kKv4Sorted = 32;
 // Workgroups differ in length and the longest should not start last: the last rows of a
 // sequence, which see most, come first (600 tokens of two prompts of 1500, 8 heads of
 // 256: 45 us, in the rows' order 48), and up to kKv4Sorted sequences with offsets in the
-// order of their lengths (9 of 1148 to 4001 positions, 8 heads of 256: 141 us, in the
-// order of the call 149).  More would cost a decode step's start more than it gives.
+// order of their lengths (9 of 1148 to 4001 positions, 8 heads of 256: 139 us, in the
+// order of the call 147).  More would cost a decode step's start more than it gives.
 template <int ROWS>
 __device__ __forceinline__ Kv4Tile kv4_tile(const Kv4Seqs& s, const Kv4Divs& by, int64_t min_rows,
                                             int64_t max_rows, int idx) {
