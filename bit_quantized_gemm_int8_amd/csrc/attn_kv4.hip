@@ -401,7 +401,7 @@ __global__ __launch_bounds__(64 * NW, D * RT == 64 ? 4 : D == 128 && RT == 1 ? 3
             for (int e = 0; e < 4; ++e) {
               // no infinity, which an exponential of zero would make a NaN
               const float v = vs[gd][i][e] * unit[r][gd];
-              sv[gd][i][e] = y[r][i][e] == -__builtin_inff() ? 0.f : v > 0x1p100f ? 0x1p100f : v;
+              sv[gd][i][e] = y[r][i][e] == -__builtin_inff() ? 0.f : v > 0x1p127f ? 0x1p127f : v;
             }
         }
       }

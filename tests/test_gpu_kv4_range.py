@@ -148,6 +148,19 @@ def test_values_that_shrink_under_higher_scores(D, n, e0, e1):
         close(*attend(q, pages, table, L, "bf16", page), "bf16")
 
 
+@pytest.mark.parametrize("D,n", [(64, 2), (128, 2), (256, 2), (64, 12), (64, 150), (128, 150)])
+@pytest.mark.parametrize("e0,e1", [(-60, 60), (-100, 24), (-20, 90)])
+def test_values_that_grow_under_lower_scores(D, n, e0, e1):
+    """The first positions have the weight, by some 112 bits, and the later ones the values, by 110 to 124."""
+    L, page = 700, 32
+    rng = np.random.default_rng(D + n)
+    for first in (40, 330):
+        pages, table = cache(lifted(L, D, 1, rng, first, -62.0 * (D / 64) ** 0.5), history(D, L, 1, rng, first, [2.0 ** e0], [2.0 ** e1]), page)
+        q = rng.standard_normal((n, 2, D)).astype(np.float32)
+        q[:, :, 0] = 10.0
+        close(*attend(q, pages, table, L, "bf16", page), "bf16")
+
+
 # D, tokens, query heads, positions, dtype, window, first positions
 GROW = [
     (64, 10, 2, 700, "bf16", 0, 0),          # tiles of 32 rows
